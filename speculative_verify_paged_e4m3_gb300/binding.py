@@ -1,4 +1,5 @@
-"""Thin ctypes binding over libdflash_verify_attn.so (the C ABI in include/dflash_verify_attn.h).
+"""Thin ctypes binding over libdflash_verify_attn.so (the C ABI in include/dflash_verify_attn.h and
+include/dflash_paged_step.h).
 
 Argument marshalling only: every step of the computation runs in the library's CUDA kernels.
 Functions carry the C names; tensors are torch CUDA tensors whose data pointers are passed
@@ -7,6 +8,7 @@ been built, every entry point raises (there is no fallback).
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 import threading
@@ -31,6 +33,23 @@ DFLASH_KERNEL_AUTO = 0
 DFLASH_KERNEL_SIMT = 1
 DFLASH_KERNEL_TCGEN05 = 2
 
+DFLASH_PAGED_STEP_VERSION = 1
+DFLASH_FLAG_PAGES_EXHAUSTED = 0x10
+DFLASH_FLAG_TOKENS_DROPPED = 0x20
+DFLASH_FLAG_SLOT_RANGE = 0x40
+DFLASH_ROPE_HALF = 0
+DFLASH_ROPE_INTERLEAVED = 1
+DFLASH_ROPE_SCALE_NONE = 0
+DFLASH_ROPE_SCALE_LINEAR = 1
+DFLASH_ROPE_SCALE_NTK = 2
+DFLASH_ROPE_SCALE_YARN = 3
+DFLASH_ROPE_SCALE_WAVELENGTH = 4
+DFLASH_FP16 = 0
+DFLASH_BF16 = 1
+DFLASH_PREFIX_KERNEL_AUTO = 0
+DFLASH_PREFIX_KERNEL_ROWS = 1
+DFLASH_PREFIX_KERNEL_PAIRS = 2
+
 EXPORTED = (
     "dflash_verify_attn_plan",
     "dflash_verify_attn_split_bounds",
@@ -42,6 +61,12 @@ EXPORTED = (
     "dflash_verify_attn_read_flags",
     "dflash_verify_attn_forward_static_scratch",
     "dflash_verify_attn_kv_write",
+    "dflash_paged_tables",
+    "dflash_rope_plan",
+    "dflash_rope_apply",
+    "dflash_rope_kv_write",
+    "dflash_prefix_attn_plan",
+    "dflash_prefix_attn_forward",
     "dflash_verify_attn_status_string",
 )
 
@@ -61,6 +86,44 @@ class Plan(ctypes.Structure):
         ("ws_state_offset", ctypes.c_size_t),
         ("ws_acc_offset", ctypes.c_size_t),
         ("problem", Problem),
+    ]
+
+
+class PagedTablesProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "version", "batch", "page_size", "max_pages_per_seq", "num_pages", "max_context",
+        "max_tokens", "num_free", "prefix_capacity")]
+
+
+class RopeProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "version", "num_q_heads", "num_kv_heads", "head_dim", "rotary_dim", "layout", "dtype",
+        "scaling", "trained_context", "page_size", "num_pages", "reserved")] + [
+        (n, ctypes.c_double) for n in ("base", "factor", "beta_fast", "beta_slow", "low_turns",
+                                       "high_turns")]
+
+
+class RopePlan(ctypes.Structure):
+    _fields_ = [("version", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("problem", RopeProblem)]
+
+
+class PrefixAttnProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "version", "batch", "q_len", "num_q_heads", "num_kv_heads", "head_dim", "page_size",
+        "max_pages_per_seq", "num_pages", "max_context", "max_prefix", "device", "kernel",
+        "flags")]
+
+
+class PrefixAttnPlan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "version", "prefix_kernel", "prefix_rows", "prefix_row_blocks", "prefix_splits",
+        "prefix_slots", "prefix_slot_rows", "sm_count")] + [
+        ("suffix", Plan),
+        ("ws_prefix_state_offset", ctypes.c_size_t),
+        ("ws_prefix_acc_offset", ctypes.c_size_t),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("problem", PrefixAttnProblem),
     ]
 
 
@@ -100,6 +163,18 @@ def load_library() -> ctypes.CDLL:
             lib.dflash_verify_attn_forward.argtypes = [pp] + [vp] * 8 + [sz, vp, vp, vp]
             lib.dflash_verify_attn_forward_static_scratch.argtypes = [pp] + [vp] * 10
             lib.dflash_verify_attn_kv_write.argtypes = [pp] + [vp] * 9 + [sz, vp]
+            lib.dflash_paged_tables.argtypes = [ctypes.POINTER(PagedTablesProblem)] + [vp] * 16
+            lib.dflash_rope_plan.argtypes = [ctypes.POINTER(RopeProblem),
+                                             ctypes.POINTER(RopePlan),
+                                             ctypes.POINTER(ctypes.c_uint64)]
+            rp = ctypes.POINTER(RopePlan)
+            lib.dflash_rope_apply.argtypes = [rp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64,
+                                              vp]
+            lib.dflash_rope_kv_write.argtypes = [rp, i64, vp, i64, vp, i64, vp, i64] + [vp] * 6 + [
+                i64] + [vp] * 4
+            xp = ctypes.POINTER(PrefixAttnPlan)
+            lib.dflash_prefix_attn_plan.argtypes = [ctypes.POINTER(PrefixAttnProblem), xp]
+            lib.dflash_prefix_attn_forward.argtypes = [xp] + [vp] * 10 + [sz, vp, vp, vp]
             lib.dflash_verify_attn_debug_dequant.argtypes = [vp, i64, vp, vp, vp, vp]
             lib.dflash_verify_attn_read_flags.argtypes = [vp, ctypes.POINTER(ctypes.c_int32),
                                                           ctypes.c_int, vp]
@@ -260,6 +335,39 @@ def dflash_verify_attn_read_flags(workspace, clear=False, stream=None) -> int:
     return v.value
 
 
+def make_rope_problem(num_q_heads, num_kv_heads, head_dim, rotary_dim, layout=DFLASH_ROPE_HALF,
+                      dtype=DFLASH_FP16, base=10000.0, scaling=DFLASH_ROPE_SCALE_NONE, factor=1.0,
+                      trained_context=1, beta_fast=32.0, beta_slow=1.0, low_turns=1.0,
+                      high_turns=4.0, page_size=16, num_pages=1) -> RopeProblem:
+    return RopeProblem(DFLASH_PAGED_STEP_VERSION, num_q_heads, num_kv_heads, head_dim, rotary_dim,
+                       layout, dtype, scaling, trained_context, page_size, num_pages, 0, base,
+                       factor, beta_fast, beta_slow, low_turns, high_turns)
+
+
+def dflash_rope_plan(problem: RopeProblem):
+    """(plan, phases): phases is a ctypes array of rotary_dim / 2 64-bit fractions of a turn."""
+    plan = RopePlan()
+    phases = (ctypes.c_uint64 * max(1, problem.rotary_dim // 2))()
+    _check("dflash_rope_plan",
+           load_library().dflash_rope_plan(ctypes.byref(problem), ctypes.byref(plan), phases))
+    return plan, phases
+
+
+def make_prefix_problem(batch, q_len, num_q_heads, num_kv_heads, head_dim, page_size,
+                        max_pages_per_seq, num_pages, max_context, max_prefix, device=0,
+                        kernel=DFLASH_PREFIX_KERNEL_AUTO, flags=0) -> PrefixAttnProblem:
+    return PrefixAttnProblem(DFLASH_PAGED_STEP_VERSION, batch, q_len, num_q_heads, num_kv_heads,
+                             head_dim, page_size, max_pages_per_seq, num_pages, max_context,
+                             max_prefix, device, kernel, flags)
+
+
+def dflash_prefix_attn_plan(problem: PrefixAttnProblem) -> PrefixAttnPlan:
+    plan = PrefixAttnPlan()
+    _check("dflash_prefix_attn_plan",
+           load_library().dflash_prefix_attn_plan(ctypes.byref(problem), ctypes.byref(plan)))
+    return plan
+
+
 # ---------------------------------------------------------------------------------------------
 # convenience layer (still marshalling only)
 
@@ -312,3 +420,265 @@ class VerifyAttention:
         """Write the drafted tokens' K/V rows ([B, q_len, Hkv, D] FP16) into the pools."""
         dflash_verify_attn_kv_write(self.plan, k_new, v_new, block_table, context_lens, k_scale,
                                     v_scale, k_pool, v_pool, self.workspace, stream)
+
+
+# ---------------------------------------------------------------------------------------------
+# a paged decoding step (include/dflash_paged_step.h): tables, rotary positions with the cache
+# write, attention over a shared prefix. These classes check types, shapes, strides and devices
+# before they pass pointers on, and launch on their own device whichever is current.
+
+def _want(name, t, dtype, shape, device):
+    """Raise unless t is a contiguous tensor of this type and shape on this device."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous() and t.device == device):
+        got = (f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}"
+               if isinstance(t, torch.Tensor) else type(t).__name__)
+        raise ValueError(f"{name}: want contiguous {dtype} {tuple(shape)} on {device}, got {got}")
+
+
+def _want_rows(name, t, dtype, tokens, heads, head_dim, device):
+    """Raise unless t is [tokens, heads, head_dim] with heads one after the other (tokens may be
+    further apart: a slice of a fused projection); returns the token stride in elements."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device
+            and t.shape == (tokens, heads, head_dim)):
+        got = (f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor)
+               else type(t).__name__)
+        raise ValueError(f"{name}: want {dtype} {(tokens, heads, head_dim)} on {device}, got {got}")
+    st = t.stride()
+    if (heads > 1 and st[1] != head_dim) or st[2] != 1:
+        raise ValueError(f"{name}: heads must lie one after the other, got strides {st}")
+    return st[0] if tokens > 1 else heads * head_dim
+
+
+class _OnDevice:
+    """The device of an operator and its launches."""
+
+    def __init__(self, device):
+        dev = torch.device("cuda", torch.cuda.current_device() if device is None else device)
+        self.device = dev
+
+    def _launch(self, fn_name, args, stream):
+        fn = getattr(load_library(), fn_name)
+        if torch.cuda.current_device() == self.device.index:
+            rc = fn(*args, _stream(stream))
+        else:
+            with torch.cuda.device(self.device):
+                rc = fn(*args, _stream(stream))
+        if rc != DFLASH_OK:
+            raise DflashError(fn_name, rc)
+
+
+TablesOut = collections.namedtuple("TablesOut", (
+    "context_lens", "held_pages", "free_head", "token_starts", "positions", "slots"))
+
+
+class PagedTables(_OnDevice):
+    """The block-table entries, positions and cache slots of each step's new tokens, from request
+    lengths on the GPU (dflash_paged_tables)."""
+
+    def __init__(self, batch, page_size, max_pages_per_seq, num_pages, max_context, max_tokens,
+                 device=None, status=None):
+        super().__init__(device)
+        self.batch, self.page_size, self.max_tokens = batch, page_size, max_tokens
+        self.max_pages_per_seq, self.num_pages = max_pages_per_seq, num_pages
+        self.max_context = max_context
+        if status is None:
+            status = torch.zeros(4, dtype=torch.int32, device=self.device)
+        self.status = status
+
+    def empty(self) -> TablesOut:
+        """Output buffers of one step."""
+        def i32(n):
+            return torch.empty(n, dtype=torch.int32, device=self.device)
+        return TablesOut(i32(self.batch), i32(self.batch), i32(1), i32(self.batch + 1),
+                         i32(self.max_tokens),
+                         torch.empty(self.max_tokens, dtype=torch.int64, device=self.device))
+
+    def __call__(self, cached_lens, new_lens, held_pages, free_pages, free_head, block_table,
+                 prefix_table=None, prefix_pages=None, out=None, stream=None) -> TablesOut:
+        """Fill the rows' new entries of block_table in place; the rest goes to out (buffers of
+        empty(), made anew when not given)."""
+        B, dev, i32 = self.batch, self.device, torch.int32
+        if out is None:
+            out = self.empty()
+        _want("cached_lens", cached_lens, i32, (B,), dev)
+        _want("new_lens", new_lens, i32, (B,), dev)
+        _want("held_pages", held_pages, i32, (B,), dev)
+        _want("free_pages", free_pages, i32, (free_pages.numel(),), dev)
+        _want("free_head", free_head, i32, (1,), dev)
+        _want("block_table", block_table, i32, (B, self.max_pages_per_seq), dev)
+        _want("out.context_lens", out.context_lens, i32, (B,), dev)
+        _want("out.held_pages", out.held_pages, i32, (B,), dev)
+        _want("out.free_head", out.free_head, i32, (1,), dev)
+        _want("out.token_starts", out.token_starts, i32, (B + 1,), dev)
+        _want("out.positions", out.positions, i32, (self.max_tokens,), dev)
+        _want("out.slots", out.slots, torch.int64, (self.max_tokens,), dev)
+        capacity = 0
+        if prefix_table is not None:
+            capacity = min(prefix_table.numel(), self.max_pages_per_seq)
+            _want("prefix_table", prefix_table, i32, (prefix_table.numel(),), dev)
+            _want("prefix_pages", prefix_pages, i32, (1,), dev)
+        elif prefix_pages is not None:
+            raise ValueError("prefix_pages without prefix_table")
+        problem = PagedTablesProblem(DFLASH_PAGED_STEP_VERSION, B, self.page_size,
+                                     self.max_pages_per_seq, self.num_pages, self.max_context,
+                                     self.max_tokens, free_pages.numel(), capacity)
+        self._launch("dflash_paged_tables", (
+            ctypes.byref(problem), cached_lens.data_ptr(), new_lens.data_ptr(),
+            held_pages.data_ptr(), free_pages.data_ptr(), free_head.data_ptr(),
+            prefix_table.data_ptr() if capacity else None,
+            prefix_pages.data_ptr() if capacity else None, block_table.data_ptr(),
+            out.context_lens.data_ptr(), out.held_pages.data_ptr(), out.free_head.data_ptr(),
+            out.token_starts.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr(),
+            self.status.data_ptr()), stream)
+        return out
+
+    def read_flags(self, clear=False) -> int:
+        """The sticky status word (synchronises)."""
+        with torch.cuda.device(self.device):
+            return dflash_verify_attn_read_flags(self.status, clear)
+
+
+_ROPE_LAYOUTS = {"half": DFLASH_ROPE_HALF, "interleaved": DFLASH_ROPE_INTERLEAVED}
+_ROPE_SCALINGS = {"none": DFLASH_ROPE_SCALE_NONE, "linear": DFLASH_ROPE_SCALE_LINEAR,
+                  "ntk": DFLASH_ROPE_SCALE_NTK, "yarn": DFLASH_ROPE_SCALE_YARN,
+                  "wavelength": DFLASH_ROPE_SCALE_WAVELENGTH}
+_ROPE_DTYPES = {torch.float16: DFLASH_FP16, torch.bfloat16: DFLASH_BF16}
+
+
+class Rotary(_OnDevice):
+    """Rotary positions of one model's heads: apply() rotates Q and K, kv_write() rotates Q and
+    writes the rotated K and V into the paged E4M3 pools (dflash_rope_apply,
+    dflash_rope_kv_write)."""
+
+    def __init__(self, num_q_heads, num_kv_heads, head_dim, rotary_dim=None, layout="half",
+                 dtype=torch.float16, base=10000.0, scaling="none", factor=1.0,
+                 trained_context=1, beta_fast=32.0, beta_slow=1.0, low_turns=1.0, high_turns=4.0,
+                 page_size=16, num_pages=1, device=None, status=None):
+        super().__init__(device)
+        if layout not in _ROPE_LAYOUTS or scaling not in _ROPE_SCALINGS:
+            raise ValueError(f"unknown layout {layout!r} or scaling {scaling!r}")
+        if dtype not in _ROPE_DTYPES:
+            raise ValueError(f"dtype {dtype}: want float16 or bfloat16")
+        self.dtype, self.shape = dtype, (num_q_heads, num_kv_heads, head_dim)
+        self.pool_shape = (num_pages, page_size, num_kv_heads, head_dim)
+        self.plan, phases = dflash_rope_plan(make_rope_problem(
+            num_q_heads, num_kv_heads, head_dim, head_dim if rotary_dim is None else rotary_dim,
+            _ROPE_LAYOUTS[layout], _ROPE_DTYPES[dtype], base, _ROPE_SCALINGS[scaling], factor,
+            trained_context, beta_fast, beta_slow, low_turns, high_turns, page_size, num_pages))
+        # below 2^62: the same bits as int64
+        self.phases = torch.tensor(list(phases), dtype=torch.int64, device=self.device)
+        if status is None:
+            status = torch.zeros(4, dtype=torch.int32, device=self.device)
+        self.status = status
+
+    def apply(self, q, k, positions, q_out=None, k_out=None, stream=None):
+        """(q_out, k_out): q [T, Hq, D] and k [T, Hkv, D] (or None) rotated to positions [T].
+        q_out may be q itself, k_out k itself."""
+        (Hq, Hkv, D), T, dt, dev = self.shape, positions.numel(), self.dtype, self.device
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=dt, device=dev)
+        qs = _want_rows("q", q, dt, T, Hq, D, dev)
+        qo = _want_rows("q_out", q_out, dt, T, Hq, D, dev)
+        _want("positions", positions, torch.int32, (T,), dev)
+        ks = ko = 0
+        if k is not None:
+            if k_out is None:
+                k_out = torch.empty((T, Hkv, D), dtype=dt, device=dev)
+            ks = _want_rows("k", k, dt, T, Hkv, D, dev)
+            ko = _want_rows("k_out", k_out, dt, T, Hkv, D, dev)
+        elif k_out is not None:
+            raise ValueError("k_out without k")
+        self._launch("dflash_rope_apply", (
+            ctypes.byref(self.plan), T, q.data_ptr(), qs, _ptr(k), ks, positions.data_ptr(),
+            self.phases.data_ptr(), q_out.data_ptr(), qo, _ptr(k_out), ko), stream)
+        return q_out, k_out
+
+    def kv_write(self, q, k, v, positions, slots, k_scale, v_scale, k_pool, v_pool, q_out=None,
+                 stream=None):
+        """q_out: q [T, Hq, D] rotated to positions [T] (it may be q itself); the rotated k and v
+        [T, Hkv, D] go to the pools at slots [T]. A token with a negative slot is left alone."""
+        (Hq, Hkv, D), T, dt, dev = self.shape, positions.numel(), self.dtype, self.device
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=dt, device=dev)
+        qs = _want_rows("q", q, dt, T, Hq, D, dev)
+        qo = _want_rows("q_out", q_out, dt, T, Hq, D, dev)
+        ks = _want_rows("k", k, dt, T, Hkv, D, dev)
+        vs = _want_rows("v", v, dt, T, Hkv, D, dev)
+        _want("positions", positions, torch.int32, (T,), dev)
+        _want("slots", slots, torch.int64, (T,), dev)
+        _want("k_scale", k_scale, torch.float32, (1,), dev)
+        _want("v_scale", v_scale, torch.float32, (1,), dev)
+        _want("k_pool", k_pool, torch.uint8, self.pool_shape, dev)
+        _want("v_pool", v_pool, torch.uint8, self.pool_shape, dev)
+        self._launch("dflash_rope_kv_write", (
+            ctypes.byref(self.plan), T, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+            positions.data_ptr(), slots.data_ptr(), self.phases.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), q_out.data_ptr(), qo, k_pool.data_ptr(), v_pool.data_ptr(),
+            self.status.data_ptr()), stream)
+        return q_out
+
+    def read_flags(self, clear=False) -> int:
+        """The sticky status word (synchronises)."""
+        with torch.cuda.device(self.device):
+            return dflash_verify_attn_read_flags(self.status, clear)
+
+
+class SharedPrefixAttention(_OnDevice):
+    """Verification attention of a batch whose sequences share their first tokens: the shared
+    pages are read once for all of them (dflash_prefix_attn_forward). A plan plus its workspace;
+    calls that may overlap on the GPU need an instance (or a workspace) each."""
+
+    def __init__(self, batch, q_len, num_q_heads, num_kv_heads, head_dim, page_size,
+                 max_pages_per_seq, num_pages, max_context, max_prefix, device=None,
+                 kernel=DFLASH_PREFIX_KERNEL_AUTO, workspace=None):
+        super().__init__(device)
+        self.problem = make_prefix_problem(batch, q_len, num_q_heads, num_kv_heads, head_dim,
+                                           page_size, max_pages_per_seq, num_pages, max_context,
+                                           max_prefix, self.device.index, kernel)
+        self.plan = dflash_prefix_attn_plan(self.problem)
+        if workspace is None:
+            workspace = torch.zeros(self.plan.workspace_bytes, dtype=torch.uint8,
+                                    device=self.device)
+        elif workspace.numel() * workspace.element_size() < self.plan.workspace_bytes:
+            raise ValueError("workspace smaller than plan.workspace_bytes")
+        self.workspace = workspace
+        self.q_shape = (batch, q_len, num_q_heads, head_dim)
+        self.pool_shape = (num_pages, page_size, num_kv_heads, head_dim)
+
+    def __call__(self, q, k_pool, v_pool, prefix_table, prefix_len, block_table, context_lens,
+                 k_scale, v_scale, out=None, lse=None, stream=None):
+        """(out, lse) of q over the pools. prefix_table: int32, the shared pages in order (at least
+        floor(max_prefix / page_size) entries); prefix_len: int32 [1]; both None when the plan's
+        max_prefix is 0."""
+        pr, dev, i32, f32 = self.problem, self.device, torch.int32, torch.float32
+        if out is None:
+            out = torch.empty(self.q_shape, dtype=torch.float16, device=dev)
+        if lse is None:
+            lse = torch.empty(self.q_shape[:3], dtype=f32, device=dev)
+        _want("q", q, torch.float16, self.q_shape, dev)
+        _want("k_pool", k_pool, torch.uint8, self.pool_shape, dev)
+        _want("v_pool", v_pool, torch.uint8, self.pool_shape, dev)
+        _want("block_table", block_table, i32, (pr.batch, pr.max_pages_per_seq), dev)
+        _want("context_lens", context_lens, i32, (pr.batch,), dev)
+        _want("k_scale", k_scale, f32, (1,), dev)
+        _want("v_scale", v_scale, f32, (1,), dev)
+        _want("out", out, torch.float16, self.q_shape, dev)
+        _want("lse", lse, f32, self.q_shape[:3], dev)
+        if pr.max_prefix > 0:
+            _want("prefix_len", prefix_len, i32, (1,), dev)
+            _want("prefix_table", prefix_table, i32, (prefix_table.numel(),), dev)
+            if prefix_table.numel() * pr.page_size < pr.max_prefix // pr.page_size * pr.page_size:
+                raise ValueError("prefix_table has fewer pages than max_prefix fills")
+        self._launch("dflash_prefix_attn_forward", (
+            ctypes.byref(self.plan), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+            _ptr(prefix_table), _ptr(prefix_len), block_table.data_ptr(),
+            context_lens.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            self.workspace.data_ptr(), self.workspace.numel() * self.workspace.element_size(),
+            out.data_ptr(), lse.data_ptr()), stream)
+        return out, lse
+
+    def read_flags(self, clear=False) -> int:
+        """The sticky status word (synchronises)."""
+        with torch.cuda.device(self.device):
+            return dflash_verify_attn_read_flags(self.workspace, clear)

@@ -18,7 +18,7 @@
 
 namespace dflash {
 cudaError_t launch_simt_partial(const PartialParams& p, cudaStream_t stream);
-cudaError_t launch_tc_partial(const PartialParams& p, cudaStream_t stream);
+cudaError_t launch_tc_partial(const PartialParams& p, cudaStream_t stream, View view);
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream);
 cudaError_t launch_kv_write(const dflash_verify_attn_plan_t* plan, const void* k_new,
                             const void* v_new, const int32_t* block_table,
@@ -342,7 +342,7 @@ int dflash_verify_attn_run(const dflash_verify_attn_plan_t* plan, const void* q,
     if (plan->kernel == DFLASH_KERNEL_SIMT)
         e = launch_simt_partial(p, stream);
     else if (plan->kernel == DFLASH_KERNEL_TCGEN05)
-        e = launch_tc_partial(p, stream);
+        e = launch_tc_partial(p, stream, View::kWhole);
     else
         return DFLASH_ERR_INVALID_ARGUMENT;
     if (e != cudaSuccess) {
@@ -434,7 +434,7 @@ int dflash_verify_attn_forward(const dflash_verify_attn_plan_t* plan, const void
         p.pdl = 0;  // the cooperative fused launch is never a programmatic dependent
         p.out = static_cast<__half*>(out);
         p.lse = lse;
-        if (launch_tc_partial(p, static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess) {
+        if (launch_tc_partial(p, static_cast<cudaStream_t>(cuda_stream), View::kWhole) != cudaSuccess) {
             cudaGetLastError();
             return DFLASH_ERR_CUDA;
         }

@@ -40,7 +40,18 @@ struct PartialParams {
     __half* out;
     float* lse;
     int pdl;  // host side: launch as a programmatic dependent of the preceding kernel
+    // Which keys of which rows a launch covers. View::kWhole: every sequence's rows over its own
+    // context. Shared-prefix attention cuts each context at `shared_keys` (below):
+    // View::kSuffix covers the keys from there on, sequence by sequence; View::kPrefix the keys
+    // before it, once for the rows of the whole batch (one sequence of batch * q_len tokens whose
+    // block table is the prefix's; batch_q_len below is then each sequence's q_len).
+    const int32_t* prefix_len;  // device scalar; null for View::kWhole
+    int max_prefix;             // bound of *prefix_len
+    int batch_q_len;            // View::kPrefix: tokens per sequence (q_len is the batch's total)
+    int batch_max_context;      // View::kPrefix: bound of context_lens (max_context: max_prefix)
 };
+
+enum class View { kWhole, kSuffix, kPrefix };
 
 struct CombineParams {
     const float2* ws_state;
@@ -117,6 +128,19 @@ __device__ __forceinline__ int clamped_context(const int32_t* context_lens, int 
     return n;
 }
 
+// Keys that a batch takes from its shared prefix: the prefix's whole pages (a page that the prefix
+// ends in is in every sequence's own row). Sets DFLASH_FLAG_CONTEXT_CLAMPED for a length above the
+// plan's.
+__device__ __forceinline__ int shared_keys(const int32_t* prefix_len, int max_prefix,
+                                           int page_size, int* flags) {
+    int n = *prefix_len;
+    if (n > max_prefix) {
+        n = max_prefix;
+        *flags |= DFLASH_FLAG_CONTEXT_CLAMPED;
+    }
+    return n <= 0 ? 0 : n / page_size * page_size;
+}
+
 // Keys per split for context n (the rule dflash_verify_attn_split_bounds restates on the host).
 __device__ __forceinline__ int keys_per_split(int n, int num_splits, int tile_keys,
                                               int min_split_keys) {
@@ -163,9 +187,9 @@ struct UnitSlots {
 
 __device__ __forceinline__ int slot_granules(int n) { return (n + 127) >> 7; }
 
-// The clamped length of sequence b; sets the batch's context flags.
+// The clamped length of sequence b past its first `base` keys; sets the batch's context flags.
 __device__ __forceinline__ int slot_length(const int32_t* context_lens, int b, int max_context,
-                                           int q_len, int* flags) {
+                                           int q_len, int* flags, int base = 0) {
     int n = context_lens[b];
     if (n > max_context) {
         n = max_context;
@@ -173,16 +197,17 @@ __device__ __forceinline__ int slot_length(const int32_t* context_lens, int b, i
     }
     n = n < 0 ? 0 : n;
     if (n < q_len) *flags |= DFLASH_FLAG_CONTEXT_SHORT;
-    return n;
+    return max(n - base, 0);
 }
 
 // Slots of a single sequence: its units are equal, S slots each.
 __device__ __forceinline__ UnitSlots locate_slots_single(const int32_t* context_lens, int Hkv,
                                                          int S, int max_context, int q_len,
-                                                         int key, bool by_slot) {
+                                                         int key, bool by_slot,
+                                                         int base = 0) {
     UnitSlots r = {-1, 0, 0, 0, 0, 0};
     int flags = 0;
-    const int n = slot_length(context_lens, 0, max_context, q_len, &flags);
+    const int n = slot_length(context_lens, 0, max_context, q_len, &flags, base);
     const int u = by_slot ? key / S : key;
     r.flags = flags;
     if (n == 0 || u >= Hkv) return r;
@@ -200,12 +225,13 @@ __device__ __forceinline__ UnitSlots locate_slots_single(const int32_t* context_
 __device__ __forceinline__ UnitSlots locate_slots_batch_body(const int32_t* context_lens,
                                                              int B, int Hkv, int num_slots,
                                                              int max_context, int q_len,
-                                                             int key, bool by_slot) {
+                                                             int key, bool by_slot, int base) {
     const int lane = threadIdx.x & 31;
     UnitSlots r = {-1, 0, 0, 0, 0, 0};
     int unused = 0;
     auto tiles = [&](int b) {  // w_b (0 past the batch)
-        return b < B ? slot_granules(slot_length(context_lens, b, max_context, q_len, &unused)) : 0;
+        return b < B ? slot_granules(slot_length(context_lens, b, max_context, q_len, &unused, base))
+                     : 0;
     };
     // tiles in all (W), the longest sequence, non-empty sequences, the batch's context flags
     long long W = 0;
@@ -213,7 +239,8 @@ __device__ __forceinline__ UnitSlots locate_slots_batch_body(const int32_t* cont
     for (int b0 = 0; b0 < B; b0 += 32) {
         const int b = b0 + lane;
         const int w =
-            b < B ? slot_granules(slot_length(context_lens, b, max_context, q_len, &flags)) : 0;
+            b < B ? slot_granules(slot_length(context_lens, b, max_context, q_len, &flags, base))
+                  : 0;
         W += w;
         wmax = max(wmax, w);
         E += w > 0;
@@ -248,7 +275,7 @@ __device__ __forceinline__ UnitSlots locate_slots_batch_body(const int32_t* cont
     int c_carry = 0;
     for (int b0 = 0; b0 < B; b0 += 32) {
         const int b = b0 + lane;
-        const int n = b < B ? slot_length(context_lens, b, max_context, q_len, &unused) : 0;
+        const int n = b < B ? slot_length(context_lens, b, max_context, q_len, &unused, base) : 0;
         const int c = (slot_granules(n) + T - 1) / T;
         int sc = c;  // inclusive scan over the chunk
         for (int o = 1; o < 32; o <<= 1) {
@@ -281,18 +308,21 @@ __device__ __forceinline__ UnitSlots locate_slots_batch_body(const int32_t* cont
 static __device__ __noinline__ UnitSlots locate_slots_batch(const int32_t* context_lens, int B,
                                                             int Hkv, int num_slots,
                                                             int max_context, int q_len, int key,
-                                                            bool by_slot) {
+                                                            bool by_slot, int base) {
     return locate_slots_batch_body(context_lens, B, Hkv, num_slots, max_context, q_len, key,
-                                   by_slot);
+                                   by_slot, base);
 }
 
 // The slots of a unit or the unit of a slot (see above). Warp-cooperative. The several-sequence
 // search is called out of line: it runs once per CTA, and the kernels' hot code stays compact.
 __device__ __forceinline__ UnitSlots locate_slots(const int32_t* context_lens, int B, int Hkv,
                                                   int S, int num_slots, int max_context,
-                                                  int q_len, int key, bool by_slot) {
-    if (B == 1) return locate_slots_single(context_lens, Hkv, S, max_context, q_len, key, by_slot);
-    return locate_slots_batch(context_lens, B, Hkv, num_slots, max_context, q_len, key, by_slot);
+                                                  int q_len, int key, bool by_slot,
+                                                  int base = 0) {
+    if (B == 1)
+        return locate_slots_single(context_lens, Hkv, S, max_context, q_len, key, by_slot, base);
+    return locate_slots_batch(context_lens, B, Hkv, num_slots, max_context, q_len, key, by_slot,
+                              base);
 }
 
 // Grid of a partial launch: (splits x row blocks, Hkv, 1) for a single sequence, (slots x row

@@ -1,0 +1,383 @@
+// rope.cu -- rotary positions of Q and K, alone or with the E4M3 cache write
+// (dflash_paged_step.h has the definition).
+//
+// Angles. Position t turns pair i by t * theta_i. With the frequency held as a 64-bit fraction of a
+// turn, f_i = theta_i / (2 pi) * 2^64, the low 64 bits of t * f_i are the fraction of a turn left
+// after all whole ones: the range reduction is one integer product, exact at any distance (an FP32
+// product would be 2^-6 rad off at position 2^18). The top 32 bits, signed, are within 2^-32 of the
+// fraction and become an angle in half turns for sincospi.
+//
+// One CTA per token (or a few): its threads first compute the token's rotary_dim / 2 cosines and
+// sines, once for all heads, into shared memory, with the loads of the head rows already in flight;
+// then a warp takes a head row at a time, 8 elements (16 bytes) a lane. The partner of a half-layout
+// pair lies rotary_dim / 16 lanes away and comes by shuffle; an interleaved pair is in one lane.
+// Bound by HBM for many tokens (each element is read and written once), by latency for few.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include <type_traits>
+
+#include "common.cuh"
+#include "dflash_paged_step.h"
+#include "tc_ptx.cuh"
+
+namespace dflash {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kLaneElems = kHeadDim / 32;  // 8
+
+struct RopeParams {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t* positions;
+    const int64_t* slots;
+    const uint64_t* phases;
+    const float *k_scale, *v_scale;
+    void *q_out, *k_out;
+    int64_t q_out_stride, k_out_stride;
+    uint8_t *k_pool, *v_pool;
+    int32_t* status;
+    int64_t num_tokens, num_slots;
+    int num_q_heads, num_kv_heads, rotary_dim;
+    float amplitude;
+};
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& w, float (&x)[kLaneElems]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float2 f;
+        if constexpr (std::is_same_v<T, __half>)
+            f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+        else
+            f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float (&x)[kLaneElems]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (std::is_same_v<T, __half>) {
+            const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// This lane's cosines and sines of one token, in the places that `rotate` wants them.
+struct Turn {
+    float c[kLaneElems], s[kLaneElems];
+};
+
+template <bool kHalf>
+__device__ __forceinline__ Turn load_turn(const float2* cs, int lane, int rotary_dim) {
+    Turn t;
+    const int e0 = lane * kLaneElems;
+#pragma unroll
+    for (int e = 0; e < kLaneElems; ++e) {
+        t.c[e] = 1.f;
+        t.s[e] = 0.f;
+    }
+    if (e0 < rotary_dim) {
+        const int half = rotary_dim / 2;
+        const bool second = kHalf && e0 >= half;  // y of its pairs: y cos + x sin
+        const int i0 = kHalf ? (second ? e0 - half : e0) : e0 / 2;
+        constexpr int kPairs = kHalf ? kLaneElems : kLaneElems / 2;
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            const float2 v = cs[i0 + i];
+            if constexpr (kHalf) {
+                t.c[i] = v.x;
+                t.s[i] = second ? v.y : -v.y;
+            } else {
+                t.c[2 * i] = t.c[2 * i + 1] = v.x;
+                t.s[2 * i] = -v.y;
+                t.s[2 * i + 1] = v.y;
+            }
+        }
+    }
+    return t;
+}
+
+// The lane's 8 elements of a head row, rotated in FP32. Every lane of the warp calls it.
+template <typename T, bool kHalf>
+__device__ __forceinline__ void rotate(const uint4& w, const Turn& t, int lane, int rotary_dim,
+                                       float (&y)[kLaneElems]) {
+    float x[kLaneElems], o[kLaneElems];
+    unpack<T>(w, x);
+    if constexpr (kHalf) {
+        const int off = rotary_dim / (2 * kLaneElems);  // lanes of half the rotated part
+        const int src = lane < off ? lane + off : (lane < 2 * off ? lane - off : lane);
+        uint4 p;
+        p.x = __shfl_sync(0xffffffffu, w.x, src);
+        p.y = __shfl_sync(0xffffffffu, w.y, src);
+        p.z = __shfl_sync(0xffffffffu, w.z, src);
+        p.w = __shfl_sync(0xffffffffu, w.w, src);
+        unpack<T>(p, o);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kLaneElems; ++e) o[e] = x[e ^ 1];
+    }
+    // elements past the rotated part pass through untouched (an infinity times a zero sine
+    // would be NaN)
+    const bool turned = lane * kLaneElems < rotary_dim;
+#pragma unroll
+    for (int e = 0; e < kLaneElems; ++e)
+        y[e] = turned ? fmaf(x[e], t.c[e], o[e] * t.s[e]) : x[e];
+}
+
+// kWrite: K and V rows go to the pools as E4M3; else K (if any) to k_out.
+template <typename T, bool kHalf, bool kWrite>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+    __shared__ float2 cs[kHeadDim / 2];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rows = p.num_q_heads + p.num_kv_heads * (kWrite ? 2 : (p.k ? 1 : 0));
+    for (int64_t t = blockIdx.x; t < p.num_tokens; t += gridDim.x) {
+        const int64_t slot = kWrite ? p.slots[t] : 0;
+        if (slot < 0) continue;  // padding (the whole CTA agrees)
+        if (tid < p.rotary_dim / 2) {
+            const uint64_t turn = (uint64_t)(int64_t)p.positions[t] * p.phases[tid];
+            float s, c;
+            // signed 2^-32 turns -> half turns
+            sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);
+            cs[tid] = make_float2(c * p.amplitude, s * p.amplitude);
+        }
+        __syncthreads();
+        const Turn turn = load_turn<kHalf>(cs, lane, p.rotary_dim);
+        if (kWrite && slot >= p.num_slots && tid == 0) atomicOr(p.status, DFLASH_FLAG_SLOT_RANGE);
+        for (int r = warp; r < rows; r += kWarps) {
+            const bool is_q = r < p.num_q_heads;
+            const bool is_v = r >= p.num_q_heads + p.num_kv_heads;
+            const int h = is_q ? r : (r - p.num_q_heads) - (is_v ? p.num_kv_heads : 0);
+            const T* src = is_q ? static_cast<const T*>(p.q) + t * p.q_stride
+                                : (is_v ? static_cast<const T*>(p.v) + t * p.v_stride
+                                        : static_cast<const T*>(p.k) + t * p.k_stride);
+            const uint4 w = reinterpret_cast<const uint4*>(src + h * kHeadDim)[lane];
+            float y[kLaneElems];
+            if (is_v)
+                unpack<T>(w, y);
+            else
+                rotate<T, kHalf>(w, turn, lane, p.rotary_dim, y);
+            if (is_q || !kWrite) {
+                T* dst = is_q ? static_cast<T*>(p.q_out) + t * p.q_out_stride
+                              : static_cast<T*>(p.k_out) + t * p.k_out_stride;
+                reinterpret_cast<uint4*>(dst + h * kHeadDim)[lane] = pack<T>(y);
+            } else if (slot < p.num_slots) {
+                const float scale = is_v ? *p.v_scale : *p.k_scale;
+                uint32_t code[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    code[i] = ptx::f32x2_to_e4m3x2(__fdiv_rn(y[4 * i], scale),
+                                                   __fdiv_rn(y[4 * i + 1], scale)) |
+                              (uint32_t)ptx::f32x2_to_e4m3x2(__fdiv_rn(y[4 * i + 2], scale),
+                                                             __fdiv_rn(y[4 * i + 3], scale))
+                                  << 16;
+                uint8_t* pool = is_v ? p.v_pool : p.k_pool;
+                reinterpret_cast<uint2*>(pool + (slot * p.num_kv_heads + h) * kHeadDim)[lane] =
+                    make_uint2(code[0], code[1]);
+            }
+        }
+        __syncthreads();  // the table of turns is the next token's
+    }
+}
+
+template <bool kWrite>
+cudaError_t launch(const dflash_rope_plan_t* plan, const RopeParams& p, cudaStream_t stream) {
+    const dflash_rope_problem& pr = plan->problem;
+    const bool half = pr.layout == DFLASH_ROPE_HALF;
+    void (*kernel)(RopeParams);
+    if (pr.dtype == DFLASH_FP16)
+        kernel = half ? rope_kernel<__half, true, kWrite> : rope_kernel<__half, false, kWrite>;
+    else
+        kernel = half ? rope_kernel<__nv_bfloat16, true, kWrite>
+                      : rope_kernel<__nv_bfloat16, false, kWrite>;
+    const int64_t grid = p.num_tokens < 65536 ? p.num_tokens : 65536;
+    kernel<<<(unsigned)grid, kThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// A strided [tokens, heads, 256] operand: 16-byte rows, token stride of whole 8-element groups.
+bool rows_ok(const void* x, int64_t stride, int heads) {
+    return x && aligned(x, 16) && stride % 8 == 0 && stride >= (int64_t)heads * kHeadDim &&
+           stride <= (int64_t)1 << 40;
+}
+
+bool finite(double x) { return x - x == 0.0; }
+
+int check_problem(const dflash_rope_problem* pr) {
+    if (!pr || pr->version != DFLASH_PAGED_STEP_VERSION) return DFLASH_ERR_INVALID_ARGUMENT;
+    if (pr->num_q_heads < 1 || pr->num_q_heads > 256 || pr->num_kv_heads < 1 ||
+        pr->num_kv_heads > 256 || pr->page_size < 1 || pr->num_pages < 1 || pr->reserved != 0 ||
+        pr->layout < DFLASH_ROPE_HALF || pr->layout > DFLASH_ROPE_INTERLEAVED ||
+        pr->dtype < DFLASH_FP16 || pr->dtype > DFLASH_BF16 ||
+        pr->scaling < DFLASH_ROPE_SCALE_NONE || pr->scaling > DFLASH_ROPE_SCALE_WAVELENGTH)
+        return DFLASH_ERR_INVALID_ARGUMENT;
+    if (pr->head_dim < 1 || pr->rotary_dim < 1 || pr->rotary_dim > pr->head_dim)
+        return DFLASH_ERR_INVALID_ARGUMENT;
+    if (!finite(pr->base) || pr->base <= 1.0) return DFLASH_ERR_INVALID_ARGUMENT;
+    if (pr->scaling != DFLASH_ROPE_SCALE_NONE && (!finite(pr->factor) || pr->factor < 1.0))
+        return DFLASH_ERR_INVALID_ARGUMENT;
+    if (pr->scaling >= DFLASH_ROPE_SCALE_YARN && pr->trained_context < 1)
+        return DFLASH_ERR_INVALID_ARGUMENT;
+    if (pr->scaling == DFLASH_ROPE_SCALE_YARN &&
+        (!finite(pr->beta_fast) || !finite(pr->beta_slow) || pr->beta_fast <= 0.0 ||
+         pr->beta_slow <= 0.0))
+        return DFLASH_ERR_INVALID_ARGUMENT;
+    if (pr->scaling == DFLASH_ROPE_SCALE_WAVELENGTH &&
+        (!finite(pr->low_turns) || !finite(pr->high_turns) || pr->low_turns >= pr->high_turns))
+        return DFLASH_ERR_INVALID_ARGUMENT;
+    if (pr->head_dim != kHeadDim || pr->rotary_dim % 16 != 0) return DFLASH_ERR_UNSUPPORTED;
+    return DFLASH_OK;
+}
+
+int check_plan(const dflash_rope_plan_t* plan) {
+    if (!plan || plan->version != DFLASH_PAGED_STEP_VERSION) return DFLASH_ERR_INVALID_ARGUMENT;
+    return check_problem(&plan->problem);
+}
+
+double clamp01(double x) { return x < 0.0 ? 0.0 : (x > 1.0 ? 1.0 : x); }
+
+}  // namespace
+}  // namespace dflash
+
+using namespace dflash;
+
+extern "C" {
+
+int dflash_rope_plan(const dflash_rope_problem* pr, dflash_rope_plan_t* plan, uint64_t* phases) {
+    const int rc = check_problem(pr);
+    if (rc != DFLASH_OK) return rc;
+    if (!plan || !phases) return DFLASH_ERR_INVALID_ARGUMENT;
+    const double kTwoPi = 6.283185307179586476925;
+    const int d = pr->rotary_dim;
+    const double s = pr->factor;
+    double base = pr->base;
+    if (pr->scaling == DFLASH_ROPE_SCALE_NTK) base *= pow(s, (double)d / (d - 2));
+    double lo = 0, hi = 0;
+    if (pr->scaling == DFLASH_ROPE_SCALE_YARN) {
+        const double per = d / (2.0 * log(base));
+        lo = floor(per * log(pr->trained_context / (pr->beta_fast * kTwoPi)));
+        hi = ceil(per * log(pr->trained_context / (pr->beta_slow * kTwoPi)));
+        if (lo < 0) lo = 0;
+        if (hi > d - 1) hi = d - 1;
+    }
+    for (int i = 0; i < d / 2; ++i) {
+        double theta = pow(base, -2.0 * i / d);
+        if (pr->scaling == DFLASH_ROPE_SCALE_LINEAR) {
+            theta /= s;
+        } else if (pr->scaling == DFLASH_ROPE_SCALE_YARN) {
+            const double r = clamp01((i - lo) / (hi - lo < 0.001 ? 0.001 : hi - lo));
+            theta = theta / s * r + theta * (1.0 - r);
+        } else if (pr->scaling == DFLASH_ROPE_SCALE_WAVELENGTH) {
+            const double turns = pr->trained_context * theta / kTwoPi;
+            const double g = clamp01((turns - pr->low_turns) / (pr->high_turns - pr->low_turns));
+            theta = theta / s * (1.0 - g) + theta * g;
+        }
+        phases[i] = (uint64_t)ldexp(theta / kTwoPi, 64);  // theta <= 1: below 2^62
+    }
+    plan->version = DFLASH_PAGED_STEP_VERSION;
+    plan->amplitude =
+        pr->scaling == DFLASH_ROPE_SCALE_YARN ? (float)(0.1 * log(s) + 1.0) : 1.0f;
+    plan->problem = *pr;
+    return DFLASH_OK;
+}
+
+int dflash_rope_apply(const dflash_rope_plan_t* plan, int64_t num_tokens, const void* q,
+                      int64_t q_stride, const void* k, int64_t k_stride, const int32_t* positions,
+                      const uint64_t* phases, void* q_out, int64_t q_out_stride, void* k_out,
+                      int64_t k_out_stride, void* cuda_stream) {
+    const int rc = check_plan(plan);
+    if (rc != DFLASH_OK) return rc;
+    const dflash_rope_problem& pr = plan->problem;
+    if (num_tokens < 0 || (k == nullptr) != (k_out == nullptr)) return DFLASH_ERR_INVALID_ARGUMENT;
+    if (num_tokens == 0) return DFLASH_OK;
+    if (!rows_ok(q, q_stride, pr.num_q_heads) || !rows_ok(q_out, q_out_stride, pr.num_q_heads) ||
+        (k && (!rows_ok(k, k_stride, pr.num_kv_heads) ||
+               !rows_ok(k_out, k_out_stride, pr.num_kv_heads))) ||
+        !positions || !aligned(positions, 4) || !phases || !aligned(phases, 8) ||
+        (q == q_out && q_stride != q_out_stride) || (k && k == k_out && k_stride != k_out_stride))
+        return DFLASH_ERR_INVALID_ARGUMENT;
+    RopeParams p = {};
+    p.q = q;
+    p.k = k;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.positions = positions;
+    p.phases = phases;
+    p.q_out = q_out;
+    p.k_out = k_out;
+    p.q_out_stride = q_out_stride;
+    p.k_out_stride = k_out_stride;
+    p.num_tokens = num_tokens;
+    p.num_q_heads = pr.num_q_heads;
+    p.num_kv_heads = pr.num_kv_heads;
+    p.rotary_dim = pr.rotary_dim;
+    p.amplitude = plan->amplitude;
+    return launch<false>(plan, p, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
+               ? DFLASH_OK
+               : DFLASH_ERR_CUDA;
+}
+
+int dflash_rope_kv_write(const dflash_rope_plan_t* plan, int64_t num_tokens, const void* q,
+                         int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                         int64_t v_stride, const int32_t* positions, const int64_t* slots,
+                         const uint64_t* phases, const float* k_scale, const float* v_scale,
+                         void* q_out, int64_t q_out_stride, void* k_pool, void* v_pool,
+                         int32_t* status, void* cuda_stream) {
+    const int rc = check_plan(plan);
+    if (rc != DFLASH_OK) return rc;
+    const dflash_rope_problem& pr = plan->problem;
+    if (num_tokens < 0) return DFLASH_ERR_INVALID_ARGUMENT;
+    if (num_tokens == 0) return DFLASH_OK;
+    if (!rows_ok(q, q_stride, pr.num_q_heads) || !rows_ok(k, k_stride, pr.num_kv_heads) ||
+        !rows_ok(v, v_stride, pr.num_kv_heads) || !rows_ok(q_out, q_out_stride, pr.num_q_heads) ||
+        !positions || !aligned(positions, 4) || !slots || !aligned(slots, 8) || !phases ||
+        !aligned(phases, 8) || !k_scale || !aligned(k_scale, 4) || !v_scale ||
+        !aligned(v_scale, 4) || !k_pool || !aligned(k_pool, 8) || !v_pool ||
+        !aligned(v_pool, 8) || !status || !aligned(status, 4) ||
+        (q == q_out && q_stride != q_out_stride))
+        return DFLASH_ERR_INVALID_ARGUMENT;
+    RopeParams p = {};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.positions = positions;
+    p.slots = slots;
+    p.phases = phases;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.q_out = q_out;
+    p.q_out_stride = q_out_stride;
+    p.k_pool = static_cast<uint8_t*>(k_pool);
+    p.v_pool = static_cast<uint8_t*>(v_pool);
+    p.status = status;
+    p.num_tokens = num_tokens;
+    p.num_slots = (int64_t)pr.num_pages * pr.page_size;
+    p.num_q_heads = pr.num_q_heads;
+    p.num_kv_heads = pr.num_kv_heads;
+    p.rotary_dim = pr.rotary_dim;
+    p.amplitude = plan->amplitude;
+    return launch<true>(plan, p, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
+               ? DFLASH_OK
+               : DFLASH_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -135,6 +135,7 @@ struct Small {
     float rsum[kMaxRP / kGroupRows][4][kGroupRows];  // per-group, per-warp row sums of the split
     float mref[kMaxRP / kGroupRows][kGroupRows];     // the split state's max (m - s) of each row
     float nmcur[kMaxRP / kGroupRows][4][kGroupRows];  // each warp's copy of s - reference max
+    alignas(16) int limit[kMaxRP];  // View::kPrefix: first key that each row does not see
     int rows[kRowCache];  // source row (physical page * page + slot) of chunk c of the split
 };
 static_assert(offsetof(Small, c0) % 16 == 0, "row constants are read as float4");
@@ -234,11 +235,12 @@ __device__ __noinline__ int2 table_row(const int32_t* block_table, int b, int ma
 
 // Source row in the page pool of the 16-key chunk starting at key j0 of sequence b: read from the
 // split's cache when the chunk is in it, else straight from the block table.
-__device__ __forceinline__ int chunk_row(const PartialParams& p, const Small& sm, int b, int start,
-                                         int j0, bool* clamped) {
+__device__ __forceinline__ int chunk_row(const PartialParams& p, const int32_t* block_table,
+                                         const Small& sm, int b, int start, int j0,
+                                         bool* clamped) {
     const int c = (j0 - start) / kChunk;
     if (c < kRowCache) return sm.rows[c];
-    const int2 r = table_row(p.block_table, b, p.max_pages_per_seq, p.page_size, p.num_pages, j0);
+    const int2 r = table_row(block_table, b, p.max_pages_per_seq, p.page_size, p.num_pages, j0);
     if (r.y) *clamped = true;
     return r.x;
 }
@@ -341,8 +343,8 @@ __device__ __forceinline__ void fused_merge(const PartialParams& p, uint8_t* sme
 }
 
 // kFused: the instance that merges the splits after the grid barrier (p.out set); the other
-// carries no merge code at all.
-template <int RP, bool kFused>
+// carries no merge code at all. kView: which keys and rows the launch covers (common.cuh).
+template <int RP, bool kFused, View kView>
 __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     tc_partial_kernel(const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, const PartialParams p) {
@@ -368,21 +370,32 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     // the guess holds.
     // (divisions by the page size become shifts for power-of-two pages, and the tile size is
     // this kernel's constant: the set-up's dependent chain is short)
+    // A shared prefix's length is read first (no lookup ahead of it).
+    int base = 0, view_flags = 0;
+    const int32_t* table = p.block_table;
+    if constexpr (kView != View::kWhole) {
+        base = shared_keys(p.prefix_len, p.max_prefix, P, &view_flags);
+        if constexpr (kView == View::kSuffix) table += base / P;
+    }
     const int per_max = p.per_max;
     int page_max = 0;
-    if (tid < kRowCache && rblk.xs * per_max + tid * kChunk < p.max_context) {
+    if (kView == View::kWhole && tid < kRowCache && rblk.xs * per_max + tid * kChunk < p.max_context) {
         const int j = rblk.xs * per_max + tid * kChunk;
         page_max = p.block_table[(int64_t)blockIdx.z * p.max_pages_per_seq +
                                  (p.page_shift >= 0 ? j >> p.page_shift : j / P)];
     }
     const int slot = rblk.slot;
     // a single sequence's unit is the grid row (KV head): no search, no division
-    const UnitSlots us =
-        p.batch == 1 ? locate_slots_single(p.context_lens, p.num_kv_heads, p.num_splits,
-                                           p.max_context, p.q_len, blockIdx.y, false)
-                     : locate_slots(p.context_lens, p.batch, p.num_kv_heads, p.num_splits,
-                                    p.num_slots, p.max_context, p.q_len, slot, true);
-    if (slot == 0 && tid == 0 && us.flags) atomicOr(p.status, us.flags);
+    UnitSlots us;
+    if constexpr (kView == View::kPrefix)
+        us = UnitSlots{0, (int)blockIdx.y, (int)blockIdx.y * p.num_splits, p.num_splits, base, 0};
+    else
+        us = p.batch == 1 ? locate_slots_single(p.context_lens, p.num_kv_heads, p.num_splits,
+                                                p.max_context, p.q_len, blockIdx.y, false, base)
+                          : locate_slots(p.context_lens, p.batch, p.num_kv_heads, p.num_splits,
+                                         p.num_slots, p.max_context, p.q_len, slot, true, base);
+    if (slot == 0 && tid == 0 && (us.flags | view_flags))
+        atomicOr(p.status, us.flags | view_flags);
     const int b = us.b, h = us.h, split = slot - us.first, n = us.n;
     int per = 1;
     if (b >= 0) {  // keys_per_split with this kernel's tile size
@@ -394,7 +407,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         if constexpr (kFused) fused_merge<C::kThreads>(p, smem);
         return;
     }
-    const bool guessed = b == (int)blockIdx.z && split == rblk.xs && per == per_max;
+    const bool guessed = kView == View::kWhole && b == (int)blockIdx.z && split == rblk.xs && per == per_max;
     const int end = min(n, start + per);
     const int ntiles = (end - start + kTile - 1) / kTile;
     const int nvst = (end - start + kVKeys - 1) / kVKeys;
@@ -439,7 +452,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
             const int lp = p.page_shift >= 0 ? j0 >> p.page_shift : j0 / P;
             const int phys = (guessed && c == tid)
                                  ? clamp_page(page_max, p.num_pages, &clamped)
-                                 : physical_page(p.block_table, b, p.max_pages_per_seq, lp,
+                                 : physical_page(table, b, p.max_pages_per_seq, lp,
                                                  p.num_pages, &clamped);
             sm.rows[c] = phys * P + (j0 - lp * P);
         }
@@ -476,14 +489,14 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
             for (int k = 0; k < kOwn; ++k) {
                 const int c = first + 3 * k;
                 const int j0 = tile0 + kChunk * c;
-                rows[k] = (c < kChunks && j0 < end) ? chunk_row(p, sm, b, start, j0, &clamped) : -1;
+                rows[k] = (c < kChunks && j0 < end) ? chunk_row(p, table, sm, b, start, j0, &clamped) : -1;
             }
         };
         const int kfirst = ci, vfirst = (ci + 1) % 3;
         // Keys from n - q_len on (the drafted tokens) may be written by the kernel just before
         // this one (their KV write): tiles reaching them are copied only after griddep_wait,
         // which returns at once unless this grid is a programmatic dependent.
-        const int drafted = n - p.q_len;
+        const int drafted = kView == View::kPrefix ? n : n - p.q_len;
         bool dep_done = false;
         int krows[kOwn], vrows[kOwn];
         if (lane == 0) {
@@ -556,7 +569,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                         const uint32_t dst = smem_u32(vstage);
 #pragma unroll 1
                         for (int c = 0; c < nval; ++c) {
-                            const int row = chunk_row(p, sm, b, start, h0 + kChunk * c, &clamped);
+                            const int row = chunk_row(p, table, sm, b, start, h0 + kChunk * c, &clamped);
                             tma_load_4d(dst + c * kChunkBytes, &vmap, 0, 0, 2 * h, row / 8, bar,
                                         stream);
                         }
@@ -694,7 +707,9 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         const int st = (wq << 5) | lane;  // key of the tile = tensor-memory lane
         const int row0 = kGroupRows * g;
         const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16);
-        const int qoff = n - p.q_len;  // row r of the slot sees keys j <= qoff + r / G
+        // row r of the slot sees keys j <= qoff + r / G; over a shared prefix every row has a limit
+        // of its own, and qoff becomes the least of the group's
+        int qoff = n - p.q_len;
 
         // Q -> three E4M3 terms (one warp per row), row scales. Q and the scales, and every
         // workspace write below, come after the preceding kernel's completion (a no-op unless
@@ -763,6 +778,17 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                         make_uint2(packed[0], packed[1]);
                 }
                 if (lane == 0) sm.c0[r] = qk_scale * __int_as_float((127 - a) << 23);
+                if constexpr (kView == View::kPrefix) {
+                    if (lane == 0) {
+                        const int i = (row_lo + r) / G, sb = i / p.batch_q_len;
+                        int lim = n;  // a sequence's last tokens may stand inside the prefix
+                        if (r < R) {
+                            const int ctx = min(p.context_lens[sb], p.batch_max_context);
+                            lim = min(lim, ctx - p.batch_q_len + (i - sb * p.batch_q_len) + 1);
+                        }
+                        sm.limit[r] = lim;
+                    }
+                }
             }
             fence_async_smem();
             __syncwarp();
@@ -773,6 +799,11 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         // of 64-bit words, identical for every thread of the group). Scores, exponents, row sums
         // and probabilities are handled as FP32 pairs (element i of a 16-row block is word i / 2,
         // half i % 2).
+        if constexpr (kView == View::kPrefix) {
+            qoff = n - 1;
+#pragma unroll
+            for (int i = 0; i < kGroupRows; ++i) qoff = min(qoff, sm.limit[row0 + i] - 1);
+        }
         uint64_t lsum[kGroupRows / 2];
         uint32_t rowmask = 0;
 #pragma unroll
@@ -820,9 +851,13 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                 // row r of the slot (query token r / G) sees key j iff r / G >= j - qoff, that is
                 // r >= (j - qoff) G: the group's rows from `first` on
                 const int first = (j - qoff) * G - row_lo - row0;
-                if (j >= end)
+                if (j >= end) {
                     validm = 0;
-                else if (first > 0)
+                } else if constexpr (kView == View::kPrefix) {
+#pragma unroll 1
+                    for (int i = 0; i < kGroupRows; ++i)
+                        if (j >= sm.limit[row0 + i]) validm &= ~(1u << i);
+                } else if (first > 0)
                     validm &= first >= kGroupRows ? 0u : (0xFFFFFFFFu << first);
             }
             // e = y c0 + (s - m): the exponent of the shifted probability, one fused multiply-add
@@ -1100,11 +1135,11 @@ static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     return fn;
 }
 
-template <int RP, bool kFused>
+template <int RP, bool kFused, View kView = View::kWhole>
 static cudaError_t launch_rp(const CUtensorMap& kmap, const CUtensorMap& vmap,
                              const PartialParams& p, cudaStream_t stream) {
     constexpr uint32_t smem = tc::smem_bytes<RP>();
-    cudaError_t e = cudaFuncSetAttribute(tc::tc_partial_kernel<RP, kFused>,
+    cudaError_t e = cudaFuncSetAttribute(tc::tc_partial_kernel<RP, kFused, kView>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -1124,10 +1159,20 @@ static cudaError_t launch_rp(const CUtensorMap& kmap, const CUtensorMap& vmap,
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
-    return cudaLaunchKernelEx(&cfg, tc::tc_partial_kernel<RP, kFused>, kmap, vmap, p);
+    return cudaLaunchKernelEx(&cfg, tc::tc_partial_kernel<RP, kFused, kView>, kmap, vmap, p);
 }
 
-cudaError_t launch_tc_partial(const PartialParams& p, cudaStream_t stream) {
+template <View kView>
+static cudaError_t launch_view(const CUtensorMap& kmap, const CUtensorMap& vmap, int rp,
+                               const PartialParams& p, cudaStream_t stream) {
+    switch (rp) {
+        case 16: return launch_rp<16, false, kView>(kmap, vmap, p, stream);
+        case 32: return launch_rp<32, false, kView>(kmap, vmap, p, stream);
+        default: return launch_rp<48, false, kView>(kmap, vmap, p, stream);
+    }
+}
+
+cudaError_t launch_tc_partial(const PartialParams& p, cudaStream_t stream, View view) {
     if (!row_blocks_valid(p, tc::kMaxRP)) return cudaErrorInvalidValue;
     const int rp = tc_rows_pad(p.block_rows);
     const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
@@ -1153,6 +1198,8 @@ cudaError_t launch_tc_partial(const PartialParams& p, cudaStream_t stream) {
                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r1 != CUDA_SUCCESS || r2 != CUDA_SUCCESS) return cudaErrorInvalidValue;
+    if (view == View::kSuffix) return launch_view<View::kSuffix>(kmap, vmap, rp, p, stream);
+    if (view == View::kPrefix) return launch_view<View::kPrefix>(kmap, vmap, rp, p, stream);
     switch (rp) {
         case 16: return p.out ? launch_rp<16, true>(kmap, vmap, p, stream)
                               : launch_rp<16, false>(kmap, vmap, p, stream);
