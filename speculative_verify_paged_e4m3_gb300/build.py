@@ -19,7 +19,8 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 INCLUDE = os.path.join(ROOT, "include")
 
 SOURCES = ["api.cu", "simt_partial.cu", "tc_partial.cu", "combine.cu", "static_scratch.cu",
-           "kv_write.cu", "paged_tables.cu", "rope.cu", "prefix_attn.cu"]
+           "kv_write.cu", "paged_tables.cu", "rope.cu", "prefix_attn.cu",
+           "prefix_pairs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
           "-I", INCLUDE, "-I", CSRC]

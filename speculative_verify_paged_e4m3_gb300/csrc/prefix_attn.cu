@@ -15,6 +15,7 @@
 #include "combine_impl.cuh"
 #include "common.cuh"
 #include "dflash_paged_step.h"
+#include "prefix_pairs.cuh"
 
 namespace dflash {
 
@@ -25,6 +26,7 @@ namespace {
 
 constexpr int kMaxBatch = 4096;
 constexpr int kMinSplitKeys = 256;
+constexpr int kPairsFromRows = 400;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -40,6 +42,7 @@ struct PrefixCombineParams {
     int max_context, max_prefix;
     int own_splits, own_slots;   // the suffix plan's num_splits and num_slots
     int pre_splits, pre_rows;    // prefix: splits per KV head, rows of the whole batch
+    int pre_blocks, pre_pairs;   // pair kernel: row blocks per KV head, pairs of SMs (else 0)
 };
 
 constexpr int kRowCols = kHeadDim / 4;                   // 64 float4 columns per row
@@ -63,19 +66,32 @@ __global__ void __launch_bounds__(kCombineThreads)
     const int own_n = us.count > 0 ? us.n : 0;
     const int own_per = own_n > 0 ? keys_per_split(own_n, us.count, 128, kMinSplitKeys) : 1;
     const int own_active = own_n > 0 ? (own_n + own_per - 1) / own_per : 0;
-    // prefix: slots [h * pre_splits, + pre_active) of pre_rows rows, this row at b * rows + r
-    const int pre_per = base > 0 ? keys_per_split(base, p.pre_splits, 128, kMinSplitKeys) : 1;
-    const int pre_active = base > 0 ? (base + pre_per - 1) / pre_per : 0;
+    // prefix: pre_active states, pre_step rows apart from pre0 on
+    const int prow = b * p.rows + r;  // row of the whole batch
+    int pre_active = 0, pre_step = p.pre_rows;
+    int64_t pre0 = 0;
+    if (base > 0 && p.pre_pairs > 0) {  // the segments of this row's block, in slots pair + unit
+        const PairShare share = pair_share(base, p.pre_blocks * p.num_kv_heads, p.pre_pairs);
+        const int pu = h * p.pre_blocks + prow / kPairRows;
+        const int64_t t0 = (int64_t)pu * share.tiles;
+        const int first = (int)(t0 / share.per_pair);
+        pre_active = (int)((t0 + share.tiles - 1) / share.per_pair) - first + 1;
+        pre_step = kPairRows;
+        pre0 = (int64_t)(first + pu) * kPairRows + prow % kPairRows;
+    } else if (base > 0) {  // slots [h * pre_splits, + pre_active) of pre_rows rows
+        const int per = keys_per_split(base, p.pre_splits, 128, kMinSplitKeys);
+        pre_active = (base + per - 1) / per;
+        pre0 = (int64_t)h * p.pre_splits * p.pre_rows + prow;
+    }
     const int64_t own0 = (int64_t)us.first * p.rows + r;
-    const int64_t pre0 = (int64_t)h * p.pre_splits * p.pre_rows + (int64_t)b * p.rows + r;
     const int total = pre_active + own_active;
     auto state_at = [&](int s) {
-        return s < pre_active ? p.pre_state + pre0 + (int64_t)s * p.pre_rows
+        return s < pre_active ? p.pre_state + pre0 + (int64_t)s * pre_step
                               : p.own_state + own0 + (int64_t)(s - pre_active) * p.rows;
     };
     auto acc_at = [&](int s) {
         const float* a = s < pre_active
-                             ? p.pre_acc + (pre0 + (int64_t)s * p.pre_rows) * kHeadDim
+                             ? p.pre_acc + (pre0 + (int64_t)s * pre_step) * kHeadDim
                              : p.own_acc + (own0 + (int64_t)(s - pre_active) * p.rows) * kHeadDim;
         return reinterpret_cast<const float4*>(a) + col;
     };
@@ -149,17 +165,32 @@ int make_plan(const dflash_prefix_attn_problem* pr, dflash_prefix_attn_plan_t* p
     plan->sm_count = plan->suffix.sm_count;
     const int64_t rows = (int64_t)pr->batch * plan->suffix.rows;
     plan->prefix_rows = (int32_t)rows;
-    plan->prefix_kernel = DFLASH_PREFIX_KERNEL_ROWS;
-    const int64_t blocks = ceil_div(rows, tc_max_rows());
-    int64_t S = plan->sm_count / (blocks * pr->num_kv_heads);  // one wave
-    const int64_t cap = ceil_div(pr->max_prefix, kMinSplitKeys);
-    if (S > cap) S = cap;
-    if (S < 1) S = 1;
-    plan->prefix_row_blocks = (int32_t)blocks;
-    plan->prefix_splits = (int32_t)S;
-    plan->prefix_slots = pr->max_prefix > 0 ? (int32_t)(S * pr->num_kv_heads) : 0;
-    plan->prefix_slot_rows = (int32_t)rows;
-    if (S * blocks > 0x7FFFFFFF || pr->num_kv_heads > 65535) return DFLASH_ERR_UNSUPPORTED;
+    const bool use_pairs = pr->kernel == DFLASH_PREFIX_KERNEL_PAIRS ||
+                           (pr->kernel == DFLASH_PREFIX_KERNEL_AUTO && rows >= kPairsFromRows);
+    int64_t slots;
+    if (use_pairs) {
+        plan->prefix_kernel = DFLASH_PREFIX_KERNEL_PAIRS;
+        const int64_t blocks = ceil_div(rows, kPairRows);
+        plan->prefix_row_blocks = (int32_t)blocks;
+        plan->prefix_splits = plan->sm_count / 2;
+        if (plan->prefix_splits < 1) return DFLASH_ERR_UNSUPPORTED;
+        slots = plan->prefix_splits + blocks * pr->num_kv_heads;  // a segment's slot: pair + unit
+        plan->prefix_slot_rows = kPairRows;
+    } else {
+        plan->prefix_kernel = DFLASH_PREFIX_KERNEL_ROWS;
+        const int64_t blocks = ceil_div(rows, tc_max_rows());
+        int64_t S = plan->sm_count / (blocks * pr->num_kv_heads);  // one wave
+        const int64_t cap = ceil_div(pr->max_prefix, kMinSplitKeys);
+        if (S > cap) S = cap;
+        if (S < 1) S = 1;
+        plan->prefix_row_blocks = (int32_t)blocks;
+        plan->prefix_splits = (int32_t)S;
+        slots = S * pr->num_kv_heads;
+        plan->prefix_slot_rows = (int32_t)rows;
+        if (S * blocks > 0x7FFFFFFF || pr->num_kv_heads > 65535) return DFLASH_ERR_UNSUPPORTED;
+    }
+    if (slots > 0x7FFFFFFF) return DFLASH_ERR_UNSUPPORTED;
+    plan->prefix_slots = pr->max_prefix > 0 ? (int32_t)slots : 0;
     const size_t states = (size_t)plan->prefix_slots * plan->prefix_slot_rows;
     plan->ws_prefix_state_offset = align_up(plan->suffix.workspace_bytes, 256);
     plan->ws_prefix_acc_offset =
@@ -232,7 +263,35 @@ int dflash_prefix_attn_forward(const dflash_prefix_attn_plan_t* plan, const void
     p.max_prefix = pr.max_prefix;
     p.prefix_len = prefix_len;
     cudaError_t e = cudaSuccess;
-    if (prefix) {
+    const bool by_pairs = plan->prefix_kernel == DFLASH_PREFIX_KERNEL_PAIRS;
+    if (prefix && by_pairs) {
+        PrefixPairsParams a;
+        a.q = p.q;
+        a.k_pool = p.k_pool;
+        a.v_pool = p.v_pool;
+        a.prefix_table = prefix_table;
+        a.prefix_len = prefix_len;
+        a.context_lens = context_lens;
+        a.k_scale = k_scale;
+        a.v_scale = v_scale;
+        a.status = p.status;
+        a.ws_state = reinterpret_cast<float2*>(ws + plan->ws_prefix_state_offset);
+        a.ws_acc = reinterpret_cast<float*>(ws + plan->ws_prefix_acc_offset);
+        a.rows = plan->prefix_rows;
+        a.blocks = plan->prefix_row_blocks;
+        a.units = a.blocks * pr.num_kv_heads;
+        a.pairs = plan->prefix_splits;
+        a.q_len = pr.q_len;
+        a.group = p.group;
+        a.num_q_heads = pr.num_q_heads;
+        a.num_kv_heads = pr.num_kv_heads;
+        a.page_size = pr.page_size;
+        a.page_shift = p.page_shift;
+        a.num_pages = pr.num_pages;
+        a.max_prefix = pr.max_prefix;
+        a.max_context = pr.max_context;
+        e = launch_prefix_pairs(a, stream);
+    } else if (prefix) {
         PartialParams a = p;
         a.block_table = prefix_table;
         a.ws_state = reinterpret_cast<float2*>(ws + plan->ws_prefix_state_offset);
@@ -286,6 +345,8 @@ int dflash_prefix_attn_forward(const dflash_prefix_attn_plan_t* plan, const void
         c.own_slots = own.num_slots;
         c.pre_splits = plan->prefix_splits;
         c.pre_rows = plan->prefix_rows;
+        c.pre_blocks = plan->prefix_row_blocks;
+        c.pre_pairs = by_pairs ? plan->prefix_splits : 0;
         const dim3 grid(pr.batch * pr.num_kv_heads, (own.rows + kRowsPerCta - 1) / kRowsPerCta);
         prefix_combine_kernel<<<grid, kCombineThreads, 0, stream>>>(c);
         e = cudaGetLastError();

@@ -1,0 +1,692 @@
+// prefix_pairs.cu -- attention over a shared prefix for many query rows: FP16 tensor-core products
+// on pairs of SMs (tcgen05, cta_group::2).
+//
+// With batch * q_len * Hq / Hkv rows per KV head the prefix is no longer bound by HBM but by the
+// products, 4 D flops per row and key. The split kernel's three E4M3 terms cost 1.5 times the
+// tensor work of FP16 operands, and its accumulators (one per term) leave room for 48 rows. Here Q
+// stays FP16, K and V are decoded to FP16 (exact) on their way into shared memory, P is rounded
+// to FP16 (2^-11 of each probability), all sums are FP32.
+//
+//  * A pair of SMs carries 256 rows: 128 on each (tensor-memory lane = row), accumulator O [128,
+//    256] FP32 in each SM's tensor memory. One SM's 128 rows alone would need each decoded K and V
+//    byte written and read by that SM only: about 3500 clocks of shared-memory traffic per 2048 of
+//    tensor work. With cta_group::2 the pair's second operand is split between the two SMs, so that
+//    each decodes and stores half of it (half of the tile's keys of K, half of the head dim of V).
+//  * Tiles of 96 keys: two score buffers of 96 columns and P (48 columns, two FP16 each) fit beside O
+//    in the 512 columns of tensor memory, and P needs no buffer of its own in shared memory. P does not
+//    share its columns with scores, so that no product overwrites what another one may still read.
+//  * Warps: 0-3 softmax (thread = row), 4-6 decode K, 7-9 decode V, 10 issues the products of the pair
+//    (one thread, in the leader SM alone), 11 copies the codes (TMA, three tiles of K and two of V ahead). While the
+//    softmax works on tile t the tensor core has QK of tile t + 1, then PV of t.
+//  * Probabilities are p = 2^(score - m) for a reference maximum m that is the first tile's, and moves
+//    only when a row's probabilities of one tile sum to more than 2^15 (so that all are inside FP16):
+//    scores, exponentials and sums are one pass with no maximum in front of it. When it moves, the
+//    rows' O columns are rescaled in place and the tile is done again; peaked scores should rarely
+//    get there (with m shifted by 2^-7 they did in most tiles: 177 us for 16 x 8 tokens over 32768).
+//    Below 2^-14 FP16 has a fixed grid, 2^-24 of the reference: noise of 2^-25 a key beside a sum of
+//    at least one.
+//  * Pairs take equal shares of all (KV head, row block) units' tiles (prefix_pairs.cuh); a share may
+//    end in the middle of a unit, the combine puts the parts together.
+//  * Every wait is bounded (200 ms, then DFLASH_FLAG_KERNEL_TIMEOUT and a clean exit); both SMs of
+//    a pair leave together.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include <type_traits>
+
+#include "common.cuh"
+#include "e4m3.cuh"
+#include "prefix_pairs.cuh"
+#include "tc_ptx.cuh"
+
+namespace dflash {
+namespace pairs {
+
+using namespace ptx;
+
+constexpr int kRows = kPairRows / 2;  // per SM
+constexpr int kTile = kPairTile;
+constexpr int kHalfKeys = kTile / 2;
+constexpr int kStages = 2;      // decoded tiles of K, and of V
+constexpr int kRawK = 3, kRawV = 2;  // tiles of codes on their way
+constexpr int kSoftWarps = 4, kDecodeWarps = 3;  // decoders per operand
+constexpr int kMmaWarp = kSoftWarps + 2 * kDecodeWarps, kCopyWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kCopyWarp + 1);  // 12 warps: 168 registers a thread
+constexpr uint64_t kWaitLimitNs = 200ull * 1000 * 1000;
+constexpr float kMaxSum = 32768.f;  // a row's probabilities of one tile sum to this at most
+
+// Shared memory: Q | K stages | V stages | codes of K | codes of V | Small. All operands are 128-byte swizzled: Q and K
+// [head-dim block of 64][row][64 FP16], V [head-dim block of 64][key][64 FP16].
+constexpr uint32_t kQBytes = kRows * kHeadDim * 2;
+constexpr uint32_t kKStage = kHalfKeys * kHeadDim * 2;       // this SM's 48 keys
+constexpr uint32_t kVStage = kTile * (kHeadDim / 2) * 2;     // this SM's 128 elements of 96 keys
+constexpr uint32_t kOffK = kQBytes;
+constexpr uint32_t kOffV = kOffK + kStages * kKStage;
+constexpr uint32_t kRawStage = kHalfKeys * kHeadDim;         // codes of either: 12 KB
+constexpr uint32_t kOffRawK = kOffV + kStages * kVStage;     // [key][256]
+constexpr uint32_t kOffRawV = kOffRawK + kRawK * kRawStage;  // [key][128]
+constexpr uint32_t kOffSmall = kOffRawV + kRawV * kRawStage;
+static_assert(kRawStage == kTile * kHeadDim / 2, "either operand");
+// Tensor memory columns
+constexpr uint32_t kColO = 0, kColS = kHeadDim, kColP = kColS + 2 * kTile;
+static_assert(kColP + kTile / 2 <= 512, "tensor memory");
+static_assert(kOffK % 1024 == 0 && kOffV % 1024 == 0 && kKStage % 1024 == 0 &&
+                  kVStage % 1024 == 0,
+              "swizzled operands are 1 KB aligned");
+
+struct Small {
+    uint64_t kfull[kStages], vfull[kStages], qfull, pfull;   // used in the leader
+    uint64_t kempty[kStages], vempty[kStages], sfull[2], done;  // in both, by the pair's commits
+    uint64_t rkfull[kRawK], rkempty[kRawK], rvfull[kRawV], rvempty[kRawV];  // this SM's copies
+    uint32_t tmem_base;
+    int abort;
+};
+constexpr uint32_t kSmemBytes = kOffSmall + sizeof(Small);
+static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+
+// ---- cluster and pair instructions -------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::
+                     : "memory");
+}
+// Arrive on the barrier at the same place in the leader's shared memory. What the arrival orders are
+// operands of the products (tensor memory, and shared memory through the async proxy), which the fences
+// before it cover; the default scope keeps it free of a cluster-wide fence of ordinary memory (with
+// .release.cluster an arrival took about 1200 clocks).
+__device__ __forceinline__ void arrive_leader(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .b32 remote;\n\t"
+        "mapa.shared::cluster.u32 remote, %0, 0;\n\t"
+        "mbarrier.arrive.shared::cluster.b64 _, [remote];\n\t}" ::"r"(bar)
+        : "memory");
+}
+// D += A B^T over 16 elements of K, FP16 operands: A from shared memory, or from tensor memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive on the barrier of both SMs once every product issued so far has completed.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+    const uint16_t both = 3;
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(bar),
+        "h"(both)
+        : "memory");
+}
+// 2-D tiled copy global -> this SM's shared memory; coordinates innermost first.
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, int x, int y,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
+                     taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                 "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void soft_sync() {  // the softmax warps (named barrier 1)
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftWarps) : "memory");
+}
+
+struct Ctx {
+    Small* sm;
+    int32_t* status;
+    __device__ bool aborted() const { return *reinterpret_cast<volatile int*>(&sm->abort) != 0; }
+    __device__ void give_up() const {
+        *reinterpret_cast<volatile int*>(&sm->abort) = 1;
+        atomicOr(status, DFLASH_FLAG_KERNEL_TIMEOUT);
+    }
+    __device__ bool wait(uint64_t* bar, uint32_t parity) const {
+        const uint32_t a = smem_u32(bar);
+        if (mbar_try_wait(a, parity)) return true;
+        const uint64_t t0 = globaltimer_ns();
+        for (uint32_t it = 1;; ++it) {
+            if (mbar_try_wait(a, parity)) return true;
+            if ((it & 7) == 0) {
+                if (aborted()) return false;
+                if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                    give_up();
+                    return false;
+                }
+            }
+        }
+    }
+    // every lane waits and the warp agrees on the result
+    __device__ bool wait_warp(uint64_t* bar, uint32_t parity) const {
+        return __all_sync(0xffffffffu, wait(bar, parity));
+    }
+};
+
+// Wait (bounded, whatever became of the other warps) for a copy in flight.
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(smem_u32(bar), parity) && globaltimer_ns() - t0 < kWaitLimitNs) {
+    }
+}
+
+// The segments of a pair, in order: every role walks the same list.
+struct Segments {
+    int64_t at, end;  // tiles of the line still to do
+    int tiles;        // per unit
+    int unit, first, count;  // the current segment: its unit, first tile, tile count
+    __device__ Segments(const PairShare& s, int pair, int units) {
+        const int64_t total = (int64_t)units * s.tiles;
+        tiles = s.tiles;
+        at = pair * s.per_pair;
+        end = at + s.per_pair < total ? at + s.per_pair : total;
+    }
+    __device__ bool next() {
+        if (at >= end) return false;
+        unit = (int)(at / tiles);
+        first = (int)(at - (int64_t)unit * tiles);
+        const int64_t left = end - at;
+        count = left < tiles - first ? (int)left : tiles - first;
+        at += count;
+        return true;
+    }
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    prefix_pairs_kernel(const __grid_constant__ CUtensorMap kmap,
+                        const __grid_constant__ CUtensorMap vmap, const PrefixPairsParams p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Small& sm = *reinterpret_cast<Small*>(smem + kOffSmall);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1;
+    int flags = 0;
+    const int keys = shared_keys(p.prefix_len, p.max_prefix, p.page_size, &flags);
+    if (flags && blockIdx.x == 0 && tid == 0) atomicOr(p.status, flags);
+    const PairShare share = pair_share(keys, p.units, p.pairs);
+    if (pair * share.per_pair >= (int64_t)p.units * share.tiles) return;  // both SMs agree
+    if (smem_u32(smem) & 1023u) {  // the swizzled layouts need a 1 KB aligned base
+        if (tid == 0) atomicOr(p.status, DFLASH_FLAG_KERNEL_TIMEOUT);
+        return;
+    }
+    Segments seg(share, pair, p.units);
+    const Ctx ctx{&sm, p.status};
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_u32(&sm.kfull[i]), 2 * kDecodeWarps);
+            mbar_init(smem_u32(&sm.vfull[i]), 2 * kDecodeWarps);
+            mbar_init(smem_u32(&sm.kempty[i]), 1);
+            mbar_init(smem_u32(&sm.vempty[i]), 1);
+        }
+        mbar_init(smem_u32(&sm.qfull), 2 * kSoftWarps);
+        mbar_init(smem_u32(&sm.pfull), 2 * kSoftWarps);
+        mbar_init(smem_u32(&sm.sfull[0]), 1);
+        mbar_init(smem_u32(&sm.sfull[1]), 1);
+        mbar_init(smem_u32(&sm.done), 1);
+        for (int i = 0; i < kRawK; ++i) {
+            mbar_init(smem_u32(&sm.rkfull[i]), 1);
+            mbar_init(smem_u32(&sm.rkempty[i]), kDecodeWarps);
+        }
+        for (int i = 0; i < kRawV; ++i) {
+            mbar_init(smem_u32(&sm.rvfull[i]), 1);
+            mbar_init(smem_u32(&sm.rvempty[i]), kDecodeWarps);
+        }
+        prefetch_tensormap(&kmap);
+        prefetch_tensormap(&vmap);
+        sm.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        __syncwarp();
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         smem_u32(&sm.tmem_base))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+
+    if (warp >= kSoftWarps && warp < kMmaWarp) {
+        // ------------------------------------------------------------------ decoders
+        // A lane takes 8 codes (8 bytes) at a time and stores them as one 16-byte unit: loads of a warp
+        // are whole rows of codes and the 8 lanes of a store phase fill one 128-byte row, so neither
+        // meets a bank twice. K warp w has keys 16 w + i of this SM's 48, V warp w keys 32 w + 2 i and
+        // 32 w + 2 i + 1 of the tile's 96 (i < 16).
+        const bool is_k = warp < kSoftWarps + kDecodeWarps;
+        const int w = warp - kSoftWarps - (is_k ? 0 : kDecodeWarps);
+        uint64_t* full = is_k ? sm.kfull : sm.vfull;
+        uint64_t* empty = is_k ? sm.kempty : sm.vempty;
+        uint64_t* raw_full = is_k ? sm.rkfull : sm.rvfull;
+        uint64_t* raw_empty = is_k ? sm.rkempty : sm.rvempty;
+        const int raw_stages = is_k ? kRawK : kRawV;
+        const uint8_t* src0 = smem + (is_k ? kOffRawK : kOffRawV) + w * (kRawStage / 3) + 8 * lane;
+        const int b = is_k ? 0 : lane >> 4;  // which of a V lane's two keys
+        const int group = is_k ? lane : lane & 15;
+        uint8_t* dst0 = smem + (is_k ? kOffK : kOffV) +
+                        (group >> 3) * ((is_k ? kHalfKeys : kTile) * 128) +
+                        (is_k ? 16 * w : 32 * w + b) * 128;
+        const uint32_t unit = (uint32_t)((group & 7) ^ b) << 4;  // swizzled by the key's low bits
+        const uint32_t stage_bytes = is_k ? kKStage : kVStage;
+        int rs = 0, rphase = 0;
+        bool live = true;
+        for (int g = 0; live && seg.next();) {
+            for (int i = 0; i < seg.count; ++i, ++g) {
+                const int s = g % kStages;
+                const int j0 = (seg.first + i) * kTile +
+                               (is_k ? (int)rank * kHalfKeys + 16 * w : 32 * w);
+                live = ctx.wait_warp(&raw_full[rs], rphase) &&
+                       ctx.wait_warp(&empty[s], ((g / kStages) & 1) ^ 1);
+                if (!live) break;
+                const uint8_t* src = src0 + rs * kRawStage;
+                uint8_t* dst = dst0 + s * stage_bytes;
+                // the keys of this warp in 16-key chunks (one of K, two of V); a chunk past the
+                // prefix was not copied, and its keys are zeros
+                const bool live_a = j0 < keys, live_b = is_k ? live_a : j0 + 16 < keys;
+                auto decode = [&](auto is_k_) {
+                    constexpr bool kK = decltype(is_k_)::value;
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {  // 16 keys of V each, half of K's
+                        auto put = [&](int k, const uint4& f) {
+                            const int r = (8 * hf + k) * (kK ? 1 : 2);  // less the lane's key bit
+                            *reinterpret_cast<uint4*>(dst + r * 128 + (unit ^ ((r & 7) << 4))) = f;
+                        };
+                        if (hf ? live_b : live_a) {
+                            uint2 v[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                v[k] = *reinterpret_cast<const uint2*>(src + (8 * hf + k) * 256);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                uint4 f;
+                                e4m3x4_to_f16x4(v[k].x, f.x, f.y);
+                                e4m3x4_to_f16x4(v[k].y, f.z, f.w);
+                                put(k, f);
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) put(k, make_uint4(0, 0, 0, 0));
+                        }
+                    }
+                };
+                if (is_k)
+                    decode(std::true_type{});
+                else
+                    decode(std::false_type{});
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    arrive_leader(smem_u32(&full[s]));
+                    mbar_arrive(smem_u32(&raw_empty[rs]));
+                }
+                if (++rs == raw_stages) {
+                    rs = 0;
+                    rphase ^= 1;
+                }
+            }
+        }
+    } else if (warp == kCopyWarp) {
+        // ------------------------------------------------------------------ copies
+        // Lane c < 6 looks up the page of the tile's 16-key chunk c, a tile ahead (the entry is not
+        // looked at before its tile's turn, so its load waits for nobody); lane 0 issues.
+        bool clamped = false;
+        auto logical = [&](int j) { return p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size; };
+        auto lookup = [&](int tile) {
+            const int j = tile * kTile + 16 * lane;
+            return lane < kTile / 16 && j < keys ? p.prefix_table[logical(j)] : 0;
+        };
+        int nk = 0, nv = 0;  // tiles of K and of V issued
+        bool live = true;
+        while (live && seg.next()) {
+            const int head = seg.unit / p.blocks;
+            int page = lookup(seg.first);
+            for (int i = 0; live && i < seg.count; ++i) {
+                const int page_next = lookup(seg.first + i + 1);
+                const int tile0 = (seg.first + i) * kTile, j = tile0 + 16 * lane;
+                const int chunks = min((keys - tile0) / 16, kTile / 16);  // of this tile
+                int row = 0;  // the chunk's row of the pool
+                if (lane < chunks)
+                    row = clamp_page(page, p.num_pages, &clamped) * p.page_size +
+                          (j - logical(j) * p.page_size);
+                const int ks = nk % kRawK, vs = nv % kRawV;
+                live = ctx.wait_warp(&sm.rkempty[ks], ((nk / kRawK) & 1) ^ 1);
+                if (!live) break;
+                {
+                    const int n = min(max(chunks - 3 * (int)rank, 0), 3);
+                    const uint32_t bar = smem_u32(&sm.rkfull[ks]);
+                    const uint32_t dst = smem_u32(smem + kOffRawK + ks * kRawStage);
+                    if (lane == 0) mbar_arrive_expect_tx(bar, n * 16 * kHeadDim);
+#pragma unroll
+                    for (int c = 0; c < 3; ++c) {
+                        const int y = __shfl_sync(0xffffffffu, row, 3 * rank + c);
+                        if (lane == 0 && c < n)
+                            tma_load_2d(dst + c * 16 * kHeadDim, &kmap, head * kHeadDim, y, bar);
+                    }
+                }
+                ++nk;
+                live = ctx.wait_warp(&sm.rvempty[vs], ((nv / kRawV) & 1) ^ 1);
+                if (!live) break;
+                {
+                    const uint32_t bar = smem_u32(&sm.rvfull[vs]);
+                    const uint32_t dst = smem_u32(smem + kOffRawV + vs * kRawStage);
+                    if (lane == 0) mbar_arrive_expect_tx(bar, chunks * 16 * (kHeadDim / 2));
+#pragma unroll
+                    for (int c = 0; c < kTile / 16; ++c) {
+                        const int y = __shfl_sync(0xffffffffu, row, c);
+                        if (lane == 0 && c < chunks)
+                            tma_load_2d(dst + c * 16 * (kHeadDim / 2), &vmap,
+                                        head * kHeadDim + (int)rank * (kHeadDim / 2), y, bar);
+                    }
+                }
+                ++nv;
+                page = page_next;
+            }
+        }
+        if (clamped) atomicOr(p.status, DFLASH_FLAG_PAGE_CLAMPED);
+        // no copy may still be writing this SM's shared memory when it leaves
+        for (int t = max(nk - kRawK, 0); t < nk; ++t)
+            drain(&sm.rkfull[t % kRawK], (t / kRawK) & 1);
+        for (int t = max(nv - kRawV, 0); t < nv; ++t)
+            drain(&sm.rvfull[t % kRawV], (t / kRawV) & 1);
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------------ products
+        if (rank == 0 && lane == 0) {
+            const uint32_t idesc_qk = idesc_f32acc(256, kTile, 0, 0, 0, 0);
+            const uint32_t idesc_pv = idesc_f32acc(256, kHeadDim, 0, 0, 0, 1);
+            const uint32_t qb = smem_u32(smem), kb0 = smem_u32(smem + kOffK),
+                           vb0 = smem_u32(smem + kOffV);
+            int g = 0, sidx = 0;
+            bool ok = true;
+            auto issue_qk = [&](int t) {  // t: tile of the pair's line
+                const int s = t % kStages;
+                ok = ctx.wait(&sm.kfull[s], (t / kStages) & 1);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t kb = kb0 + s * kKStage;
+                const uint32_t d = tmem + kColS + (t & 1) * kTile;
+#pragma unroll
+                for (int k = 0; k < kHeadDim / 16; ++k)
+                    mma_ss(d,
+                           smem_desc(qb + (k >> 2) * (kRows * 128) + (k & 3) * 32, 16, 1024,
+                                     kSwizzle128B),
+                           smem_desc(kb + (k >> 2) * (kHalfKeys * 128) + (k & 3) * 32, 16, 1024,
+                                     kSwizzle128B),
+                           idesc_qk, k > 0);
+                commit_pair(smem_u32(&sm.kempty[s]));
+                commit_pair(smem_u32(&sm.sfull[t & 1]));
+            };
+            while (ok && seg.next()) {
+                ok = ctx.wait(&sm.qfull, sidx & 1);
+                if (ok) issue_qk(g);
+                for (int i = 0; ok && i < seg.count; ++i) {
+                    const int t = g + i, s = t % kStages;
+                    // scores of tile t + 1 take the buffer of t - 1, which the softmax has read: it
+                    // wrote P of t - 1 afterwards, and that was waited for
+                    if (i + 1 < seg.count) issue_qk(t + 1);
+                    ok = ok && ctx.wait(&sm.vfull[s], (t / kStages) & 1) &&
+                         ctx.wait(&sm.pfull, t & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t vb = vb0 + s * kVStage;
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        mma_ts(tmem + kColO, tmem + kColP + 8 * k,
+                               smem_desc(vb + k * 2048, kTile * 128, 1024, kSwizzle128B),
+                               idesc_pv, i > 0 || k > 0);
+                    commit_pair(smem_u32(&sm.vempty[s]));
+                }
+                g += seg.count;
+                ++sidx;
+            }
+            commit_pair(smem_u32(&sm.done));  // every product issued above
+        }
+    } else {
+        // ------------------------------------------------------------------ softmax
+        const int row = tid;  // of this SM's 128 = lane of tensor memory
+        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+        // D^-1/2 = 1/16, log2 units. Row maxima below are taken before this factor, so it has to be
+        // positive: a negative scale's sign goes into Q, a scale of zero becomes a tiny one.
+        const float c_signed = __ldg(p.k_scale) * 0.0625f * kLog2e;
+        const float c = fmaxf(fabsf(c_signed), 1e-30f);
+        const uint32_t q_sign = c_signed < 0.f ? 0x80008000u : 0u;
+        const float vs = __ldg(p.v_scale);
+        const uint64_t c2 = pk2(c, c);
+        int g = 0;  // tile of the pair's line
+        bool alive = true;
+        while (seg.next()) {
+            const int head = seg.unit / p.blocks, blk = seg.unit - head * p.blocks;
+            const int row0 = blk * kPairRows + (int)rank * kRows;  // this SM's first row
+            const int slot = pair + seg.unit;
+            // Q rows -> swizzled shared memory, 32 rows a warp
+#pragma unroll 8
+            for (int k = 0; k < kRows / kSoftWarps; ++k) {
+                const int r = warp * (kRows / kSoftWarps) + k, rr = row0 + r;
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (rr < p.rows) {
+                    const int i = rr / p.group;
+                    const int64_t qrow =
+                        (int64_t)i * p.num_q_heads + head * p.group + (rr - i * p.group);
+                    w = reinterpret_cast<const uint4*>(p.q + qrow * kHeadDim)[lane];
+                    w = make_uint4(w.x ^ q_sign, w.y ^ q_sign, w.z ^ q_sign, w.w ^ q_sign);
+                }
+                *reinterpret_cast<uint4*>(smem + (lane >> 3) * (kRows * 128) + r * 128 +
+                                          (((lane & 7) ^ (r & 7)) << 4)) = w;
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive_leader(smem_u32(&sm.qfull));
+            // keys [0, limit) are visible to this thread's row
+            int limit = keys;
+            if (row0 + row < p.rows) {
+                const int i = (row0 + row) / p.group, b = i / p.q_len;
+                const int ctx_len = min(p.context_lens[b], p.max_context);
+                limit = min(limit, ctx_len - p.q_len + (i - b * p.q_len) + 1);
+            }
+            float nm = INFINITY;  // minus the reference maximum (log2 units); +inf: no key yet
+            float lsum = 0.f;
+            for (int i = 0; i < seg.count; ++i) {
+                const int t = g + i;
+                const int j0 = (seg.first + i) * kTile;
+                const uint32_t s_col = lanes + kColS + (t & 1) * kTile;
+                const bool whole = __all_sync(0xffffffffu, j0 + kTile <= limit);
+                if (alive && !ctx.wait_warp(&sm.sfull[t & 1], (t >> 1) & 1)) alive = false;
+                if (!alive) continue;
+                tc_fence_after();
+                uint32_t code[kTile / 2];
+                // p = 2^(s c + nm) as FP16 pairs and their FP32 sum, of the unrounded values, in one
+                // pass over the scores
+                auto probabilities = [&](auto whole_) {
+                    constexpr bool kWhole = decltype(whole_)::value;
+                    const uint64_t nm2 = pk2(nm, nm);
+                    uint64_t sum[2] = {0, 0};
+                    uint32_t a[2][16];
+                    tmem_ld16(s_col, a[0]);
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k) {
+                        tmem_ld_wait(a[k & 1]);
+                        if (k + 1 < kTile / 16) tmem_ld16(s_col + 16 * (k + 1), a[(k + 1) & 1]);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const uint64_t e = fma2(pk2(__uint_as_float(a[k & 1][2 * q]),
+                                                        __uint_as_float(a[k & 1][2 * q + 1])),
+                                                    c2, nm2);
+                            const int j = j0 + 16 * k + 2 * q;
+                            const float p0 = kWhole || j < limit ? ex2(lo2(e)) : 0.f;
+                            const float p1 = kWhole || j + 1 < limit ? ex2(hi2(e)) : 0.f;
+                            sum[q & 1] = add2(sum[q & 1], pk2(p0, p1));
+                            const __half2 h = __floats2half2_rn(p0, p1);
+                            code[8 * k + q] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                    }
+                    sum[0] = add2(sum[0], sum[1]);
+                    return lo2(sum[0]) + hi2(sum[0]);
+                };
+                float tsum = INFINITY;
+                if (i > 0) tsum = whole ? probabilities(std::true_type{})
+                                        : probabilities(std::false_type{});
+                // A sum that is too large (or infinite, or not a number) moves the row's reference: no
+                // probability is above its tile's sum, so smaller sums are inside FP16.
+                if (__any_sync(0xffffffffu, !(tsum <= kMaxSum))) {
+                    float mx = -INFINITY;
+#pragma unroll 1
+                    for (int k = 0; k < kTile / 16; ++k) {
+                        uint32_t a[16];
+                        tmem_ld16(s_col + 16 * k, a);
+                        tmem_ld_wait(a);
+#pragma unroll
+                        for (int q = 0; q < 16; ++q)
+                            if (j0 + 16 * k + q < limit) mx = fmaxf(mx, __uint_as_float(a[q]));
+                    }
+                    const float mo = -nm, mn = fmaxf(mo, mx * c);
+                    const float alpha = mn == -INFINITY ? 1.f : ex2(mo - mn);
+                    nm = -mn;
+                    lsum *= alpha;
+                    if (i > 0) {  // O holds the tiles before this one
+                        if (!ctx.wait_warp(&sm.vempty[(t - 1) % kStages], ((t - 1) / kStages) & 1)) {
+                            alive = false;
+                            continue;
+                        }
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int k = 0; k < kHeadDim / 16; ++k) {
+                            uint32_t o[16];
+                            tmem_ld16(lanes + kColO + 16 * k, o);
+                            tmem_ld_wait(o);
+#pragma unroll
+                            for (int q = 0; q < 16; ++q)
+                                o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
+                            tmem_st16(lanes + kColO + 16 * k, o);
+                        }
+                        tmem_st_wait();
+                    }
+                    tsum = probabilities(std::false_type{});
+                }
+                lsum += tsum;
+                // P of tile t - 1 has been read once its PV is done
+                if (i > 0 &&
+                    !ctx.wait_warp(&sm.vempty[(t - 1) % kStages], ((t - 1) / kStages) & 1)) {
+                    alive = false;
+                    continue;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < kTile / 16; ++k) tmem_st8(lanes + kColP + 8 * k, code + 8 * k);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_leader(smem_u32(&sm.pfull));
+            }
+            g += seg.count;
+            // ---- the segment's split state: (m, l), then the numerator through this warp's 16 KB
+            // of the Q area (no product reads Q any more), so that rows are stored whole
+            if (alive && !ctx.wait_warp(&sm.vempty[(g - 1) % kStages], ((g - 1) / kStages) & 1))
+                alive = false;
+            soft_sync();  // the last scores are complete for every warp: the Q area is free
+            if (alive) {
+                tc_fence_after();
+                if (row0 + row < p.rows)
+                    p.ws_state[(int64_t)slot * kPairRows + rank * kRows + row] =
+                        make_float2(-nm, lsum);
+                float4* stage = reinterpret_cast<float4*>(smem + warp * 16384);
+#pragma unroll 1
+                for (int part = 0; part < 2; ++part) {  // 128 columns each
+#pragma unroll 1
+                    for (int k = 0; k < 8; ++k) {
+                        uint32_t o[16];
+                        tmem_ld16(lanes + kColO + part * 128 + 16 * k, o);
+                        tmem_ld_wait(o);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            stage[lane * 32 + ((4 * k + q) ^ lane)] =
+                                make_float4(__uint_as_float(o[4 * q]) * vs,
+                                            __uint_as_float(o[4 * q + 1]) * vs,
+                                            __uint_as_float(o[4 * q + 2]) * vs,
+                                            __uint_as_float(o[4 * q + 3]) * vs);
+                    }
+                    __syncwarp();
+#pragma unroll 8
+                    for (int r = 0; r < 32; ++r) {
+                        const int rr = warp * 32 + r;
+                        if (row0 + rr < p.rows)
+                            reinterpret_cast<float4*>(
+                                p.ws_acc + ((int64_t)slot * kPairRows + rank * kRows + rr) *
+                                               kHeadDim)[part * 32 + lane] =
+                                stage[r * 32 + (lane ^ r)];
+                    }
+                    __syncwarp();
+                }
+            }
+            tc_fence_before();
+            soft_sync();  // every warp is through with the Q area
+        }
+        if (alive) ctx.wait_warp(&sm.done, 0);
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither SM leaves while the other may still arrive here or read here
+    if (warp == kMmaWarp) {
+        __syncwarp();
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem)
+                     : "memory");
+    }
+}
+
+}  // namespace pairs
+
+// (tc_partial.cu)
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+cudaError_t launch_prefix_pairs(const PrefixPairsParams& p, cudaStream_t stream) {
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode) return cudaErrorNotSupported;
+    // A pool as rows (tokens) of Hkv * 256 codes; boxes of one 16-token chunk of one head: whole rows
+    // of K (4 KB), this SM's half of the head dim of V (2 KB).
+    CUtensorMap kmap, vmap;
+    const cuuint64_t row = (cuuint64_t)p.num_kv_heads * kHeadDim;
+    const cuuint64_t dims[2] = {row, (cuuint64_t)p.num_pages * p.page_size};
+    const cuuint64_t strides[1] = {row};
+    const cuuint32_t kbox[2] = {kHeadDim, 16}, vbox[2] = {kHeadDim / 2, 16}, unit[2] = {1, 1};
+    const CUresult r1 = encode(&kmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                               const_cast<uint8_t*>(p.k_pool), dims, strides, kbox, unit,
+                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r2 = encode(&vmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                               const_cast<uint8_t*>(p.v_pool), dims, strides, vbox, unit,
+                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r1 != CUDA_SUCCESS || r2 != CUDA_SUCCESS) return cudaErrorInvalidValue;
+    const cudaError_t e = cudaFuncSetAttribute(pairs::prefix_pairs_kernel,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               pairs::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    pairs::prefix_pairs_kernel<<<2 * p.pairs, pairs::kThreads, pairs::kSmemBytes, stream>>>(
+        kmap, vmap, p);
+    return cudaGetLastError();
+}
+
+}  // namespace dflash

@@ -1,0 +1,48 @@
+// prefix_pairs.cuh -- how the pair kernel deals the shared prefix out to pairs of SMs, for the
+// kernel, the combine and the planner.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace dflash {
+
+constexpr int kPairRows = 256;     // query rows of a block: 128 on each SM of a pair
+constexpr int kPairTile = 96;      // keys per tile
+constexpr int kPairMinTiles = 4;   // least tiles worth a pair of their own
+
+// The work is units (KV head, row block), tiles of keys inside a unit, in one line: pair p takes
+// tiles [p * per_pair, (p + 1) * per_pair) of it. A pair's share of one unit is a segment with a
+// split state of its own in workspace slot p + unit: along the line either p or the unit moves on
+// at each new segment, so the sum names it, and pairs + units slots are enough.
+struct PairShare {
+    int tiles;         // per unit
+    int64_t per_pair;  // tiles per pair
+};
+
+__device__ __forceinline__ PairShare pair_share(int keys, int units, int pairs) {
+    PairShare s;
+    s.tiles = (keys + kPairTile - 1) / kPairTile;
+    const int64_t total = (int64_t)units * s.tiles;
+    s.per_pair = (total + pairs - 1) / pairs;
+    if (s.per_pair < kPairMinTiles) s.per_pair = kPairMinTiles;
+    return s;
+}
+
+struct PrefixPairsParams {
+    const __half* q;
+    const uint8_t *k_pool, *v_pool;
+    const int32_t *prefix_table, *prefix_len, *context_lens;
+    const float *k_scale, *v_scale;
+    int32_t* status;
+    float2* ws_state;  // [slots, 256]
+    float* ws_acc;     // [slots, 256, D]
+    int rows, blocks, units, pairs;
+    int q_len, group, num_q_heads, num_kv_heads;
+    int page_size, page_shift, num_pages, max_prefix, max_context;
+};
+
+cudaError_t launch_prefix_pairs(const PrefixPairsParams& p, cudaStream_t stream);
+
+}  // namespace dflash

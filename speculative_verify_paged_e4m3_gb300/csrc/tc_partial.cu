@@ -1119,7 +1119,7 @@ int tc_threads(int rows) {
 
 // The tensor-map encoder lives in the driver library; it is looked up at first use through the
 // runtime (so the library itself loads on machines without a driver, e.g. to plan and test).
-static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     static std::once_flag once;
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     std::call_once(once, [] {
