@@ -14,14 +14,17 @@
 //    each decodes and stores half of it (half of the tile's keys of K, half of the head dim of V).
 //  * Tiles of 96 keys: two score buffers of 96 columns and P (48 columns, two FP16 each) fit beside O
 //    in the 512 columns of tensor memory, and P needs no buffer of its own in shared memory. P does not
-//    share its columns with scores, so that no product overwrites what another one may still read.
-//  * Warps: 0-3 softmax (thread = row), 4-6 decode K, 7-9 decode V, 10 issues the products of the pair
-//    (one thread, in the leader SM alone), 11 copies the codes (TMA, three tiles of K and two of V ahead). While the
-//    softmax works on tile t the tensor core has QK of tile t + 1, then PV of t.
+//    share its columns with scores, so that no product overwrites what another one may still read; it
+//    is handed over in two halves of 48 keys, so that the softmax writes the next tile's first half
+//    while the products still read this one's second (in one piece that hand-over, 2000 clocks a tile,
+//    set the pace).
+//  * Warps: 0-7 softmax (thread = row, warps 0-3 the tile's first 48 keys, 4-7 the others), 8-9 decode
+//    K, 10-11 decode V, 12 issues the score products of the pair and 13 its PV (one thread each, in
+//    the leader SM alone), 14 copies the codes (TMA, three tiles of K and two of V ahead).
 //  * Probabilities are p = 2^(score - m) for a reference maximum m that is the first tile's, and moves
-//    only when a row's probabilities of one tile sum to more than 2^15 (so that all are inside FP16):
+//    only when a row's probabilities of 48 keys sum to more than 2^15 (so that all are inside FP16):
 //    scores, exponentials and sums are one pass with no maximum in front of it. When it moves, the
-//    rows' O columns are rescaled in place and the tile is done again; peaked scores should rarely
+//    rows' O columns are rescaled in place and the 48 keys are done again; peaked scores should rarely
 //    get there (with m shifted by 2^-7 they did in most tiles: 177 us for 16 x 8 tokens over 32768).
 //    Below 2^-14 FP16 has a fixed grid, 2^-24 of the reference: noise of 2^-25 a key beside a sum of
 //    at least one.
@@ -51,11 +54,12 @@ constexpr int kTile = kPairTile;
 constexpr int kHalfKeys = kTile / 2;
 constexpr int kStages = 2;      // decoded tiles of K, and of V
 constexpr int kRawK = 3, kRawV = 2;  // tiles of codes on their way
-constexpr int kSoftWarps = 4, kDecodeWarps = 3;  // decoders per operand
-constexpr int kMmaWarp = kSoftWarps + 2 * kDecodeWarps, kCopyWarp = kMmaWarp + 1;
-constexpr int kThreads = 32 * (kCopyWarp + 1);  // 12 warps: 168 registers a thread
+constexpr int kSoftWarps = 8, kDecodeWarps = 2;  // decoders per operand
+constexpr int kQkWarp = kSoftWarps + 2 * kDecodeWarps, kPvWarp = kQkWarp + 1;
+constexpr int kCopyWarp = kPvWarp + 1;
+constexpr int kThreads = 32 * (kCopyWarp + 1);  // 15 warps: 128 registers a thread
 constexpr uint64_t kWaitLimitNs = 200ull * 1000 * 1000;
-constexpr float kMaxSum = 32768.f;  // a row's probabilities of one tile sum to this at most
+constexpr float kMaxSum = 32768.f;  // a row's probabilities of a half tile sum to this at most
 
 // Shared memory: Q | K stages | V stages | codes of K | codes of V | Small. All operands are 128-byte swizzled: Q and K
 // [head-dim block of 64][row][64 FP16], V [head-dim block of 64][key][64 FP16].
@@ -77,11 +81,15 @@ static_assert(kOffK % 1024 == 0 && kOffV % 1024 == 0 && kKStage % 1024 == 0 &&
               "swizzled operands are 1 KB aligned");
 
 struct Small {
-    uint64_t kfull[kStages], vfull[kStages], qfull, pfull;   // used in the leader
-    uint64_t kempty[kStages], vempty[kStages], sfull[2], done;  // in both, by the pair's commits
+    // in the leader: operands and P ready, scores read
+    uint64_t kfull[kStages], vfull[kStages], qfull, pfull[2], sfree[2];
+    // in both, by the pair's commits: scores complete (and their K stage free), P's first half read,
+    // V stage (and P's second half) free, everything complete
+    uint64_t sfull[kStages], pdone, vempty[kStages], done;
     uint64_t rkfull[kRawK], rkempty[kRawK], rvfull[kRawV], rvempty[kRawV];  // this SM's copies
     uint32_t tmem_base;
     int abort;
+    float part[2][kRows];  // row maxima, then row sums, of the two halves of a tile's keys
 };
 constexpr uint32_t kSmemBytes = kOffSmall + sizeof(Small);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
@@ -149,7 +157,18 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
                  "r"(r[7])
                  : "memory");
 }
-__device__ __forceinline__ void soft_sync() {  // the softmax warps (named barrier 1)
+// OR of a predicate over the softmax threads (named barrier 1), and a plain barrier of theirs.
+__device__ __forceinline__ bool soft_vote(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred pv, pr;\n\tsetp.ne.u32 pv, %1, 0;\n\t"
+        "bar.red.or.pred pr, 1, %2, pv;\n\tselp.u32 %0, 1, 0, pr;\n\t}"
+        : "=r"(r)
+        : "r"(v ? 1u : 0u), "n"(32 * kSoftWarps)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void soft_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftWarps) : "memory");
 }
 
@@ -235,14 +254,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kStages; ++i) {
             mbar_init(smem_u32(&sm.kfull[i]), 2 * kDecodeWarps);
             mbar_init(smem_u32(&sm.vfull[i]), 2 * kDecodeWarps);
-            mbar_init(smem_u32(&sm.kempty[i]), 1);
+            mbar_init(smem_u32(&sm.sfull[i]), 1);
             mbar_init(smem_u32(&sm.vempty[i]), 1);
         }
         mbar_init(smem_u32(&sm.qfull), 2 * kSoftWarps);
-        mbar_init(smem_u32(&sm.pfull), 2 * kSoftWarps);
-        mbar_init(smem_u32(&sm.sfull[0]), 1);
-        mbar_init(smem_u32(&sm.sfull[1]), 1);
-        mbar_init(smem_u32(&sm.done), 1);
+        mbar_init(smem_u32(&sm.pfull[0]), kSoftWarps);  // half of the warps, on both SMs
+        mbar_init(smem_u32(&sm.pfull[1]), kSoftWarps);
+        mbar_init(smem_u32(&sm.pdone), 1);
+        mbar_init(smem_u32(&sm.sfree[0]), 2 * kSoftWarps);
+        mbar_init(smem_u32(&sm.sfree[1]), 2 * kSoftWarps);
+        mbar_init(smem_u32(&sm.done), 2);  // one commit of each issuing warp
         for (int i = 0; i < kRawK; ++i) {
             mbar_init(smem_u32(&sm.rkfull[i]), 1);
             mbar_init(smem_u32(&sm.rkempty[i]), kDecodeWarps);
@@ -256,7 +277,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         sm.abort = 0;
         fence_mbar_init();
     }
-    if (warp == kMmaWarp) {
+    if (warp == kQkWarp) {
         __syncwarp();
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                          smem_u32(&sm.tmem_base))
@@ -267,74 +288,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncthreads();
     cluster_sync();
     tc_fence_after();
-    const uint32_t tmem = sm.tmem_base;
+    // All 512 columns were allocated, so they start at column 0, lane 0: the addresses below are
+    // constants. (Both SMs of the pair must agree, and always do: an allocation elsewhere would be
+    // a smaller one.)
+    constexpr uint32_t tmem = 0;
 
-    if (warp >= kSoftWarps && warp < kMmaWarp) {
+    if (warp >= kSoftWarps && warp < kQkWarp) {
         // ------------------------------------------------------------------ decoders
         // A lane takes 8 codes (8 bytes) at a time and stores them as one 16-byte unit: loads of a warp
         // are whole rows of codes and the 8 lanes of a store phase fill one 128-byte row, so neither
-        // meets a bank twice. K warp w has keys 16 w + i of this SM's 48, V warp w keys 32 w + 2 i and
-        // 32 w + 2 i + 1 of the tile's 96 (i < 16).
+        // meets a bank twice. K warp w has keys 24 w + n of this SM's 48, V warp w keys 48 w + 2 n and
+        // 48 w + 2 n + 1 of the tile's 96 (n < 24).
         const bool is_k = warp < kSoftWarps + kDecodeWarps;
         const int w = warp - kSoftWarps - (is_k ? 0 : kDecodeWarps);
         uint64_t* full = is_k ? sm.kfull : sm.vfull;
-        uint64_t* empty = is_k ? sm.kempty : sm.vempty;
+        uint64_t* empty = is_k ? sm.sfull : sm.vempty;  // the scores of a tile free its K
         uint64_t* raw_full = is_k ? sm.rkfull : sm.rvfull;
         uint64_t* raw_empty = is_k ? sm.rkempty : sm.rvempty;
         const int raw_stages = is_k ? kRawK : kRawV;
-        const uint8_t* src0 = smem + (is_k ? kOffRawK : kOffRawV) + w * (kRawStage / 3) + 8 * lane;
+        const int own_keys = (is_k ? kHalfKeys : kTile) / kDecodeWarps;  // of a tile
+        const uint8_t* src0 = smem + (is_k ? kOffRawK : kOffRawV) + w * (kRawStage / kDecodeWarps) + 8 * lane;
         const int b = is_k ? 0 : lane >> 4;  // which of a V lane's two keys
         const int group = is_k ? lane : lane & 15;
         uint8_t* dst0 = smem + (is_k ? kOffK : kOffV) +
                         (group >> 3) * ((is_k ? kHalfKeys : kTile) * 128) +
-                        (is_k ? 16 * w : 32 * w + b) * 128;
+                        (w * own_keys + b) * 128;
         const uint32_t unit = (uint32_t)((group & 7) ^ b) << 4;  // swizzled by the key's low bits
         const uint32_t stage_bytes = is_k ? kKStage : kVStage;
+        const int key_shift = is_k ? 0 : 1;
+        constexpr int kRounds = kHalfKeys / kDecodeWarps;  // keys of K, pairs of keys of V
+        static_assert(kRounds % 4 == 0 && kRounds * kDecodeWarps == kHalfKeys, "decoders");
         int rs = 0, rphase = 0;
         bool live = true;
         for (int g = 0; live && seg.next();) {
             for (int i = 0; i < seg.count; ++i, ++g) {
                 const int s = g % kStages;
                 const int j0 = (seg.first + i) * kTile +
-                               (is_k ? (int)rank * kHalfKeys + 16 * w : 32 * w);
+                               (is_k ? (int)rank * kHalfKeys : 0) + w * own_keys;
                 live = ctx.wait_warp(&raw_full[rs], rphase) &&
                        ctx.wait_warp(&empty[s], ((g / kStages) & 1) ^ 1);
                 if (!live) break;
                 const uint8_t* src = src0 + rs * kRawStage;
                 uint8_t* dst = dst0 + s * stage_bytes;
-                // the keys of this warp in 16-key chunks (one of K, two of V); a chunk past the
-                // prefix was not copied, and its keys are zeros
-                const bool live_a = j0 < keys, live_b = is_k ? live_a : j0 + 16 < keys;
-                auto decode = [&](auto is_k_) {
-                    constexpr bool kK = decltype(is_k_)::value;
+                // Keys past the prefix were not copied and become zeros. Four keys (pairs of V) a round,
+                // and the same code for both operands: the roles share the instruction cache, and
+                // straight-line code for each of them was slower.
+                const int live_n = (keys - j0) >> key_shift;
+#pragma unroll 1
+                for (int n0 = 0; n0 < kRounds; n0 += 4) {
+                    uint2 v[4];
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {  // 16 keys of V each, half of K's
-                        auto put = [&](int k, const uint4& f) {
-                            const int r = (8 * hf + k) * (kK ? 1 : 2);  // less the lane's key bit
-                            *reinterpret_cast<uint4*>(dst + r * 128 + (unit ^ ((r & 7) << 4))) = f;
-                        };
-                        if (hf ? live_b : live_a) {
-                            uint2 v[8];
+                    for (int k = 0; k < 4; ++k)
+                        v[k] = *reinterpret_cast<const uint2*>(src + (n0 + k) * 256);
 #pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                v[k] = *reinterpret_cast<const uint2*>(src + (8 * hf + k) * 256);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                uint4 f;
-                                e4m3x4_to_f16x4(v[k].x, f.x, f.y);
-                                e4m3x4_to_f16x4(v[k].y, f.z, f.w);
-                                put(k, f);
-                            }
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) put(k, make_uint4(0, 0, 0, 0));
-                        }
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t r = (n0 + k) << key_shift;  // key, less the lane's own bit
+                        uint4 f;
+                        e4m3x4_to_f16x4(v[k].x, f.x, f.y);
+                        e4m3x4_to_f16x4(v[k].y, f.z, f.w);
+                        if (n0 >= live_n) f = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(dst + r * 128 + (unit ^ ((r & 7) << 4))) = f;
                     }
-                };
-                if (is_k)
-                    decode(std::true_type{});
-                else
-                    decode(std::false_type{});
+                }
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -410,62 +425,85 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             drain(&sm.rkfull[t % kRawK], (t / kRawK) & 1);
         for (int t = max(nv - kRawV, 0); t < nv; ++t)
             drain(&sm.rvfull[t % kRawV], (t / kRawV) & 1);
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kQkWarp || warp == kPvWarp) {
         // ------------------------------------------------------------------ products
-        if (rank == 0 && lane == 0) {
-            const uint32_t idesc_qk = idesc_f32acc(256, kTile, 0, 0, 0, 0);
-            const uint32_t idesc_pv = idesc_f32acc(256, kHeadDim, 0, 0, 0, 1);
-            const uint32_t qb = smem_u32(smem), kb0 = smem_u32(smem + kOffK),
-                           vb0 = smem_u32(smem + kOffV);
-            int g = 0, sidx = 0;
+        // Issuing a product takes its thread about 50 clocks, a commit as long and a wait that is
+        // already over some 80: one thread needed 1700 clocks and more for the products, commits and
+        // waits of a tile whose products run in 1570. So one warp issues the scores and one PV; the
+        // tensor core takes from both. Stages and score buffers go by the tile's parity, a compile-time
+        // constant below: every descriptor is then a constant from the shared-memory base.
+        static_assert(kStages == 2, "a tile's stage is its parity");
+        using Even = std::integral_constant<int, 0>;
+        using Odd = std::integral_constant<int, 1>;
+        if (rank == 0 && lane == 0 && warp == kQkWarp) {
+            constexpr uint32_t idesc = idesc_f32acc(256, kTile, 0, 0, 0, 0);
+            const uint32_t qb = smem_u32(smem), kb = smem_u32(smem + kOffK);
+            int sidx = 0;
             bool ok = true;
-            auto issue_qk = [&](int t) {  // t: tile of the pair's line
-                const int s = t % kStages;
-                ok = ctx.wait(&sm.kfull[s], (t / kStages) & 1);
+            auto tile = [&](auto parity, int t) {
+                constexpr int kS = decltype(parity)::value;
+                // the softmax has read the scores of tile t - 2 out of this buffer
+                ok = ctx.wait(&sm.kfull[kS], (t >> 1) & 1) &&
+                     ctx.wait(&sm.sfree[kS], ((t >> 1) & 1) ^ 1);
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t kb = kb0 + s * kKStage;
-                const uint32_t d = tmem + kColS + (t & 1) * kTile;
 #pragma unroll
                 for (int k = 0; k < kHeadDim / 16; ++k)
-                    mma_ss(d,
+                    mma_ss(kColS + kS * kTile,
                            smem_desc(qb + (k >> 2) * (kRows * 128) + (k & 3) * 32, 16, 1024,
                                      kSwizzle128B),
-                           smem_desc(kb + (k >> 2) * (kHalfKeys * 128) + (k & 3) * 32, 16, 1024,
-                                     kSwizzle128B),
-                           idesc_qk, k > 0);
-                commit_pair(smem_u32(&sm.kempty[s]));
-                commit_pair(smem_u32(&sm.sfull[t & 1]));
+                           smem_desc(kb + kS * kKStage + (k >> 2) * (kHalfKeys * 128) + (k & 3) * 32,
+                                     16, 1024, kSwizzle128B),
+                           idesc, k > 0);
+                commit_pair(smem_u32(&sm.sfull[kS]));
             };
-            while (ok && seg.next()) {
+            for (int t = 0; ok && seg.next(); ++sidx) {
                 ok = ctx.wait(&sm.qfull, sidx & 1);
-                if (ok) issue_qk(g);
-                for (int i = 0; ok && i < seg.count; ++i) {
-                    const int t = g + i, s = t % kStages;
-                    // scores of tile t + 1 take the buffer of t - 1, which the softmax has read: it
-                    // wrote P of t - 1 afterwards, and that was waited for
-                    if (i + 1 < seg.count) issue_qk(t + 1);
-                    ok = ok && ctx.wait(&sm.vfull[s], (t / kStages) & 1) &&
-                         ctx.wait(&sm.pfull, t & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t vb = vb0 + s * kVStage;
-#pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        mma_ts(tmem + kColO, tmem + kColP + 8 * k,
-                               smem_desc(vb + k * 2048, kTile * 128, 1024, kSwizzle128B),
-                               idesc_pv, i > 0 || k > 0);
-                    commit_pair(smem_u32(&sm.vempty[s]));
+                for (int i = 0; ok && i < seg.count; ++i, ++t) {
+                    if (t & 1)
+                        tile(Odd{}, t);
+                    else
+                        tile(Even{}, t);
                 }
-                g += seg.count;
-                ++sidx;
             }
             commit_pair(smem_u32(&sm.done));  // every product issued above
+        } else if (rank == 0 && lane == 0) {
+            constexpr uint32_t idesc = idesc_f32acc(256, kHeadDim, 0, 0, 0, 1);
+            const uint32_t vb = smem_u32(smem + kOffV);
+            bool ok = true;
+            auto tile = [&](auto parity, int t, bool first) {
+                constexpr int kS = decltype(parity)::value;
+                ok = ctx.wait(&sm.vfull[kS], (t >> 1) & 1);
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {  // the two halves of P
+                    ok = ok && ctx.wait(&sm.pfull[hf], t & 1);
+                    if (!ok) return;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 3 * hf; k < 3 * hf + 3; ++k)
+                        mma_ts(kColO, kColP + 8 * k,
+                               smem_desc(vb + kS * kVStage + k * 2048, kTile * 128, 1024,
+                                         kSwizzle128B),
+                               idesc, k > 0 || !first);
+                    commit_pair(smem_u32(hf ? &sm.vempty[kS] : &sm.pdone));
+                }
+            };
+            for (int t = 0; ok && seg.next();) {
+                for (int i = 0; ok && i < seg.count; ++i, ++t) {
+                    if (t & 1)
+                        tile(Odd{}, t, i == 0);
+                    else
+                        tile(Even{}, t, i == 0);
+                }
+            }
+            commit_pair(smem_u32(&sm.done));
         }
     } else {
         // ------------------------------------------------------------------ softmax
-        const int row = tid;  // of this SM's 128 = lane of tensor memory
-        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+        // Warps 0-3 have the first 48 keys of every tile, warps 4-7 the others; both halves of a row
+        // keep the same reference.
+        const int hf = warp >> 2, row = tid & (kRows - 1);  // row of this SM's = tensor-memory lane
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         // D^-1/2 = 1/16, log2 units. Row maxima below are taken before this factor, so it has to be
         // positive: a negative scale's sign goes into Q, a scale of zero becomes a tiny one.
         const float c_signed = __ldg(p.k_scale) * 0.0625f * kLog2e;
@@ -479,20 +517,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int head = seg.unit / p.blocks, blk = seg.unit - head * p.blocks;
             const int row0 = blk * kPairRows + (int)rank * kRows;  // this SM's first row
             const int slot = pair + seg.unit;
-            // Q rows -> swizzled shared memory, 32 rows a warp
-#pragma unroll 8
-            for (int k = 0; k < kRows / kSoftWarps; ++k) {
-                const int r = warp * (kRows / kSoftWarps) + k, rr = row0 + r;
-                uint4 w = make_uint4(0, 0, 0, 0);
-                if (rr < p.rows) {
+            // Q rows -> swizzled shared memory, 16 rows a warp, all loads in flight. The loads are
+            // not conditional (rows past the last read it again): a branch around each would make
+            // them wait for one another.
+            {
+                constexpr int kOwn = kRows / kSoftWarps;
+                int at;  // row of Q that this lane's row of the warp is
+                {
+                    const int rr = min(row0 + warp * kOwn + (lane & (kOwn - 1)), p.rows - 1);
                     const int i = rr / p.group;
-                    const int64_t qrow =
-                        (int64_t)i * p.num_q_heads + head * p.group + (rr - i * p.group);
-                    w = reinterpret_cast<const uint4*>(p.q + qrow * kHeadDim)[lane];
-                    w = make_uint4(w.x ^ q_sign, w.y ^ q_sign, w.z ^ q_sign, w.w ^ q_sign);
+                    at = i * p.num_q_heads + head * p.group + (rr - i * p.group);
                 }
-                *reinterpret_cast<uint4*>(smem + (lane >> 3) * (kRows * 128) + r * 128 +
-                                          (((lane & 7) ^ (r & 7)) << 4)) = w;
+                uint4 w[kOwn];
+#pragma unroll
+                for (int k = 0; k < kOwn; ++k) {
+                    const int qrow = __shfl_sync(0xffffffffu, at, k);
+                    w[k] = reinterpret_cast<const uint4*>(p.q + (int64_t)qrow * kHeadDim)[lane];
+                }
+#pragma unroll
+                for (int k = 0; k < kOwn; ++k) {
+                    const int r = warp * kOwn + k;
+                    const uint32_t keep = row0 + r < p.rows ? 0xffffffffu : 0u;
+                    *reinterpret_cast<uint4*>(smem + (lane >> 3) * (kRows * 128) + r * 128 +
+                                              (((lane & 7) ^ (r & 7)) << 4)) =
+                        make_uint4((w[k].x ^ q_sign) & keep, (w[k].y ^ q_sign) & keep,
+                                   (w[k].z ^ q_sign) & keep, (w[k].w ^ q_sign) & keep);
+                }
             }
             fence_async_smem();
             __syncwarp();
@@ -506,52 +556,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             float nm = INFINITY;  // minus the reference maximum (log2 units); +inf: no key yet
             float lsum = 0.f;
+#pragma unroll 1
             for (int i = 0; i < seg.count; ++i) {
                 const int t = g + i;
-                const int j0 = (seg.first + i) * kTile;
-                const uint32_t s_col = lanes + kColS + (t & 1) * kTile;
-                const bool whole = __all_sync(0xffffffffu, j0 + kTile <= limit);
-                if (alive && !ctx.wait_warp(&sm.sfull[t & 1], (t >> 1) & 1)) alive = false;
-                if (!alive) continue;
+                const int j0 = (seg.first + i) * kTile + hf * kHalfKeys;
+                const uint32_t s_col = lanes + kColS + (t & 1) * kTile + hf * kHalfKeys;
+                if (alive) alive = ctx.wait_warp(&sm.sfull[t & 1], (t >> 1) & 1);
                 tc_fence_after();
-                uint32_t code[kTile / 2];
+                uint32_t code[kHalfKeys / 2];
                 // p = 2^(s c + nm) as FP16 pairs and their FP32 sum, of the unrounded values, in one
                 // pass over the scores
                 auto probabilities = [&](auto whole_) {
                     constexpr bool kWhole = decltype(whole_)::value;
                     const uint64_t nm2 = pk2(nm, nm);
                     uint64_t sum[2] = {0, 0};
-                    uint32_t a[2][16];
-                    tmem_ld16(s_col, a[0]);
+                    uint32_t a[3][16];
 #pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k) {
-                        tmem_ld_wait(a[k & 1]);
-                        if (k + 1 < kTile / 16) tmem_ld16(s_col + 16 * (k + 1), a[(k + 1) & 1]);
+                    for (int k = 0; k < 3; ++k) tmem_ld16(s_col + 16 * k, a[k]);
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) tmem_ld_wait(a[k]);
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
 #pragma unroll
                         for (int q = 0; q < 8; ++q) {
-                            const uint64_t e = fma2(pk2(__uint_as_float(a[k & 1][2 * q]),
-                                                        __uint_as_float(a[k & 1][2 * q + 1])),
+                            const uint64_t e = fma2(pk2(__uint_as_float(a[k][2 * q]),
+                                                        __uint_as_float(a[k][2 * q + 1])),
                                                     c2, nm2);
                             const int j = j0 + 16 * k + 2 * q;
                             const float p0 = kWhole || j < limit ? ex2(lo2(e)) : 0.f;
                             const float p1 = kWhole || j + 1 < limit ? ex2(hi2(e)) : 0.f;
                             sum[q & 1] = add2(sum[q & 1], pk2(p0, p1));
-                            const __half2 h = __floats2half2_rn(p0, p1);
-                            code[8 * k + q] = *reinterpret_cast<const uint32_t*>(&h);
+                            const __half2 x = __floats2half2_rn(p0, p1);
+                            code[8 * k + q] = *reinterpret_cast<const uint32_t*>(&x);
                         }
-                    }
                     sum[0] = add2(sum[0], sum[1]);
                     return lo2(sum[0]) + hi2(sum[0]);
                 };
-                float tsum = INFINITY;
-                if (i > 0) tsum = whole ? probabilities(std::true_type{})
-                                        : probabilities(std::false_type{});
-                // A sum that is too large (or infinite, or not a number) moves the row's reference: no
-                // probability is above its tile's sum, so smaller sums are inside FP16.
-                if (__any_sync(0xffffffffu, !(tsum <= kMaxSum))) {
+                float psum = INFINITY;
+                if (i > 0 && __all_sync(0xffffffffu, j0 + kHalfKeys <= limit))
+                    psum = probabilities(std::true_type{});
+                // A sum that is too large (or infinite, or not a number) moves the reference: no
+                // probability is above its half tile's sum, so smaller sums are inside FP16. The first
+                // tile of a segment and those with keys that some row does not see come here too. All
+                // 256 threads agree (and reach the barriers whatever became of their waits).
+                if (soft_vote(!(psum <= kMaxSum))) {
                     float mx = -INFINITY;
 #pragma unroll 1
-                    for (int k = 0; k < kTile / 16; ++k) {
+                    for (int k = 0; k < 3; ++k) {
                         uint32_t a[16];
                         tmem_ld16(s_col + 16 * k, a);
                         tmem_ld_wait(a);
@@ -559,67 +610,80 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         for (int q = 0; q < 16; ++q)
                             if (j0 + 16 * k + q < limit) mx = fmaxf(mx, __uint_as_float(a[q]));
                     }
+                    sm.part[hf][row] = mx;
+                    soft_sync();
+                    mx = fmaxf(mx, sm.part[hf ^ 1][row]);
                     const float mo = -nm, mn = fmaxf(mo, mx * c);
                     const float alpha = mn == -INFINITY ? 1.f : ex2(mo - mn);
                     nm = -mn;
                     lsum *= alpha;
-                    if (i > 0) {  // O holds the tiles before this one
-                        if (!ctx.wait_warp(&sm.vempty[(t - 1) % kStages], ((t - 1) / kStages) & 1)) {
-                            alive = false;
-                            continue;
-                        }
+                    if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                        // O holds the tiles before this one, once their products are done: this
+                        // half's columns
+                        if (alive)
+                            alive = ctx.wait_warp(&sm.vempty[(t - 1) & 1], ((t - 1) >> 1) & 1);
                         tc_fence_after();
+                        if (alive) {
 #pragma unroll 1
-                        for (int k = 0; k < kHeadDim / 16; ++k) {
-                            uint32_t o[16];
-                            tmem_ld16(lanes + kColO + 16 * k, o);
-                            tmem_ld_wait(o);
+                            for (int k = 0; k < 8; ++k) {
+                                const uint32_t col = lanes + kColO + hf * 128 + 16 * k;
+                                uint32_t o[16];
+                                tmem_ld16(col, o);
+                                tmem_ld_wait(o);
 #pragma unroll
-                            for (int q = 0; q < 16; ++q)
-                                o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
-                            tmem_st16(lanes + kColO + 16 * k, o);
+                                for (int q = 0; q < 16; ++q)
+                                    o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
+                                tmem_st16(col, o);
+                            }
+                            tmem_st_wait();
                         }
-                        tmem_st_wait();
                     }
-                    tsum = probabilities(std::false_type{});
+                    psum = probabilities(std::false_type{});
+                    // O is rescaled as a whole, and part read, before P of either half is handed over
+                    tc_fence_before();
+                    soft_sync();
+                    tc_fence_after();
                 }
-                lsum += tsum;
-                // P of tile t - 1 has been read once its PV is done
-                if (i > 0 &&
-                    !ctx.wait_warp(&sm.vempty[(t - 1) % kStages], ((t - 1) / kStages) & 1)) {
-                    alive = false;
-                    continue;
-                }
+                lsum += psum;
+                // this half of P is free once the products that read it in tile t - 1 are done
+                if (alive && i > 0)
+                    alive = hf ? ctx.wait_warp(&sm.vempty[(t - 1) & 1], ((t - 1) >> 1) & 1)
+                               : ctx.wait_warp(&sm.pdone, (t - 1) & 1);
+                if (!alive) continue;
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k) tmem_st8(lanes + kColP + 8 * k, code + 8 * k);
+                for (int k = 0; k < 3; ++k)
+                    tmem_st8(lanes + kColP + hf * (kHalfKeys / 2) + 8 * k, code + 8 * k);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_leader(smem_u32(&sm.pfull));
+                if (lane == 0) {
+                    arrive_leader(smem_u32(&sm.pfull[hf]));
+                    arrive_leader(smem_u32(&sm.sfree[t & 1]));  // scores are read
+                }
             }
             g += seg.count;
-            // ---- the segment's split state: (m, l), then the numerator through this warp's 16 KB
-            // of the Q area (no product reads Q any more), so that rows are stored whole
-            if (alive && !ctx.wait_warp(&sm.vempty[(g - 1) % kStages], ((g - 1) / kStages) & 1))
-                alive = false;
-            soft_sync();  // the last scores are complete for every warp: the Q area is free
+            // ---- the segment's split state: (m, l), then the numerator through this warp's 8 KB of
+            // the Q area (no product reads Q any more), so that rows are stored whole
+            if (alive) alive = ctx.wait_warp(&sm.vempty[(g - 1) & 1], ((g - 1) >> 1) & 1);
+            sm.part[hf][row] = lsum;
+            soft_sync();  // (also: the last scores are complete for every warp, the Q area is free)
             if (alive) {
                 tc_fence_after();
-                if (row0 + row < p.rows)
+                if (hf == 0 && row0 + row < p.rows)
                     p.ws_state[(int64_t)slot * kPairRows + rank * kRows + row] =
-                        make_float2(-nm, lsum);
-                float4* stage = reinterpret_cast<float4*>(smem + warp * 16384);
+                        make_float2(-nm, lsum + sm.part[1][row]);
+                float4* stage = reinterpret_cast<float4*>(smem + warp * 8192);
 #pragma unroll 1
-                for (int part = 0; part < 2; ++part) {  // 128 columns each
-#pragma unroll 1
-                    for (int k = 0; k < 8; ++k) {
+                for (int part = 0; part < 2; ++part) {  // 64 of this half's 128 columns each
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
                         uint32_t o[16];
-                        tmem_ld16(lanes + kColO + part * 128 + 16 * k, o);
+                        tmem_ld16(lanes + kColO + hf * 128 + part * 64 + 16 * k, o);
                         tmem_ld_wait(o);
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            stage[lane * 32 + ((4 * k + q) ^ lane)] =
+                            stage[lane * 16 + ((4 * k + q) ^ (lane & 15))] =
                                 make_float4(__uint_as_float(o[4 * q]) * vs,
                                             __uint_as_float(o[4 * q + 1]) * vs,
                                             __uint_as_float(o[4 * q + 2]) * vs,
@@ -627,26 +691,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();
 #pragma unroll 8
-                    for (int r = 0; r < 32; ++r) {
-                        const int rr = warp * 32 + r;
+                    for (int r2 = 0; r2 < 16; ++r2) {
+                        const int r = 2 * r2 + (lane >> 4), cc = lane & 15;
+                        const int rr = (warp & 3) * 32 + r;
                         if (row0 + rr < p.rows)
                             reinterpret_cast<float4*>(
                                 p.ws_acc + ((int64_t)slot * kPairRows + rank * kRows + rr) *
-                                               kHeadDim)[part * 32 + lane] =
-                                stage[r * 32 + (lane ^ r)];
+                                               kHeadDim)[hf * 32 + part * 16 + cc] =
+                                stage[r * 16 + (cc ^ (r & 15))];
                     }
                     __syncwarp();
                 }
             }
             tc_fence_before();
-            soft_sync();  // every warp is through with the Q area
+            soft_sync();  // every warp is through with the Q area and part
         }
         if (alive) ctx.wait_warp(&sm.done, 0);
     }
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // neither SM leaves while the other may still arrive here or read here
-    if (warp == kMmaWarp) {
+    if (warp == kQkWarp) {
         __syncwarp();
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem)
