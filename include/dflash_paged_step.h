@@ -238,6 +238,7 @@ typedef struct {
     dflash_verify_attn_plan_t suffix; /* the sequences' own keys: its workspace part comes first */
     size_t ws_prefix_state_offset;    /* float2 (m, l) [prefix_slots, prefix_slot_rows] */
     size_t ws_prefix_acc_offset;      /* float [prefix_slots, prefix_slot_rows, head_dim] */
+    size_t ws_unit_offset;            /* int4 [batch, Hkv]: split slots of the own keys */
     size_t workspace_bytes;
     dflash_prefix_attn_problem problem;
 } dflash_prefix_attn_plan_t;

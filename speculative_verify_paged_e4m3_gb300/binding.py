@@ -122,6 +122,7 @@ class PrefixAttnPlan(ctypes.Structure):
         ("suffix", Plan),
         ("ws_prefix_state_offset", ctypes.c_size_t),
         ("ws_prefix_acc_offset", ctypes.c_size_t),
+        ("ws_unit_offset", ctypes.c_size_t),
         ("workspace_bytes", ctypes.c_size_t),
         ("problem", PrefixAttnProblem),
     ]

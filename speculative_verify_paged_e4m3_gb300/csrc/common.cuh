@@ -49,6 +49,7 @@ struct PartialParams {
     int max_prefix;             // bound of *prefix_len
     int batch_q_len;            // View::kPrefix: tokens per sequence (q_len is the batch's total)
     int batch_max_context;      // View::kPrefix: bound of context_lens (max_context: max_prefix)
+    int4* unit_slots;           // View::kSuffix: each unit's (first slot, slots, keys) for the combine
 };
 
 enum class View { kWhole, kSuffix, kPrefix };

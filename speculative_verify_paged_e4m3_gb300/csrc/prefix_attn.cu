@@ -27,6 +27,7 @@ namespace {
 constexpr int kMaxBatch = 4096;
 constexpr int kMinSplitKeys = 256;
 constexpr int kPairsFromRows = 400;
+constexpr int kLongOwn = 2048;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -35,37 +36,45 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 struct PrefixCombineParams {
     const float2 *own_state, *pre_state;
     const float *own_acc, *pre_acc;
+    const int4* unit_slots;  // of the own keys, by the split kernel (tc_partial.cu)
     const int32_t *context_lens, *prefix_len;
     __half* out;
     float* lse;
-    int batch, q_len, num_q_heads, num_kv_heads, group, rows, page_size;
+    int total_rows;  // batch * q_len * num_q_heads
+    int q_len, num_q_heads, num_kv_heads, group, rows, page_size;
     int max_context, max_prefix;
-    int own_splits, own_slots;   // the suffix plan's num_splits and num_slots
-    int pre_splits, pre_rows;    // prefix: splits per KV head, rows of the whole batch
-    int pre_blocks, pre_pairs;   // pair kernel: row blocks per KV head, pairs of SMs (else 0)
+    int pre_splits, pre_rows;   // prefix: splits per KV head, rows of the whole batch
+    int pre_blocks, pre_pairs;  // pair kernel: row blocks per KV head, pairs of SMs (else 0)
 };
 
-constexpr int kRowCols = kHeadDim / 4;                   // 64 float4 columns per row
-constexpr int kRowsPerCta = kCombineThreads / kRowCols;  // 4
+constexpr int kMergeWarps = 8;
 
-// One CTA per four rows of a (sequence, KV head) unit, a thread per float4 column of a row: the
-// maximum over both parts' splits, then one weighted sum, as combine_rows_kernel does it.
-__global__ void __launch_bounds__(kCombineThreads)
+// One warp per query row, 8 columns a lane. The row's split states are read a lane each (so that their
+// loads overlap, whatever their number), the maximum and the weights follow by shuffles, then every
+// split's numerator is added in split order: prefix first. Bound by the latency of three dependent
+// loads for few rows, by L2 for many (4 KB of state a row and split).
+__global__ void __launch_bounds__(32 * kMergeWarps)
     prefix_combine_kernel(const PrefixCombineParams p) {
-    const int unit = blockIdx.x, b = unit / p.num_kv_heads, h = unit % p.num_kv_heads;
-    const int r = blockIdx.y * kRowsPerCta + threadIdx.x / kRowCols;
-    const int col = threadIdx.x % kRowCols;
+    griddep_wait();  // both kernels before this one are complete (the split kernel waited for the other)
+    const int orow = blockIdx.x * kMergeWarps + threadIdx.x / 32, lane = threadIdx.x & 31;
+    if (orow >= p.total_rows) return;
+    const int token = orow / p.num_q_heads, hq = orow - token * p.num_q_heads;
+    const int b = token / p.q_len, h = hq / p.group;
+    const int r = (token - b * p.q_len) * p.group + (hq - h * p.group);  // of its (sequence, KV head)
     int unused = 0;
     const int base = p.max_prefix > 0
                          ? shared_keys(p.prefix_len, p.max_prefix, p.page_size, &unused)
                          : 0;
-    const UnitSlots us = locate_slots(p.context_lens, p.batch, p.num_kv_heads, p.own_splits,
-                                      p.own_slots, p.max_context, p.q_len, unit, false, base);
-    if (r >= p.rows) return;  // whole warps: a row is two warps
-    // own keys: slots [us.first, + own_active) of p.rows rows, this row at r
-    const int own_n = us.count > 0 ? us.n : 0;
-    const int own_per = own_n > 0 ? keys_per_split(own_n, us.count, 128, kMinSplitKeys) : 1;
-    const int own_active = own_n > 0 ? (own_n + own_per - 1) / own_per : 0;
+    const int ctx = min(p.context_lens[b], p.max_context);
+    // own keys: own_active states, rows apart from own0 on
+    int own_active = 0;
+    int64_t own0 = 0;
+    if (ctx > base) {
+        const int4 us = p.unit_slots[b * p.num_kv_heads + h];
+        const int per = keys_per_split(us.z, us.y, 128, kMinSplitKeys);
+        own_active = (us.z + per - 1) / per;
+        own0 = (int64_t)us.x * p.rows + r;
+    }
     // prefix: pre_active states, pre_step rows apart from pre0 on
     const int prow = b * p.rows + r;  // row of the whole batch
     int pre_active = 0, pre_step = p.pre_rows;
@@ -73,7 +82,7 @@ __global__ void __launch_bounds__(kCombineThreads)
     if (base > 0 && p.pre_pairs > 0) {  // the segments of this row's block, in slots pair + unit
         const PairShare share = pair_share(base, p.pre_blocks * p.num_kv_heads, p.pre_pairs);
         const int pu = h * p.pre_blocks + prow / kPairRows;
-        const int64_t t0 = (int64_t)pu * share.tiles;
+        const int64_t t0 = pu * share.pitch;
         const int first = (int)(t0 / share.per_pair);
         pre_active = (int)((t0 + share.tiles - 1) / share.per_pair) - first + 1;
         pre_step = kPairRows;
@@ -83,56 +92,57 @@ __global__ void __launch_bounds__(kCombineThreads)
         pre_active = (base + per - 1) / per;
         pre0 = (int64_t)h * p.pre_splits * p.pre_rows + prow;
     }
-    const int64_t own0 = (int64_t)us.first * p.rows + r;
     const int total = pre_active + own_active;
-    auto state_at = [&](int s) {
-        return s < pre_active ? p.pre_state + pre0 + (int64_t)s * pre_step
-                              : p.own_state + own0 + (int64_t)(s - pre_active) * p.rows;
+    auto state_of = [&](int s) {  // split s: past the end, no weight
+        if (s >= total) return make_float2(-INFINITY, 0.f);
+        return __ldcg(s < pre_active ? p.pre_state + pre0 + (int64_t)s * pre_step
+                                     : p.own_state + own0 + (int64_t)(s - pre_active) * p.rows);
     };
-    auto acc_at = [&](int s) {
-        const float* a = s < pre_active
-                             ? p.pre_acc + (pre0 + (int64_t)s * pre_step) * kHeadDim
-                             : p.own_acc + (own0 + (int64_t)(s - pre_active) * p.rows) * kHeadDim;
-        return reinterpret_cast<const float4*>(a) + col;
-    };
-    float M = -INFINITY;
-    for (int s = 0; s < total; ++s) M = fmaxf(M, __ldcg(state_at(s)).x);
-    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float2 st0 = state_of(lane);
+    float M = st0.x;
+    for (int s = 32 + lane; s < total; s += 32) M = fmaxf(M, state_of(s).x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float4 t0 = make_float4(0.f, 0.f, 0.f, 0.f), t1 = t0;
     float L = 0.f;
     if (M != -INFINITY) {
-        constexpr int kLoads = 8;  // splits whose loads are in flight together
-        for (int s0 = 0; s0 < total; s0 += kLoads) {
-            float2 st[kLoads];
-            float4 a[kLoads];
-#pragma unroll
-            for (int k = 0; k < kLoads; ++k) {
-                const int s = min(s0 + k, total - 1);
-                st[k] = __ldcg(state_at(s));
-                a[k] = __ldcg(acc_at(s));
-            }
-#pragma unroll
-            for (int k = 0; k < kLoads; ++k) {
-                if (s0 + k >= total) break;
-                const float w = st[k].x == -INFINITY ? 0.f : merge_ex2(st[k].x - M);
-                t.x = fmaf(w, a[k].x, t.x);
-                t.y = fmaf(w, a[k].y, t.y);
-                t.z = fmaf(w, a[k].z, t.z);
-                t.w = fmaf(w, a[k].w, t.w);
-                L = fmaf(w, st[k].y, L);
+        for (int s0 = 0; s0 < total; s0 += 32) {
+            const float2 st = s0 == 0 ? st0 : state_of(s0 + lane);
+            const float w = st.x == -INFINITY ? 0.f : merge_ex2(st.x - M);
+            L = fmaf(w, st.y, L);
+            const int n = min(total - s0, 32);
+#pragma unroll 4
+            for (int k = 0; k < n; ++k) {
+                const int s = s0 + k;
+                const float wk = __shfl_sync(0xffffffffu, w, k);
+                const float* a = s < pre_active
+                                     ? p.pre_acc + (pre0 + (int64_t)s * pre_step) * kHeadDim
+                                     : p.own_acc +
+                                           (own0 + (int64_t)(s - pre_active) * p.rows) * kHeadDim;
+                const float4 a0 = __ldcg(reinterpret_cast<const float4*>(a) + lane);
+                const float4 a1 = __ldcg(reinterpret_cast<const float4*>(a) + 32 + lane);
+                t0.x = fmaf(wk, a0.x, t0.x);
+                t0.y = fmaf(wk, a0.y, t0.y);
+                t0.z = fmaf(wk, a0.z, t0.z);
+                t0.w = fmaf(wk, a0.w, t0.w);
+                t1.x = fmaf(wk, a1.x, t1.x);
+                t1.y = fmaf(wk, a1.y, t1.y);
+                t1.z = fmaf(wk, a1.z, t1.z);
+                t1.w = fmaf(wk, a1.w, t1.w);
             }
         }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
         const float inv = 1.f / L;
-        t.x *= inv;
-        t.y *= inv;
-        t.z *= inv;
-        t.w *= inv;
+        t0 = make_float4(t0.x * inv, t0.y * inv, t0.z * inv, t0.w * inv);
+        t1 = make_float4(t1.x * inv, t1.y * inv, t1.z * inv, t1.w * inv);
     }
-    const int i = r / p.group, g = r % p.group;
-    const int64_t orow = ((int64_t)b * p.q_len + i) * p.num_q_heads + h * p.group + g;
-    __half2* out2 = reinterpret_cast<__half2*>(p.out + orow * kHeadDim + col * 4);
-    out2[0] = __floats2half2_rn(t.x, t.y);
-    out2[1] = __floats2half2_rn(t.z, t.w);
-    if (col == 0) p.lse[orow] = (M == -INFINITY) ? -INFINITY : (M + log2f(L)) * kLn2;
+    __half2* out2 = reinterpret_cast<__half2*>(p.out + (int64_t)orow * kHeadDim);
+    out2[2 * lane] = __floats2half2_rn(t0.x, t0.y);
+    out2[2 * lane + 1] = __floats2half2_rn(t0.z, t0.w);
+    out2[64 + 2 * lane] = __floats2half2_rn(t1.x, t1.y);
+    out2[64 + 2 * lane + 1] = __floats2half2_rn(t1.z, t1.w);
+    if (lane == 0) p.lse[orow] = (M == -INFINITY) ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 // The plan that a problem has; a plan handed to forward must be the same bytes.
@@ -160,6 +170,23 @@ int make_plan(const dflash_prefix_attn_problem* pr, dflash_prefix_attn_plan_t* p
     own.kernel = DFLASH_KERNEL_TCGEN05;
     const int rc = dflash_verify_attn_plan(&own, &plan->suffix);
     if (rc != DFLASH_OK) return rc;
+    // With about as many units as SMs a slot per SM leaves the longest sequences unsplit: two of
+    // them per SM instead, where they may be long (40 sequences of up to 4000 keys and 4 KV heads on
+    // 152 SMs: the longest 32 tiles, then 12, and 13 us less in all; for up to 1000 keys a second
+    // CTA's start costs more than that, 4 us).
+    if (pr->batch > 1 && pr->max_context - pr->max_prefix >= kLongOwn &&
+        2 * (int64_t)pr->batch * pr->num_kv_heads > plan->suffix.sm_count) {
+        dflash_verify_attn_plan_t& sp = plan->suffix;
+        const int64_t most =
+            (int64_t)pr->batch * pr->num_kv_heads * ceil_div(pr->max_context, kMinSplitKeys);
+        int64_t slots = 2 * (int64_t)sp.sm_count / sp.row_blocks;
+        if (slots > most) slots = most;
+        if (slots > sp.num_slots) sp.num_slots = (int32_t)slots;
+        sp.ws_acc_offset =
+            sp.ws_state_offset + align_up((size_t)sp.num_slots * sp.rows * sizeof(float2), 256);
+        sp.workspace_bytes =
+            sp.ws_acc_offset + (size_t)sp.num_slots * sp.rows * kHeadDim * sizeof(float);
+    }
     if (pr->batch > kMaxBatch) return DFLASH_ERR_UNSUPPORTED;
     plan->version = DFLASH_PAGED_STEP_VERSION;
     plan->sm_count = plan->suffix.sm_count;
@@ -195,7 +222,9 @@ int make_plan(const dflash_prefix_attn_problem* pr, dflash_prefix_attn_plan_t* p
     plan->ws_prefix_state_offset = align_up(plan->suffix.workspace_bytes, 256);
     plan->ws_prefix_acc_offset =
         plan->ws_prefix_state_offset + align_up(states * sizeof(float2), 256);
-    plan->workspace_bytes = plan->ws_prefix_acc_offset + states * kHeadDim * sizeof(float);
+    plan->ws_unit_offset = plan->ws_prefix_acc_offset + states * kHeadDim * sizeof(float);
+    plan->workspace_bytes =
+        plan->ws_unit_offset + (size_t)pr->batch * pr->num_kv_heads * sizeof(int4);
     plan->problem = *pr;
     return DFLASH_OK;
 }
@@ -261,7 +290,8 @@ int dflash_prefix_attn_forward(const dflash_prefix_attn_plan_t* plan, const void
     for (int s = 0; s < 31; ++s)
         if (pr.page_size == (1 << s)) p.page_shift = s;
     p.max_prefix = pr.max_prefix;
-    p.prefix_len = prefix_len;
+    p.prefix_len = prefix ? prefix_len : nullptr;
+    p.unit_slots = reinterpret_cast<int4*>(ws + plan->ws_unit_offset);
     cudaError_t e = cudaSuccess;
     const bool by_pairs = plan->prefix_kernel == DFLASH_PREFIX_KERNEL_PAIRS;
     if (prefix && by_pairs) {
@@ -320,7 +350,10 @@ int dflash_prefix_attn_forward(const dflash_prefix_attn_plan_t* plan, const void
         p.max_context = pr.max_context;
         p.num_splits = own.num_splits;
         p.num_slots = own.num_slots;
-        e = launch_tc_partial(p, stream, prefix ? View::kSuffix : View::kWhole);
+        // It needs nothing of the prefix kernel and so may start beside its last CTAs (that kernel, an
+        // ordinary launch, has itself waited for everything before this call).
+        p.pdl = prefix ? 1 : 0;
+        e = launch_tc_partial(p, stream, View::kSuffix);
     }
     if (e == cudaSuccess) {
         PrefixCombineParams c;
@@ -332,7 +365,8 @@ int dflash_prefix_attn_forward(const dflash_prefix_attn_plan_t* plan, const void
         c.prefix_len = prefix_len;
         c.out = static_cast<__half*>(out);
         c.lse = lse;
-        c.batch = pr.batch;
+        c.unit_slots = p.unit_slots;
+        c.total_rows = pr.batch * pr.q_len * pr.num_q_heads;
         c.q_len = pr.q_len;
         c.num_q_heads = pr.num_q_heads;
         c.num_kv_heads = pr.num_kv_heads;
@@ -341,14 +375,22 @@ int dflash_prefix_attn_forward(const dflash_prefix_attn_plan_t* plan, const void
         c.page_size = pr.page_size;
         c.max_context = pr.max_context;
         c.max_prefix = pr.max_prefix;
-        c.own_splits = own.num_splits;
-        c.own_slots = own.num_slots;
         c.pre_splits = plan->prefix_splits;
         c.pre_rows = plan->prefix_rows;
         c.pre_blocks = plan->prefix_row_blocks;
         c.pre_pairs = by_pairs ? plan->prefix_splits : 0;
-        const dim3 grid(pr.batch * pr.num_kv_heads, (own.rows + kRowsPerCta - 1) / kRowsPerCta);
-        prefix_combine_kernel<<<grid, kCombineThreads, 0, stream>>>(c);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((c.total_rows + kMergeWarps - 1) / kMergeWarps);
+        cfg.blockDim = dim3(32 * kMergeWarps);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, prefix_combine_kernel, c);
+    }
+    if (e == cudaSuccess) {
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) {

@@ -21,13 +21,13 @@
 //  * Warps: 0-7 softmax (thread = row, warps 0-3 the tile's first 48 keys, 4-7 the others), 8-9 decode
 //    K, 10-11 decode V, 12 issues the score products of the pair and 13 its PV (one thread each, in
 //    the leader SM alone), 14 copies the codes (TMA, three tiles of K and two of V ahead).
-//  * Probabilities are p = 2^(score - m) for a reference maximum m that is the first tile's, and moves
-//    only when a row's probabilities of 48 keys sum to more than 2^15 (so that all are inside FP16):
-//    scores, exponentials and sums are one pass with no maximum in front of it. When it moves, the
-//    rows' O columns are rescaled in place and the 48 keys are done again; peaked scores should rarely
-//    get there (with m shifted by 2^-7 they did in most tiles: 177 us for 16 x 8 tokens over 32768).
-//    Below 2^-14 FP16 has a fixed grid, 2^-24 of the reference: noise of 2^-25 a key beside a sum of
-//    at least one.
+//  * Probabilities are p = 2^(score - m) for a reference m that is set 2^4 above the first tile's
+//    maximum, and moves only when a row's probabilities of 48 keys sum to more than 2^15 (so that all
+//    are inside FP16): scores, exponentials and sums are one pass with no maximum in front of it. When
+//    it moves, the rows' O columns are rescaled in place and the tile is done again, which stalls the
+//    pair for more than a tile; with scores of spread 4 over 5 % of the keys the first tile's maximum
+//    alone was passed in most tiles. Below 2^-14 FP16 has a fixed grid of 2^-24: noise of 2^-25 a key
+//    beside a sum of at least 2^-4, 2^-13 of it at worst over 2^17 keys.
 //  * Pairs take equal shares of all (KV head, row block) units' tiles (prefix_pairs.cuh); a share may
 //    end in the middle of a unit, the combine puts the parts together.
 //  * Every wait is bounded (200 ms, then DFLASH_FLAG_KERNEL_TIMEOUT and a clean exit); both SMs of
@@ -59,6 +59,7 @@ constexpr int kQkWarp = kSoftWarps + 2 * kDecodeWarps, kPvWarp = kQkWarp + 1;
 constexpr int kCopyWarp = kPvWarp + 1;
 constexpr int kThreads = 32 * (kCopyWarp + 1);  // 15 warps: 128 registers a thread
 constexpr uint64_t kWaitLimitNs = 200ull * 1000 * 1000;
+constexpr float kHeadroom = 4.f;    // a reference is set 2^4 above the maximum that moves it
 constexpr float kMaxSum = 32768.f;  // a row's probabilities of a half tile sum to this at most
 
 // Shared memory: Q | K stages | V stages | codes of K | codes of V | Small. All operands are 128-byte swizzled: Q and K
@@ -100,9 +101,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::
-                     : "memory");
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 // Arrive on the barrier at the same place in the leader's shared memory. What the arrival orders are
 // operands of the products (tensor memory, and shared memory through the async proxy), which the fences
@@ -208,24 +211,33 @@ __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
     }
 }
 
+// Keys [0, limit) of the prefix are visible to row rr of the batch.
+__device__ __forceinline__ int row_limit(const PrefixPairsParams& p, int rr, int keys) {
+    const int i = rr / p.group, b = i / p.q_len;
+    const int ctx_len = min(p.context_lens[b], p.max_context);
+    return min(keys, ctx_len - p.q_len + (i - b * p.q_len) + 1);
+}
+
 // The segments of a pair, in order: every role walks the same list.
 struct Segments {
     int64_t at, end;  // tiles of the line still to do
-    int tiles;        // per unit
+    int64_t pitch;
+    int tiles;  // per unit
     int unit, first, count;  // the current segment: its unit, first tile, tile count
     __device__ Segments(const PairShare& s, int pair, int units) {
-        const int64_t total = (int64_t)units * s.tiles;
+        const int64_t total = units * s.pitch;
+        pitch = s.pitch;
         tiles = s.tiles;
         at = pair * s.per_pair;
         end = at + s.per_pair < total ? at + s.per_pair : total;
     }
     __device__ bool next() {
         if (at >= end) return false;
-        unit = (int)(at / tiles);
-        first = (int)(at - (int64_t)unit * tiles);
+        unit = (int)(at / pitch);
+        first = (int)(at - unit * pitch);  // < tiles: a unit's empty end is shorter than a share
         const int64_t left = end - at;
         count = left < tiles - first ? (int)left : tiles - first;
-        at += count;
+        at = unit * pitch + first + count == unit * pitch + tiles ? (unit + 1) * pitch : at + count;
         return true;
     }
 };
@@ -242,7 +254,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int keys = shared_keys(p.prefix_len, p.max_prefix, p.page_size, &flags);
     if (flags && blockIdx.x == 0 && tid == 0) atomicOr(p.status, flags);
     const PairShare share = pair_share(keys, p.units, p.pairs);
-    if (pair * share.per_pair >= (int64_t)p.units * share.tiles) return;  // both SMs agree
+    // the next kernel on the stream may be launched beside this one's last CTAs
+    griddep_launch_dependents();
+    if (pair * share.per_pair >= p.units * share.pitch) return;  // both SMs agree
     if (smem_u32(smem) & 1023u) {  // the swizzled layouts need a 1 KB aligned base
         if (tid == 0) atomicOr(p.status, DFLASH_FLAG_KERNEL_TIMEOUT);
         return;
@@ -264,18 +278,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&sm.sfree[0]), 2 * kSoftWarps);
         mbar_init(smem_u32(&sm.sfree[1]), 2 * kSoftWarps);
         mbar_init(smem_u32(&sm.done), 2);  // one commit of each issuing warp
-        for (int i = 0; i < kRawK; ++i) {
-            mbar_init(smem_u32(&sm.rkfull[i]), 1);
-            mbar_init(smem_u32(&sm.rkempty[i]), kDecodeWarps);
-        }
-        for (int i = 0; i < kRawV; ++i) {
-            mbar_init(smem_u32(&sm.rvfull[i]), 1);
-            mbar_init(smem_u32(&sm.rvempty[i]), kDecodeWarps);
-        }
-        prefetch_tensormap(&kmap);
-        prefetch_tensormap(&vmap);
-        sm.abort = 0;
         fence_mbar_init();
+    }
+    if (warp == kCopyWarp) {
+        // the copies touch this SM alone: they start before the pair has met
+        if (lane == 0) {
+            prefetch_tensormap(&kmap);
+            prefetch_tensormap(&vmap);
+            for (int i = 0; i < kRawK; ++i) {
+                mbar_init(smem_u32(&sm.rkfull[i]), 1);
+                mbar_init(smem_u32(&sm.rkempty[i]), kDecodeWarps);
+            }
+            for (int i = 0; i < kRawV; ++i) {
+                mbar_init(smem_u32(&sm.rvfull[i]), 1);
+                mbar_init(smem_u32(&sm.rvempty[i]), kDecodeWarps);
+            }
+            sm.abort = 0;
+            fence_mbar_init();
+        }
+        __syncwarp();
     }
     if (warp == kQkWarp) {
         __syncwarp();
@@ -285,8 +306,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
-    __syncthreads();
-    cluster_sync();
+    if (warp == kCopyWarp) {  // arrives, and waits for the pair at the kernel's end only
+        asm volatile("bar.arrive 2, %0;" ::"n"(kThreads) : "memory");
+        cluster_arrive();
+    } else {
+        asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory");
+        cluster_arrive();
+        cluster_wait();
+    }
     tc_fence_after();
     // All 512 columns were allocated, so they start at column 0, lane 0: the addresses below are
     // constants. (Both SMs of the pair must agree, and always do: an allocation elsewhere would be
@@ -522,12 +549,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // them wait for one another.
             {
                 constexpr int kOwn = kRows / kSoftWarps;
-                int at;  // row of Q that this lane's row of the warp is
+                // row of Q that this lane's row of the warp is; a row that sees no key (a padded
+                // slot of the batch may hold anything) becomes zeros, like those past the last
+                int at;
+                bool live;
                 {
-                    const int rr = min(row0 + warp * kOwn + (lane & (kOwn - 1)), p.rows - 1);
-                    const int i = rr / p.group;
-                    at = i * p.num_q_heads + head * p.group + (rr - i * p.group);
+                    const int rr = row0 + warp * kOwn + (lane & (kOwn - 1));
+                    const int rc = min(rr, p.rows - 1), i = rc / p.group;
+                    at = i * p.num_q_heads + head * p.group + (rc - i * p.group);
+                    live = rr < p.rows && row_limit(p, rc, keys) > 0;
                 }
+                const uint32_t live_rows = __ballot_sync(0xffffffffu, live);
                 uint4 w[kOwn];
 #pragma unroll
                 for (int k = 0; k < kOwn; ++k) {
@@ -537,7 +569,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < kOwn; ++k) {
                     const int r = warp * kOwn + k;
-                    const uint32_t keep = row0 + r < p.rows ? 0xffffffffu : 0u;
+                    const uint32_t keep = (live_rows >> k) & 1 ? 0xffffffffu : 0u;
                     *reinterpret_cast<uint4*>(smem + (lane >> 3) * (kRows * 128) + r * 128 +
                                               (((lane & 7) ^ (r & 7)) << 4)) =
                         make_uint4((w[k].x ^ q_sign) & keep, (w[k].y ^ q_sign) & keep,
@@ -548,12 +580,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) arrive_leader(smem_u32(&sm.qfull));
             // keys [0, limit) are visible to this thread's row
-            int limit = keys;
-            if (row0 + row < p.rows) {
-                const int i = (row0 + row) / p.group, b = i / p.q_len;
-                const int ctx_len = min(p.context_lens[b], p.max_context);
-                limit = min(limit, ctx_len - p.q_len + (i - b * p.q_len) + 1);
-            }
+            const int limit = row0 + row < p.rows ? row_limit(p, row0 + row, keys) : keys;
             float nm = INFINITY;  // minus the reference maximum (log2 units); +inf: no key yet
             float lsum = 0.f;
 #pragma unroll 1
@@ -567,8 +594,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // p = 2^(s c + nm) as FP16 pairs and their FP32 sum, of the unrounded values, in one
                 // pass over the scores
                 auto probabilities = [&](auto whole_) {
+                    // whole: the row sees all of these keys, or none (then all are 2^-inf)
                     constexpr bool kWhole = decltype(whole_)::value;
-                    const uint64_t nm2 = pk2(nm, nm);
+                    const float nmr = kWhole && j0 >= limit ? -INFINITY : nm;
+                    const uint64_t nm2 = pk2(nmr, nmr);
                     uint64_t sum[2] = {0, 0};
                     uint32_t a[3][16];
 #pragma unroll
@@ -593,7 +622,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     return lo2(sum[0]) + hi2(sum[0]);
                 };
                 float psum = INFINITY;
-                if (i > 0 && __all_sync(0xffffffffu, j0 + kHalfKeys <= limit))
+                if (i > 0 && __all_sync(0xffffffffu, j0 + kHalfKeys <= limit || j0 >= limit))
                     psum = probabilities(std::true_type{});
                 // A sum that is too large (or infinite, or not a number) moves the reference: no
                 // probability is above its half tile's sum, so smaller sums are inside FP16. The first
@@ -613,7 +642,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     sm.part[hf][row] = mx;
                     soft_sync();
                     mx = fmaxf(mx, sm.part[hf ^ 1][row]);
-                    const float mo = -nm, mn = fmaxf(mo, mx * c);
+                    mx *= c;
+                    // (48 keys that sum to over 2^15 have one above 2^9)
+                    const float mo = -nm, mn = mx > mo + 9.f ? mx + kHeadroom : mo;
                     const float alpha = mn == -INFINITY ? 1.f : ex2(mo - mn);
                     nm = -mn;
                     lsum *= alpha;
@@ -710,7 +741,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();  // neither SM leaves while the other may still arrive here or read here
+    if (warp == kCopyWarp) cluster_wait();  // of the start
+    cluster_arrive();
+    cluster_wait();  // neither SM leaves while the other may still arrive here or read here
     if (warp == kQkWarp) {
         __syncwarp();
         tc_fence_after();

@@ -374,7 +374,9 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     int base = 0, view_flags = 0;
     const int32_t* table = p.block_table;
     if constexpr (kView != View::kWhole) {
-        base = shared_keys(p.prefix_len, p.max_prefix, P, &view_flags);
+        if constexpr (kView == View::kSuffix)  // beside the prefix length, not after it
+            prefetch_l1(p.context_lens + min(tid, p.batch - 1));
+        if (p.prefix_len) base = shared_keys(p.prefix_len, p.max_prefix, P, &view_flags);
         if constexpr (kView == View::kSuffix) table += base / P;
     }
     const int per_max = p.per_max;
@@ -397,6 +399,12 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     if (slot == 0 && tid == 0 && (us.flags | view_flags))
         atomicOr(p.status, us.flags | view_flags);
     const int b = us.b, h = us.h, split = slot - us.first, n = us.n;
+    if constexpr (kView == View::kSuffix) {
+        // the unit's slots for the combine, which then need not search for them (an empty unit has
+        // none, and the combine does not ask)
+        if (b >= 0 && split == 0 && row_lo == 0 && tid == 0)
+            p.unit_slots[b * p.num_kv_heads + h] = make_int4(us.first, us.count, n, 0);
+    }
     int per = 1;
     if (b >= 0) {  // keys_per_split with this kernel's tile size
         per = max((n + us.count - 1) / us.count, p.min_split_keys);
@@ -405,6 +413,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     const int start = split * per;
     if (b < 0 || start >= n) {  // idle slot: the combine never reads it
         if constexpr (kFused) fused_merge<C::kThreads>(p, smem);
+        if constexpr (kView == View::kSuffix) griddep_wait();
         return;
     }
     const bool guessed = kView == View::kWhole && b == (int)blockIdx.z && split == rblk.xs && per == per_max;
@@ -518,7 +527,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
             if (k_next) {
                 if (lane == 0) {
                     if (!dep_done && start + (tk + 1) * kTile > drafted) {
-                        griddep_wait();
+                        if constexpr (kView != View::kSuffix) griddep_wait();
                         dep_done = true;
                     }
                     const int s = tk % kKStages;
@@ -543,7 +552,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                 const int nkeys = min(kVKeys, end - h0);
                 uint8_t* vstage = smem + C::kOffV + vs * kVStage;
                 if (lane == 0 && !dep_done && h0 + kVKeys > drafted) {
-                    griddep_wait();
+                    if constexpr (kView != View::kSuffix) griddep_wait();
                     dep_done = true;
                 }
                 if (nkeys == kVKeys) {
@@ -714,7 +723,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         // Q -> three E4M3 terms (one warp per row), row scales. Q and the scales, and every
         // workspace write below, come after the preceding kernel's completion (a no-op unless
         // this grid is its programmatic dependent).
-        griddep_wait();
+        if constexpr (kView != View::kSuffix) griddep_wait();
         {
             constexpr int kRowsPerWarp = RP / C::kSoftWarps;  // 4
             const float qk_scale = __ldg(p.k_scale) * 0.0625f * kLog2e;  // D^-1/2 = 1/16
@@ -1091,6 +1100,9 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         tmem_dealloc(tmem, C::kTmemCols);
     }
     if constexpr (kFused) fused_merge<C::kThreads>(p, smem);
+    // The sequences' own keys need nothing of the prefix kernel before them, and may run beside its
+    // last CTAs; whoever waits for this grid must find that one complete too.
+    if constexpr (kView == View::kSuffix) griddep_wait();
 }
 
 }  // namespace tc

@@ -75,6 +75,11 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const v
     }
 }
 
+// Bring the line of an address into L1 ahead of its load.
+__device__ __forceinline__ void prefetch_l1(const void* p) {
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(p) : "memory");
+}
+
 // Fetch a TMA descriptor (a kernel parameter) ahead of its first use.
 __device__ __forceinline__ void prefetch_tensormap(const void* tensor_map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tensor_map))
