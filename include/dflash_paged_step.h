@@ -163,7 +163,7 @@ int dflash_rope_plan(const dflash_rope_problem* problem, dflash_rope_plan_t* pla
  *   phases  as written by dflash_rope_plan, device memory, 8-byte aligned
  *   q_out, k_out  token strides q_out_stride, k_out_stride. q_out may be q with the same stride
  *           (k_out likewise k): the rotation is then done in place.
- * q, k, q_out, k_out 16-byte aligned. num_tokens 0 launches nothing.
+ * q, k, q_out, k_out 16-byte aligned. num_tokens 0 .. 2^31 - 1; 0 launches nothing.
  */
 int dflash_rope_apply(const dflash_rope_plan_t* plan, int64_t num_tokens, const void* q,
                       int64_t q_stride, const void* k, int64_t k_stride, const int32_t* positions,

@@ -426,47 +426,70 @@ class VerifyAttention:
 # ---------------------------------------------------------------------------------------------
 # a paged decoding step (include/dflash_paged_step.h): tables, rotary positions with the cache
 # write, attention over a shared prefix. These classes check types, shapes, strides and devices
-# before they pass pointers on, and launch on their own device whichever is current.
+# before they pass pointers on, and launch on their own device whichever is current. Small calls
+# are bound by the host, so the checks and the look-ups of device and stream are kept short.
 
-def _want(name, t, dtype, shape, device):
+# (torch.cuda.current_stream builds a Stream object, 3 us on the host of a GB300)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _refuse(name, t, dtype, shape, index, form="contiguous "):
+    got = (f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}"
+           if isinstance(t, torch.Tensor) else type(t).__name__)
+    raise ValueError(f"{name}: want {form}{dtype} {tuple(shape)} on cuda:{index}, got {got}")
+
+
+def _want(name, t, dtype, shape, index):
     """Raise unless t is a contiguous tensor of this type and shape on this device."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.is_contiguous() and t.device == device):
-        got = (f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}"
-               if isinstance(t, torch.Tensor) else type(t).__name__)
-        raise ValueError(f"{name}: want contiguous {dtype} {tuple(shape)} on {device}, got {got}")
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape
+            or t.get_device() != index or not t.is_contiguous()):
+        _refuse(name, t, dtype, shape, index)
 
 
-def _want_rows(name, t, dtype, tokens, heads, head_dim, device):
+def _want_rows(name, t, dtype, shape, index):
     """Raise unless t is [tokens, heads, head_dim] with heads one after the other (tokens may be
     further apart: a slice of a fused projection); returns the token stride in elements."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device
-            and t.shape == (tokens, heads, head_dim)):
-        got = (f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor)
-               else type(t).__name__)
-        raise ValueError(f"{name}: want {dtype} {(tokens, heads, head_dim)} on {device}, got {got}")
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape
+            or t.get_device() != index):
+        _refuse(name, t, dtype, shape, index, "")
     st = t.stride()
-    if (heads > 1 and st[1] != head_dim) or st[2] != 1:
+    if st[2] != 1 or (st[1] != shape[2] and shape[1] > 1):
         raise ValueError(f"{name}: heads must lie one after the other, got strides {st}")
-    return st[0] if tokens > 1 else heads * head_dim
+    return st[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
 class _OnDevice:
     """The device of an operator and its launches."""
 
-    def __init__(self, device):
+    def __init__(self, device, *functions):
         dev = torch.device("cuda", torch.cuda.current_device() if device is None else device)
-        self.device = dev
+        self.device, self._index = dev, dev.index
+        lib = load_library()
+        self._functions = {name: getattr(lib, name) for name in functions}
 
-    def _launch(self, fn_name, args, stream):
-        fn = getattr(load_library(), fn_name)
-        if torch.cuda.current_device() == self.device.index:
-            rc = fn(*args, _stream(stream))
+    def _launch(self, name, stream, *args):
+        stream = _raw_stream(self._index) if stream is None else _stream(stream)
+        if _current_device() == self._index:
+            rc = self._functions[name](*args, stream)
         else:
-            with torch.cuda.device(self.device):
-                rc = fn(*args, _stream(stream))
+            with torch.cuda.device(self._index):
+                rc = self._functions[name](*args, stream)
         if rc != DFLASH_OK:
-            raise DflashError(fn_name, rc)
+            raise DflashError(name, rc)
+
+    def _status_word(self, status):
+        """The given status word, or one of this operator's own."""
+        if status is None:
+            return torch.zeros(4, dtype=torch.int32, device=self.device)
+        if status.dtype is not torch.int32 or status.numel() < 1 or status.device != self.device:
+            raise ValueError(f"status: want an int32 tensor on {self.device}")
+        return status
+
+    def _read_flags(self, word, clear):
+        with torch.cuda.device(self._index):
+            return dflash_verify_attn_read_flags(word, clear)
 
 
 TablesOut = collections.namedtuple("TablesOut", (
@@ -479,13 +502,14 @@ class PagedTables(_OnDevice):
 
     def __init__(self, batch, page_size, max_pages_per_seq, num_pages, max_context, max_tokens,
                  device=None, status=None):
-        super().__init__(device)
+        super().__init__(device, "dflash_paged_tables")
         self.batch, self.page_size, self.max_tokens = batch, page_size, max_tokens
         self.max_pages_per_seq, self.num_pages = max_pages_per_seq, num_pages
         self.max_context = max_context
-        if status is None:
-            status = torch.zeros(4, dtype=torch.int32, device=self.device)
-        self.status = status
+        self._problem = PagedTablesProblem(DFLASH_PAGED_STEP_VERSION, batch, page_size,
+                                           max_pages_per_seq, num_pages, max_context, max_tokens,
+                                           0, 0)
+        self.status = self._status_word(status)
 
     def empty(self) -> TablesOut:
         """Output buffers of one step."""
@@ -499,45 +523,48 @@ class PagedTables(_OnDevice):
                  prefix_table=None, prefix_pages=None, out=None, stream=None) -> TablesOut:
         """Fill the rows' new entries of block_table in place; the rest goes to out (buffers of
         empty(), made anew when not given)."""
-        B, dev, i32 = self.batch, self.device, torch.int32
+        ix, i32, each = self._index, torch.int32, (self.batch,)
         if out is None:
             out = self.empty()
-        _want("cached_lens", cached_lens, i32, (B,), dev)
-        _want("new_lens", new_lens, i32, (B,), dev)
-        _want("held_pages", held_pages, i32, (B,), dev)
-        _want("free_pages", free_pages, i32, (free_pages.numel(),), dev)
-        _want("free_head", free_head, i32, (1,), dev)
-        _want("block_table", block_table, i32, (B, self.max_pages_per_seq), dev)
-        _want("out.context_lens", out.context_lens, i32, (B,), dev)
-        _want("out.held_pages", out.held_pages, i32, (B,), dev)
-        _want("out.free_head", out.free_head, i32, (1,), dev)
-        _want("out.token_starts", out.token_starts, i32, (B + 1,), dev)
-        _want("out.positions", out.positions, i32, (self.max_tokens,), dev)
-        _want("out.slots", out.slots, torch.int64, (self.max_tokens,), dev)
-        capacity = 0
+        num_free = free_pages.numel()
+        _want("cached_lens", cached_lens, i32, each, ix)
+        _want("new_lens", new_lens, i32, each, ix)
+        _want("held_pages", held_pages, i32, each, ix)
+        _want("free_pages", free_pages, i32, (num_free,), ix)
+        _want("free_head", free_head, i32, (1,), ix)
+        _want("block_table", block_table, i32, (self.batch, self.max_pages_per_seq), ix)
+        ctx, held, head, starts, positions, slots = out
+        _want("out.context_lens", ctx, i32, each, ix)
+        _want("out.held_pages", held, i32, each, ix)
+        _want("out.free_head", head, i32, (1,), ix)
+        _want("out.token_starts", starts, i32, (self.batch + 1,), ix)
+        _want("out.positions", positions, i32, (self.max_tokens,), ix)
+        _want("out.slots", slots, torch.int64, (self.max_tokens,), ix)
+        capacity, prefix, pages = 0, None, None
         if prefix_table is not None:
             capacity = min(prefix_table.numel(), self.max_pages_per_seq)
-            _want("prefix_table", prefix_table, i32, (prefix_table.numel(),), dev)
-            _want("prefix_pages", prefix_pages, i32, (1,), dev)
+            _want("prefix_table", prefix_table, i32, (prefix_table.numel(),), ix)
+            _want("prefix_pages", prefix_pages, i32, (1,), ix)
+            if capacity:
+                prefix, pages = prefix_table.data_ptr(), prefix_pages.data_ptr()
         elif prefix_pages is not None:
             raise ValueError("prefix_pages without prefix_table")
-        problem = PagedTablesProblem(DFLASH_PAGED_STEP_VERSION, B, self.page_size,
-                                     self.max_pages_per_seq, self.num_pages, self.max_context,
-                                     self.max_tokens, free_pages.numel(), capacity)
-        self._launch("dflash_paged_tables", (
-            ctypes.byref(problem), cached_lens.data_ptr(), new_lens.data_ptr(),
-            held_pages.data_ptr(), free_pages.data_ptr(), free_head.data_ptr(),
-            prefix_table.data_ptr() if capacity else None,
-            prefix_pages.data_ptr() if capacity else None, block_table.data_ptr(),
-            out.context_lens.data_ptr(), out.held_pages.data_ptr(), out.free_head.data_ptr(),
-            out.token_starts.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr(),
-            self.status.data_ptr()), stream)
+        problem = self._problem
+        if problem.num_free != num_free or problem.prefix_capacity != capacity:
+            # (another object: a call on another thread may be using this one)
+            problem = PagedTablesProblem.from_buffer_copy(problem)
+            problem.num_free, problem.prefix_capacity = num_free, capacity
+            self._problem = problem
+        self._launch("dflash_paged_tables", stream, ctypes.byref(problem), cached_lens.data_ptr(),
+                     new_lens.data_ptr(), held_pages.data_ptr(), free_pages.data_ptr(),
+                     free_head.data_ptr(), prefix, pages, block_table.data_ptr(), ctx.data_ptr(),
+                     held.data_ptr(), head.data_ptr(), starts.data_ptr(), positions.data_ptr(),
+                     slots.data_ptr(), self.status.data_ptr())
         return out
 
     def read_flags(self, clear=False) -> int:
         """The sticky status word (synchronises)."""
-        with torch.cuda.device(self.device):
-            return dflash_verify_attn_read_flags(self.status, clear)
+        return self._read_flags(self.status, clear)
 
 
 _ROPE_LAYOUTS = {"half": DFLASH_ROPE_HALF, "interleaved": DFLASH_ROPE_INTERLEAVED}
@@ -556,7 +583,7 @@ class Rotary(_OnDevice):
                  dtype=torch.float16, base=10000.0, scaling="none", factor=1.0,
                  trained_context=1, beta_fast=32.0, beta_slow=1.0, low_turns=1.0, high_turns=4.0,
                  page_size=16, num_pages=1, device=None, status=None):
-        super().__init__(device)
+        super().__init__(device, "dflash_rope_apply", "dflash_rope_kv_write")
         if layout not in _ROPE_LAYOUTS or scaling not in _ROPE_SCALINGS:
             raise ValueError(f"unknown layout {layout!r} or scaling {scaling!r}")
         if dtype not in _ROPE_DTYPES:
@@ -567,62 +594,62 @@ class Rotary(_OnDevice):
             num_q_heads, num_kv_heads, head_dim, head_dim if rotary_dim is None else rotary_dim,
             _ROPE_LAYOUTS[layout], _ROPE_DTYPES[dtype], base, _ROPE_SCALINGS[scaling], factor,
             trained_context, beta_fast, beta_slow, low_turns, high_turns, page_size, num_pages))
+        self._plan_ref = ctypes.byref(self.plan)
         # below 2^62: the same bits as int64
         self.phases = torch.tensor(list(phases), dtype=torch.int64, device=self.device)
-        if status is None:
-            status = torch.zeros(4, dtype=torch.int32, device=self.device)
-        self.status = status
+        self.status = self._status_word(status)
 
     def apply(self, q, k, positions, q_out=None, k_out=None, stream=None):
         """(q_out, k_out): q [T, Hq, D] and k [T, Hkv, D] (or None) rotated to positions [T].
         q_out may be q itself, k_out k itself."""
-        (Hq, Hkv, D), T, dt, dev = self.shape, positions.numel(), self.dtype, self.device
+        (Hq, Hkv, D), T, dt, ix = self.shape, positions.numel(), self.dtype, self._index
+        q_shape, k_shape = (T, Hq, D), (T, Hkv, D)
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=dt, device=dev)
-        qs = _want_rows("q", q, dt, T, Hq, D, dev)
-        qo = _want_rows("q_out", q_out, dt, T, Hq, D, dev)
-        _want("positions", positions, torch.int32, (T,), dev)
+            q_out = torch.empty(q_shape, dtype=dt, device=self.device)
+        qs = _want_rows("q", q, dt, q_shape, ix)
+        qo = _want_rows("q_out", q_out, dt, q_shape, ix)
+        _want("positions", positions, torch.int32, (T,), ix)
         ks = ko = 0
         if k is not None:
             if k_out is None:
-                k_out = torch.empty((T, Hkv, D), dtype=dt, device=dev)
-            ks = _want_rows("k", k, dt, T, Hkv, D, dev)
-            ko = _want_rows("k_out", k_out, dt, T, Hkv, D, dev)
+                k_out = torch.empty(k_shape, dtype=dt, device=self.device)
+            ks = _want_rows("k", k, dt, k_shape, ix)
+            ko = _want_rows("k_out", k_out, dt, k_shape, ix)
         elif k_out is not None:
             raise ValueError("k_out without k")
-        self._launch("dflash_rope_apply", (
-            ctypes.byref(self.plan), T, q.data_ptr(), qs, _ptr(k), ks, positions.data_ptr(),
-            self.phases.data_ptr(), q_out.data_ptr(), qo, _ptr(k_out), ko), stream)
+        self._launch("dflash_rope_apply", stream, self._plan_ref, T, q.data_ptr(), qs, _ptr(k), ks,
+                     positions.data_ptr(), self.phases.data_ptr(), q_out.data_ptr(), qo,
+                     _ptr(k_out), ko)
         return q_out, k_out
 
     def kv_write(self, q, k, v, positions, slots, k_scale, v_scale, k_pool, v_pool, q_out=None,
                  stream=None):
         """q_out: q [T, Hq, D] rotated to positions [T] (it may be q itself); the rotated k and v
         [T, Hkv, D] go to the pools at slots [T]. A token with a negative slot is left alone."""
-        (Hq, Hkv, D), T, dt, dev = self.shape, positions.numel(), self.dtype, self.device
+        (Hq, Hkv, D), T, dt, ix = self.shape, positions.numel(), self.dtype, self._index
+        q_shape, k_shape = (T, Hq, D), (T, Hkv, D)
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=dt, device=dev)
-        qs = _want_rows("q", q, dt, T, Hq, D, dev)
-        qo = _want_rows("q_out", q_out, dt, T, Hq, D, dev)
-        ks = _want_rows("k", k, dt, T, Hkv, D, dev)
-        vs = _want_rows("v", v, dt, T, Hkv, D, dev)
-        _want("positions", positions, torch.int32, (T,), dev)
-        _want("slots", slots, torch.int64, (T,), dev)
-        _want("k_scale", k_scale, torch.float32, (1,), dev)
-        _want("v_scale", v_scale, torch.float32, (1,), dev)
-        _want("k_pool", k_pool, torch.uint8, self.pool_shape, dev)
-        _want("v_pool", v_pool, torch.uint8, self.pool_shape, dev)
-        self._launch("dflash_rope_kv_write", (
-            ctypes.byref(self.plan), T, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-            positions.data_ptr(), slots.data_ptr(), self.phases.data_ptr(), k_scale.data_ptr(),
-            v_scale.data_ptr(), q_out.data_ptr(), qo, k_pool.data_ptr(), v_pool.data_ptr(),
-            self.status.data_ptr()), stream)
+            q_out = torch.empty(q_shape, dtype=dt, device=self.device)
+        qs = _want_rows("q", q, dt, q_shape, ix)
+        qo = _want_rows("q_out", q_out, dt, q_shape, ix)
+        ks = _want_rows("k", k, dt, k_shape, ix)
+        vs = _want_rows("v", v, dt, k_shape, ix)
+        _want("positions", positions, torch.int32, (T,), ix)
+        _want("slots", slots, torch.int64, (T,), ix)
+        _want("k_scale", k_scale, torch.float32, (1,), ix)
+        _want("v_scale", v_scale, torch.float32, (1,), ix)
+        _want("k_pool", k_pool, torch.uint8, self.pool_shape, ix)
+        _want("v_pool", v_pool, torch.uint8, self.pool_shape, ix)
+        self._launch("dflash_rope_kv_write", stream, self._plan_ref, T, q.data_ptr(), qs,
+                     k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(), slots.data_ptr(),
+                     self.phases.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                     q_out.data_ptr(), qo, k_pool.data_ptr(), v_pool.data_ptr(),
+                     self.status.data_ptr())
         return q_out
 
     def read_flags(self, clear=False) -> int:
         """The sticky status word (synchronises)."""
-        with torch.cuda.device(self.device):
-            return dflash_verify_attn_read_flags(self.status, clear)
+        return self._read_flags(self.status, clear)
 
 
 class SharedPrefixAttention(_OnDevice):
@@ -633,17 +660,21 @@ class SharedPrefixAttention(_OnDevice):
     def __init__(self, batch, q_len, num_q_heads, num_kv_heads, head_dim, page_size,
                  max_pages_per_seq, num_pages, max_context, max_prefix, device=None,
                  kernel=DFLASH_PREFIX_KERNEL_AUTO, workspace=None):
-        super().__init__(device)
+        super().__init__(device, "dflash_prefix_attn_forward")
         self.problem = make_prefix_problem(batch, q_len, num_q_heads, num_kv_heads, head_dim,
                                            page_size, max_pages_per_seq, num_pages, max_context,
                                            max_prefix, self.device.index, kernel)
         self.plan = dflash_prefix_attn_plan(self.problem)
+        self._plan_ref = ctypes.byref(self.plan)
         if workspace is None:
             workspace = torch.zeros(self.plan.workspace_bytes, dtype=torch.uint8,
                                     device=self.device)
-        elif workspace.numel() * workspace.element_size() < self.plan.workspace_bytes:
-            raise ValueError("workspace smaller than plan.workspace_bytes")
+        elif (workspace.numel() * workspace.element_size() < self.plan.workspace_bytes
+              or workspace.device != self.device or not workspace.is_contiguous()):
+            raise ValueError("workspace: want plan.workspace_bytes contiguous bytes on "
+                             f"{self.device}")
         self.workspace = workspace
+        self._workspace_bytes = workspace.numel() * workspace.element_size()
         self.q_shape = (batch, q_len, num_q_heads, head_dim)
         self.pool_shape = (num_pages, page_size, num_kv_heads, head_dim)
 
@@ -652,34 +683,34 @@ class SharedPrefixAttention(_OnDevice):
         """(out, lse) of q over the pools. prefix_table: int32, the shared pages in order (at least
         floor(max_prefix / page_size) entries); prefix_len: int32 [1]; both None when the plan's
         max_prefix is 0."""
-        pr, dev, i32, f32 = self.problem, self.device, torch.int32, torch.float32
+        pr, ix, i32, f32 = self.problem, self._index, torch.int32, torch.float32
+        q_shape, pool_shape = self.q_shape, self.pool_shape
         if out is None:
-            out = torch.empty(self.q_shape, dtype=torch.float16, device=dev)
+            out = torch.empty(q_shape, dtype=torch.float16, device=self.device)
         if lse is None:
-            lse = torch.empty(self.q_shape[:3], dtype=f32, device=dev)
-        _want("q", q, torch.float16, self.q_shape, dev)
-        _want("k_pool", k_pool, torch.uint8, self.pool_shape, dev)
-        _want("v_pool", v_pool, torch.uint8, self.pool_shape, dev)
-        _want("block_table", block_table, i32, (pr.batch, pr.max_pages_per_seq), dev)
-        _want("context_lens", context_lens, i32, (pr.batch,), dev)
-        _want("k_scale", k_scale, f32, (1,), dev)
-        _want("v_scale", v_scale, f32, (1,), dev)
-        _want("out", out, torch.float16, self.q_shape, dev)
-        _want("lse", lse, f32, self.q_shape[:3], dev)
+            lse = torch.empty(q_shape[:3], dtype=f32, device=self.device)
+        _want("q", q, torch.float16, q_shape, ix)
+        _want("k_pool", k_pool, torch.uint8, pool_shape, ix)
+        _want("v_pool", v_pool, torch.uint8, pool_shape, ix)
+        _want("block_table", block_table, i32, (pr.batch, pr.max_pages_per_seq), ix)
+        _want("context_lens", context_lens, i32, (pr.batch,), ix)
+        _want("k_scale", k_scale, f32, (1,), ix)
+        _want("v_scale", v_scale, f32, (1,), ix)
+        _want("out", out, torch.float16, q_shape, ix)
+        _want("lse", lse, f32, q_shape[:3], ix)
         if pr.max_prefix > 0:
-            _want("prefix_len", prefix_len, i32, (1,), dev)
-            _want("prefix_table", prefix_table, i32, (prefix_table.numel(),), dev)
-            if prefix_table.numel() * pr.page_size < pr.max_prefix // pr.page_size * pr.page_size:
+            _want("prefix_len", prefix_len, i32, (1,), ix)
+            pages = 0 if prefix_table is None else prefix_table.numel()
+            _want("prefix_table", prefix_table, i32, (pages,), ix)
+            if pages < pr.max_prefix // pr.page_size:
                 raise ValueError("prefix_table has fewer pages than max_prefix fills")
-        self._launch("dflash_prefix_attn_forward", (
-            ctypes.byref(self.plan), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
-            _ptr(prefix_table), _ptr(prefix_len), block_table.data_ptr(),
-            context_lens.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-            self.workspace.data_ptr(), self.workspace.numel() * self.workspace.element_size(),
-            out.data_ptr(), lse.data_ptr()), stream)
+        self._launch("dflash_prefix_attn_forward", stream, self._plan_ref, q.data_ptr(),
+                     k_pool.data_ptr(), v_pool.data_ptr(), _ptr(prefix_table), _ptr(prefix_len),
+                     block_table.data_ptr(), context_lens.data_ptr(), k_scale.data_ptr(),
+                     v_scale.data_ptr(), self.workspace.data_ptr(), self._workspace_bytes,
+                     out.data_ptr(), lse.data_ptr())
         return out, lse
 
     def read_flags(self, clear=False) -> int:
         """The sticky status word (synchronises)."""
-        with torch.cuda.device(self.device):
-            return dflash_verify_attn_read_flags(self.workspace, clear)
+        return self._read_flags(self.workspace, clear)

@@ -7,10 +7,10 @@
 // product would be 2^-6 rad off at position 2^18). The top 32 bits, signed, are within 2^-32 of the
 // fraction and become an angle in half turns for sincospi.
 //
-// One CTA per token (or a few): its threads first compute the token's rotary_dim / 2 cosines and
-// sines, once for all heads, into shared memory, with the loads of the head rows already in flight;
-// then a warp takes a head row at a time, 8 elements (16 bytes) a lane. The partner of a half-layout
-// pair lies rotary_dim / 16 lanes away and comes by shuffle; an interleaved pair is in one lane.
+// One CTA per token, a warp per head row (8 elements, 16 bytes a lane). The loads of the rows go out
+// first, up to four a warp; while they are in flight the threads compute the token's rotary_dim / 2
+// cosines and sines, once for all heads, into shared memory. The partner of a half-layout pair lies
+// rotary_dim / 16 lanes away and comes by shuffle; an interleaved pair is in one lane.
 // Bound by HBM for many tokens (each element is read and written once), by latency for few.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -29,6 +29,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kLaneElems = kHeadDim / 32;  // 8
+constexpr int64_t kMaxTokens = 0x7FFFFFFF;  // one CTA each
 
 struct RopeParams {
     const void *q, *k, *v;
@@ -139,74 +140,96 @@ __device__ __forceinline__ void rotate(const uint4& w, const Turn& t, int lane, 
         y[e] = turned ? fmaf(x[e], t.c[e], o[e] * t.s[e]) : x[e];
 }
 
-// kWrite: K and V rows go to the pools as E4M3; else K (if any) to k_out.
-template <typename T, bool kHalf, bool kWrite>
+// kWrite: K and V rows go to the pools as E4M3; else K (if any) to k_out. kRows: rows a warp has in
+// flight.
+template <typename T, bool kHalf, bool kWrite, int kRows>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
     __shared__ float2 cs[kHeadDim / 2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rows = p.num_q_heads + p.num_kv_heads * (kWrite ? 2 : (p.k ? 1 : 0));
-    for (int64_t t = blockIdx.x; t < p.num_tokens; t += gridDim.x) {
-        const int64_t slot = kWrite ? p.slots[t] : 0;
-        if (slot < 0) continue;  // padding (the whole CTA agrees)
-        if (tid < p.rotary_dim / 2) {
-            const uint64_t turn = (uint64_t)(int64_t)p.positions[t] * p.phases[tid];
-            float s, c;
-            // signed 2^-32 turns -> half turns
-            sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);
-            cs[tid] = make_float2(c * p.amplitude, s * p.amplitude);
+    const int64_t t = blockIdx.x;
+    const int64_t slot = kWrite ? p.slots[t] : 0;
+    const int pos = p.positions[t];
+    const T* q = static_cast<const T*>(p.q) + t * p.q_stride;
+    const T* k = static_cast<const T*>(p.k) + t * p.k_stride;
+    const T* v = static_cast<const T*>(p.v) + t * p.v_stride;
+    for (int r0 = 0; r0 < rows; r0 += kRows * kWarps) {
+        uint4 w[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {  // (rows past the last read it again)
+            const int r = min(r0 + i * kWarps + warp, rows - 1), h = r - p.num_q_heads;
+            const T* src = h < 0 ? q + r * kHeadDim
+                                 : (h < p.num_kv_heads ? k + h * kHeadDim
+                                                       : v + (h - p.num_kv_heads) * kHeadDim);
+            w[i] = __ldcs(reinterpret_cast<const uint4*>(src) + lane);
         }
-        __syncthreads();
+        if (r0 == 0) {
+            if (tid < p.rotary_dim / 2) {
+                const uint64_t turn = (uint64_t)(int64_t)pos * p.phases[tid];
+                float s, c;
+                // signed 2^-32 turns -> half turns
+                sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);
+                cs[tid] = make_float2(c * p.amplitude, s * p.amplitude);
+            }
+            __syncthreads();
+            if (slot < 0) return;  // padding (the whole CTA agrees)
+            if (kWrite && slot >= p.num_slots && tid == 0)
+                atomicOr(p.status, DFLASH_FLAG_SLOT_RANGE);
+        }
         const Turn turn = load_turn<kHalf>(cs, lane, p.rotary_dim);
-        if (kWrite && slot >= p.num_slots && tid == 0) atomicOr(p.status, DFLASH_FLAG_SLOT_RANGE);
-        for (int r = warp; r < rows; r += kWarps) {
-            const bool is_q = r < p.num_q_heads;
-            const bool is_v = r >= p.num_q_heads + p.num_kv_heads;
-            const int h = is_q ? r : (r - p.num_q_heads) - (is_v ? p.num_kv_heads : 0);
-            const T* src = is_q ? static_cast<const T*>(p.q) + t * p.q_stride
-                                : (is_v ? static_cast<const T*>(p.v) + t * p.v_stride
-                                        : static_cast<const T*>(p.k) + t * p.k_stride);
-            const uint4 w = reinterpret_cast<const uint4*>(src + h * kHeadDim)[lane];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int r = r0 + i * kWarps + warp, h = r - p.num_q_heads;
+            if (r >= rows) break;
+            const bool is_q = h < 0, is_v = h >= p.num_kv_heads;
+            const int hk = is_v ? h - p.num_kv_heads : h;
             float y[kLaneElems];
             if (is_v)
-                unpack<T>(w, y);
+                unpack<T>(w[i], y);
             else
-                rotate<T, kHalf>(w, turn, lane, p.rotary_dim, y);
+                rotate<T, kHalf>(w[i], turn, lane, p.rotary_dim, y);
             if (is_q || !kWrite) {
-                T* dst = is_q ? static_cast<T*>(p.q_out) + t * p.q_out_stride
-                              : static_cast<T*>(p.k_out) + t * p.k_out_stride;
-                reinterpret_cast<uint4*>(dst + h * kHeadDim)[lane] = pack<T>(y);
+                T* dst = is_q ? static_cast<T*>(p.q_out) + t * p.q_out_stride + r * kHeadDim
+                              : static_cast<T*>(p.k_out) + t * p.k_out_stride + hk * kHeadDim;
+                reinterpret_cast<uint4*>(dst)[lane] = pack<T>(y);
             } else if (slot < p.num_slots) {
                 const float scale = is_v ? *p.v_scale : *p.k_scale;
                 uint32_t code[2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    code[i] = ptx::f32x2_to_e4m3x2(__fdiv_rn(y[4 * i], scale),
-                                                   __fdiv_rn(y[4 * i + 1], scale)) |
-                              (uint32_t)ptx::f32x2_to_e4m3x2(__fdiv_rn(y[4 * i + 2], scale),
-                                                             __fdiv_rn(y[4 * i + 3], scale))
+                for (int e = 0; e < 2; ++e)
+                    code[e] = ptx::f32x2_to_e4m3x2(__fdiv_rn(y[4 * e], scale),
+                                                   __fdiv_rn(y[4 * e + 1], scale)) |
+                              (uint32_t)ptx::f32x2_to_e4m3x2(__fdiv_rn(y[4 * e + 2], scale),
+                                                             __fdiv_rn(y[4 * e + 3], scale))
                                   << 16;
                 uint8_t* pool = is_v ? p.v_pool : p.k_pool;
-                reinterpret_cast<uint2*>(pool + (slot * p.num_kv_heads + h) * kHeadDim)[lane] =
+                reinterpret_cast<uint2*>(pool + (slot * p.num_kv_heads + hk) * kHeadDim)[lane] =
                     make_uint2(code[0], code[1]);
             }
         }
-        __syncthreads();  // the table of turns is the next token's
     }
 }
 
-template <bool kWrite>
-cudaError_t launch(const dflash_rope_plan_t* plan, const RopeParams& p, cudaStream_t stream) {
+template <bool kWrite, int kRows>
+cudaError_t launch_rows(const dflash_rope_plan_t* plan, const RopeParams& p, cudaStream_t stream) {
     const dflash_rope_problem& pr = plan->problem;
     const bool half = pr.layout == DFLASH_ROPE_HALF;
     void (*kernel)(RopeParams);
     if (pr.dtype == DFLASH_FP16)
-        kernel = half ? rope_kernel<__half, true, kWrite> : rope_kernel<__half, false, kWrite>;
+        kernel = half ? rope_kernel<__half, true, kWrite, kRows>
+                      : rope_kernel<__half, false, kWrite, kRows>;
     else
-        kernel = half ? rope_kernel<__nv_bfloat16, true, kWrite>
-                      : rope_kernel<__nv_bfloat16, false, kWrite>;
-    const int64_t grid = p.num_tokens < 65536 ? p.num_tokens : 65536;
-    kernel<<<(unsigned)grid, kThreads, 0, stream>>>(p);
+        kernel = half ? rope_kernel<__nv_bfloat16, true, kWrite, kRows>
+                      : rope_kernel<__nv_bfloat16, false, kWrite, kRows>;
+    kernel<<<(unsigned)p.num_tokens, kThreads, 0, stream>>>(p);
     return cudaGetLastError();
+}
+
+template <bool kWrite>
+cudaError_t launch(const dflash_rope_plan_t* plan, const RopeParams& p, cudaStream_t stream) {
+    const int rows = p.num_q_heads + p.num_kv_heads * 2;
+    return rows <= kWarps ? launch_rows<kWrite, 1>(plan, p, stream)
+                          : launch_rows<kWrite, 4>(plan, p, stream);
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -304,7 +327,8 @@ int dflash_rope_apply(const dflash_rope_plan_t* plan, int64_t num_tokens, const 
     const int rc = check_plan(plan);
     if (rc != DFLASH_OK) return rc;
     const dflash_rope_problem& pr = plan->problem;
-    if (num_tokens < 0 || (k == nullptr) != (k_out == nullptr)) return DFLASH_ERR_INVALID_ARGUMENT;
+    if (num_tokens < 0 || num_tokens > kMaxTokens || (k == nullptr) != (k_out == nullptr))
+        return DFLASH_ERR_INVALID_ARGUMENT;
     if (num_tokens == 0) return DFLASH_OK;
     if (!rows_ok(q, q_stride, pr.num_q_heads) || !rows_ok(q_out, q_out_stride, pr.num_q_heads) ||
         (k && (!rows_ok(k, k_stride, pr.num_kv_heads) ||
@@ -342,7 +366,7 @@ int dflash_rope_kv_write(const dflash_rope_plan_t* plan, int64_t num_tokens, con
     const int rc = check_plan(plan);
     if (rc != DFLASH_OK) return rc;
     const dflash_rope_problem& pr = plan->problem;
-    if (num_tokens < 0) return DFLASH_ERR_INVALID_ARGUMENT;
+    if (num_tokens < 0 || num_tokens > kMaxTokens) return DFLASH_ERR_INVALID_ARGUMENT;
     if (num_tokens == 0) return DFLASH_OK;
     if (!rows_ok(q, q_stride, pr.num_q_heads) || !rows_ok(k, k_stride, pr.num_kv_heads) ||
         !rows_ok(v, v_stride, pr.num_kv_heads) || !rows_ok(q_out, q_out_stride, pr.num_q_heads) ||
