@@ -7,10 +7,10 @@
 // product would be 2^-6 rad off at position 2^18). The top 32 bits, signed, are within 2^-32 of the
 // fraction and become an angle in half turns for sincospi.
 //
-// One CTA per token, a warp per head row (8 elements, 16 bytes a lane). The loads of the rows go out
-// first, up to four a warp; while they are in flight the threads compute the token's rotary_dim / 2
-// cosines and sines, once for all heads, into shared memory. The partner of a half-layout pair lies
-// rotary_dim / 16 lanes away and comes by shuffle; an interleaved pair is in one lane.
+// One CTA per token, a warp per head row. The loads of the rows go out first, up to four a warp; while
+// they are in flight the threads compute the token's rotary_dim / 2 cosines and sines, once for all
+// heads, into shared memory. A lane has four pairs, whole: in the half layout 4 elements of each half
+// (two 8-byte pieces), interleaved 8 in a row; lanes past the rotated part pass 8 elements through.
 // Bound by HBM for many tokens (each element is read and written once), by latency for few.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -28,7 +28,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kLaneElems = kHeadDim / 32;  // 8
 constexpr int64_t kMaxTokens = 0x7FFFFFFF;  // one CTA each
 
 struct RopeParams {
@@ -47,11 +46,12 @@ struct RopeParams {
     float amplitude;
 };
 
+// Four elements of a row (8 bytes).
 template <typename T>
-__device__ __forceinline__ void unpack(const uint4& w, float (&x)[kLaneElems]) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ void unpack(const uint2& w, float (&x)[4]) {
+    const uint32_t u[2] = {w.x, w.y};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
         float2 f;
         if constexpr (std::is_same_v<T, __half>)
             f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
@@ -63,10 +63,10 @@ __device__ __forceinline__ void unpack(const uint4& w, float (&x)[kLaneElems]) {
 }
 
 template <typename T>
-__device__ __forceinline__ uint4 pack(const float (&x)[kLaneElems]) {
-    uint32_t u[4];
+__device__ __forceinline__ uint2 pack(const float (&x)[4]) {
+    uint32_t u[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
         if constexpr (std::is_same_v<T, __half>) {
             const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
             u[i] = *reinterpret_cast<const uint32_t*>(&h);
@@ -75,76 +75,33 @@ __device__ __forceinline__ uint4 pack(const float (&x)[kLaneElems]) {
             u[i] = *reinterpret_cast<const uint32_t*>(&h);
         }
     }
-    return make_uint4(u[0], u[1], u[2], u[3]);
+    return make_uint2(u[0], u[1]);
 }
 
-// This lane's cosines and sines of one token, in the places that `rotate` wants them.
-struct Turn {
-    float c[kLaneElems], s[kLaneElems];
-};
+__device__ __forceinline__ uint32_t e4m3x4(const float (&x)[4], float scale) {
+    return ptx::f32x2_to_e4m3x2(__fdiv_rn(x[0], scale), __fdiv_rn(x[1], scale)) |
+           (uint32_t)ptx::f32x2_to_e4m3x2(__fdiv_rn(x[2], scale), __fdiv_rn(x[3], scale)) << 16;
+}
 
+// Four pairs turned in FP32: of the pieces (a, b) in the half layout, inside each of them interleaved.
 template <bool kHalf>
-__device__ __forceinline__ Turn load_turn(const float2* cs, int lane, int rotary_dim) {
-    Turn t;
-    const int e0 = lane * kLaneElems;
+__device__ __forceinline__ void rotate(float (&a)[4], float (&b)[4], const float (&c)[4],
+                                       const float (&s)[4]) {
 #pragma unroll
-    for (int e = 0; e < kLaneElems; ++e) {
-        t.c[e] = 1.f;
-        t.s[e] = 0.f;
+    for (int i = 0; i < 4; ++i) {
+        float& x = kHalf ? a[i] : (i < 2 ? a[2 * i] : b[2 * i - 4]);
+        float& y = kHalf ? b[i] : (i < 2 ? a[2 * i + 1] : b[2 * i - 3]);
+        const float x0 = x;
+        x = fmaf(x0, c[i], -y * s[i]);
+        y = fmaf(y, c[i], x0 * s[i]);
     }
-    if (e0 < rotary_dim) {
-        const int half = rotary_dim / 2;
-        const bool second = kHalf && e0 >= half;  // y of its pairs: y cos + x sin
-        const int i0 = kHalf ? (second ? e0 - half : e0) : e0 / 2;
-        constexpr int kPairs = kHalf ? kLaneElems : kLaneElems / 2;
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-            const float2 v = cs[i0 + i];
-            if constexpr (kHalf) {
-                t.c[i] = v.x;
-                t.s[i] = second ? v.y : -v.y;
-            } else {
-                t.c[2 * i] = t.c[2 * i + 1] = v.x;
-                t.s[2 * i] = -v.y;
-                t.s[2 * i + 1] = v.y;
-            }
-        }
-    }
-    return t;
-}
-
-// The lane's 8 elements of a head row, rotated in FP32. Every lane of the warp calls it.
-template <typename T, bool kHalf>
-__device__ __forceinline__ void rotate(const uint4& w, const Turn& t, int lane, int rotary_dim,
-                                       float (&y)[kLaneElems]) {
-    float x[kLaneElems], o[kLaneElems];
-    unpack<T>(w, x);
-    if constexpr (kHalf) {
-        const int off = rotary_dim / (2 * kLaneElems);  // lanes of half the rotated part
-        const int src = lane < off ? lane + off : (lane < 2 * off ? lane - off : lane);
-        uint4 p;
-        p.x = __shfl_sync(0xffffffffu, w.x, src);
-        p.y = __shfl_sync(0xffffffffu, w.y, src);
-        p.z = __shfl_sync(0xffffffffu, w.z, src);
-        p.w = __shfl_sync(0xffffffffu, w.w, src);
-        unpack<T>(p, o);
-    } else {
-#pragma unroll
-        for (int e = 0; e < kLaneElems; ++e) o[e] = x[e ^ 1];
-    }
-    // elements past the rotated part pass through untouched (an infinity times a zero sine
-    // would be NaN)
-    const bool turned = lane * kLaneElems < rotary_dim;
-#pragma unroll
-    for (int e = 0; e < kLaneElems; ++e)
-        y[e] = turned ? fmaf(x[e], t.c[e], o[e] * t.s[e]) : x[e];
 }
 
 // kWrite: K and V rows go to the pools as E4M3; else K (if any) to k_out. kRows: rows a warp has in
 // flight.
 template <typename T, bool kHalf, bool kWrite, int kRows>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
-    __shared__ float2 cs[kHeadDim / 2];
+    __shared__ __align__(16) float2 cs[kHeadDim / 2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rows = p.num_q_heads + p.num_kv_heads * (kWrite ? 2 : (p.k ? 1 : 0));
     const int64_t t = blockIdx.x;
@@ -153,15 +110,20 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
     const T* q = static_cast<const T*>(p.q) + t * p.q_stride;
     const T* k = static_cast<const T*>(p.k) + t * p.k_stride;
     const T* v = static_cast<const T*>(p.v) + t * p.v_stride;
+    // this lane's two pieces of a row
+    const bool turned = lane < p.rotary_dim / 8;
+    const int at = kHalf && turned ? 4 * lane : 8 * lane;
+    const int gap = kHalf && turned ? p.rotary_dim / 2 : 4;
     for (int r0 = 0; r0 < rows; r0 += kRows * kWarps) {
-        uint4 w[kRows];
+        uint2 wa[kRows], wb[kRows];
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {  // (rows past the last read it again)
             const int r = min(r0 + i * kWarps + warp, rows - 1), h = r - p.num_q_heads;
             const T* src = h < 0 ? q + r * kHeadDim
                                  : (h < p.num_kv_heads ? k + h * kHeadDim
                                                        : v + (h - p.num_kv_heads) * kHeadDim);
-            w[i] = __ldcs(reinterpret_cast<const uint4*>(src) + lane);
+            wa[i] = __ldcs(reinterpret_cast<const uint2*>(src + at));
+            wb[i] = __ldcs(reinterpret_cast<const uint2*>(src + at + gap));
         }
         if (r0 == 0) {
             if (tid < p.rotary_dim / 2) {
@@ -176,35 +138,41 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
             if (kWrite && slot >= p.num_slots && tid == 0)
                 atomicOr(p.status, DFLASH_FLAG_SLOT_RANGE);
         }
-        const Turn turn = load_turn<kHalf>(cs, lane, p.rotary_dim);
+        float c[4], s[4];
+        if (turned) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float4 f = reinterpret_cast<const float4*>(cs)[2 * lane + i];
+                c[2 * i] = f.x;
+                s[2 * i] = f.y;
+                c[2 * i + 1] = f.z;
+                s[2 * i + 1] = f.w;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             const int r = r0 + i * kWarps + warp, h = r - p.num_q_heads;
             if (r >= rows) break;
             const bool is_q = h < 0, is_v = h >= p.num_kv_heads;
             const int hk = is_v ? h - p.num_kv_heads : h;
-            float y[kLaneElems];
-            if (is_v)
-                unpack<T>(w[i], y);
-            else
-                rotate<T, kHalf>(w[i], turn, lane, p.rotary_dim, y);
+            float a[4], b[4];
+            unpack<T>(wa[i], a);
+            unpack<T>(wb[i], b);
+            // (elements past the rotated part are not multiplied: an infinity times a zero sine
+            // would be NaN)
+            if (!is_v && turned) rotate<kHalf>(a, b, c, s);
             if (is_q || !kWrite) {
-                T* dst = is_q ? static_cast<T*>(p.q_out) + t * p.q_out_stride + r * kHeadDim
-                              : static_cast<T*>(p.k_out) + t * p.k_out_stride + hk * kHeadDim;
-                reinterpret_cast<uint4*>(dst)[lane] = pack<T>(y);
+                T* dst = (is_q ? static_cast<T*>(p.q_out) + t * p.q_out_stride + r * kHeadDim
+                               : static_cast<T*>(p.k_out) + t * p.k_out_stride + hk * kHeadDim) +
+                         at;
+                *reinterpret_cast<uint2*>(dst) = pack<T>(a);
+                *reinterpret_cast<uint2*>(dst + gap) = pack<T>(b);
             } else if (slot < p.num_slots) {
                 const float scale = is_v ? *p.v_scale : *p.k_scale;
-                uint32_t code[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    code[e] = ptx::f32x2_to_e4m3x2(__fdiv_rn(y[4 * e], scale),
-                                                   __fdiv_rn(y[4 * e + 1], scale)) |
-                              (uint32_t)ptx::f32x2_to_e4m3x2(__fdiv_rn(y[4 * e + 2], scale),
-                                                             __fdiv_rn(y[4 * e + 3], scale))
-                                  << 16;
-                uint8_t* pool = is_v ? p.v_pool : p.k_pool;
-                reinterpret_cast<uint2*>(pool + (slot * p.num_kv_heads + hk) * kHeadDim)[lane] =
-                    make_uint2(code[0], code[1]);
+                uint8_t* dst = (is_v ? p.v_pool : p.k_pool) +
+                               (slot * p.num_kv_heads + hk) * kHeadDim + at;
+                *reinterpret_cast<uint32_t*>(dst) = e4m3x4(a, scale);
+                *reinterpret_cast<uint32_t*>(dst + gap) = e4m3x4(b, scale);
             }
         }
     }
