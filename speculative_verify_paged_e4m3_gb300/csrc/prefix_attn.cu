@@ -26,8 +26,8 @@ namespace {
 
 constexpr int kMaxBatch = 4096;
 constexpr int kMinSplitKeys = 256;
-constexpr int kPairsFromRows = 400;
 constexpr int kLongOwn = 2048;
+constexpr int kCtaPerRow = 2048;  // query rows up to which the combine takes a CTA for each
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -49,15 +49,19 @@ struct PrefixCombineParams {
 
 constexpr int kMergeWarps = 8;
 
-// One warp per query row, 8 columns a lane. The row's split states are read a lane each (so that their
-// loads overlap, whatever their number), the maximum and the weights follow by shuffles, then every
-// split's numerator is added in split order: prefix first. Bound by the latency of three dependent
-// loads for few rows, by L2 for many (4 KB of state a row and split).
+// kRowWarps warps per query row, 8 columns a lane. The row's split states are read a lane each (so that
+// their loads overlap, whatever their number), the maximum and the weights follow by shuffles, and each
+// warp adds its splits' numerators in split order, prefix first; the warps of a row add up in order.
+// One warp a row where there are rows enough for the GPU (bound by L2, 1 KB a row and split), eight for
+// few rows, which often have many splits (a warp alone took 30 us for 128 of them).
+template <int kRowWarps>
 __global__ void __launch_bounds__(32 * kMergeWarps)
     prefix_combine_kernel(const PrefixCombineParams p) {
     griddep_wait();  // both kernels before this one are complete (the split kernel waited for the other)
-    const int orow = blockIdx.x * kMergeWarps + threadIdx.x / 32, lane = threadIdx.x & 31;
-    if (orow >= p.total_rows) return;
+    constexpr int kRowsPerCta = kMergeWarps / kRowWarps;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int orow = blockIdx.x * kRowsPerCta + warp / kRowWarps, part = warp % kRowWarps;
+    if (orow >= p.total_rows) return;  // (whole rows)
     const int token = orow / p.num_q_heads, hq = orow - token * p.num_q_heads;
     const int b = token / p.q_len, h = hq / p.group;
     const int r = (token - b * p.q_len) * p.group + (hq - h * p.group);  // of its (sequence, KV head)
@@ -112,7 +116,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
             L = fmaf(w, st.y, L);
             const int n = min(total - s0, 32);
 #pragma unroll 4
-            for (int k = 0; k < n; ++k) {
+            for (int k = part; k < n; k += kRowWarps) {  // (32 is a multiple of kRowWarps)
                 const int s = s0 + k;
                 const float wk = __shfl_sync(0xffffffffu, w, k);
                 const float* a = s < pre_active
@@ -133,16 +137,45 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-        const float inv = 1.f / L;
-        t0 = make_float4(t0.x * inv, t0.y * inv, t0.z * inv, t0.w * inv);
-        t1 = make_float4(t1.x * inv, t1.y * inv, t1.z * inv, t1.w * inv);
     }
+    const float inv = M == -INFINITY ? 0.f : 1.f / L;
     __half2* out2 = reinterpret_cast<__half2*>(p.out + (int64_t)orow * kHeadDim);
-    out2[2 * lane] = __floats2half2_rn(t0.x, t0.y);
-    out2[2 * lane + 1] = __floats2half2_rn(t0.z, t0.w);
-    out2[64 + 2 * lane] = __floats2half2_rn(t1.x, t1.y);
-    out2[64 + 2 * lane + 1] = __floats2half2_rn(t1.z, t1.w);
-    if (lane == 0) p.lse[orow] = (M == -INFINITY) ? -INFINITY : (M + log2f(L)) * kLn2;
+    if constexpr (kRowWarps > 1) {
+        static_assert(kRowWarps == 1 || kRowWarps == kMergeWarps, "a row is a warp or the CTA");
+        __shared__ float4 sums[kMergeWarps][kHeadDim / 4];
+        sums[part][lane] = t0;
+        sums[part][32 + lane] = t1;
+        __syncthreads();
+        if (part < 2) {  // half a row each
+            float4 t = sums[0][32 * part + lane];
+#pragma unroll
+            for (int w = 1; w < kRowWarps; ++w) {
+                const float4 u = sums[w][32 * part + lane];
+                t = make_float4(t.x + u.x, t.y + u.y, t.z + u.z, t.w + u.w);
+            }
+            out2[64 * part + 2 * lane] = __floats2half2_rn(t.x * inv, t.y * inv);
+            out2[64 * part + 2 * lane + 1] = __floats2half2_rn(t.z * inv, t.w * inv);
+        }
+    } else {
+        out2[2 * lane] = __floats2half2_rn(t0.x * inv, t0.y * inv);
+        out2[2 * lane + 1] = __floats2half2_rn(t0.z * inv, t0.w * inv);
+        out2[64 + 2 * lane] = __floats2half2_rn(t1.x * inv, t1.y * inv);
+        out2[64 + 2 * lane + 1] = __floats2half2_rn(t1.z * inv, t1.w * inv);
+    }
+    if (part == 0 && lane == 0)
+        p.lse[orow] = (M == -INFINITY) ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+// Which kernel takes less time over the longest prefix: blocks of 48 rows at 0.067 ns a block, key and
+// KV head over the whole GPU (1.3 us a 128-key tile and SM; at least HBM's 0.076 ns a key and KV head),
+// or blocks of 256 rows at 0.16 ns (1.17 us a 96-key tile and pair), whose start and end cost 6 us
+// more. Measured, 24/4 heads over 120000 keys: 96 rows 93 against 119 us, 144 rows 137 against 119, 384
+// rows 483 against 203; over 4096 keys: 288 rows 33 against 37 us, 768 rows 47 against 42.
+bool pairs_win(int64_t rows, const dflash_prefix_attn_problem* pr) {
+    const double keys = (double)pr->max_prefix * pr->num_kv_heads;
+    const double small_ns = 0.067 * keys * (double)ceil_div(rows, tc_max_rows());
+    const double large_ns = 0.16 * keys * (double)ceil_div(rows, kPairRows);
+    return small_ns > large_ns + 6000.0;
 }
 
 // The plan that a problem has; a plan handed to forward must be the same bytes.
@@ -193,7 +226,7 @@ int make_plan(const dflash_prefix_attn_problem* pr, dflash_prefix_attn_plan_t* p
     const int64_t rows = (int64_t)pr->batch * plan->suffix.rows;
     plan->prefix_rows = (int32_t)rows;
     const bool use_pairs = pr->kernel == DFLASH_PREFIX_KERNEL_PAIRS ||
-                           (pr->kernel == DFLASH_PREFIX_KERNEL_AUTO && rows >= kPairsFromRows);
+                           (pr->kernel == DFLASH_PREFIX_KERNEL_AUTO && pairs_win(rows, pr));
     int64_t slots;
     if (use_pairs) {
         plan->prefix_kernel = DFLASH_PREFIX_KERNEL_PAIRS;
@@ -380,7 +413,8 @@ int dflash_prefix_attn_forward(const dflash_prefix_attn_plan_t* plan, const void
         c.pre_blocks = plan->prefix_row_blocks;
         c.pre_pairs = by_pairs ? plan->prefix_splits : 0;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((c.total_rows + kMergeWarps - 1) / kMergeWarps);
+        const bool few = c.total_rows <= kCtaPerRow;
+        cfg.gridDim = dim3(few ? c.total_rows : (c.total_rows + kMergeWarps - 1) / kMergeWarps);
         cfg.blockDim = dim3(32 * kMergeWarps);
         cfg.stream = stream;
         cudaLaunchAttribute attr[1];
@@ -388,7 +422,8 @@ int dflash_prefix_attn_forward(const dflash_prefix_attn_plan_t* plan, const void
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, prefix_combine_kernel, c);
+        e = cudaLaunchKernelEx(
+            &cfg, few ? prefix_combine_kernel<kMergeWarps> : prefix_combine_kernel<1>, c);
     }
     if (e == cudaSuccess) {
         e = cudaGetLastError();
