@@ -59,7 +59,6 @@ constexpr int kMergeWarps = 8;
 template <int kRowWarps>
 __global__ void __launch_bounds__(32 * kMergeWarps)
     prefix_combine_kernel(const PrefixCombineParams p) {
-    griddep_wait();  // both kernels before this one are complete (the split kernel waited for the other)
     constexpr int kRowsPerCta = kMergeWarps / kRowWarps;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int orow = blockIdx.x * kRowsPerCta + warp / kRowWarps, part = warp % kRowWarps;
@@ -72,15 +71,6 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
                          ? shared_keys(p.prefix_len, p.max_prefix, p.page_size, &unused)
                          : 0;
     const int ctx = min(p.context_lens[b], p.max_context);
-    // own keys: own_active states, rows apart from own0 on
-    int own_active = 0;
-    int64_t own0 = 0;
-    if (ctx > base) {
-        const int4 us = p.unit_slots[b * p.num_kv_heads + h];
-        const int per = keys_per_split(us.z, us.y, 128, kMinSplitKeys);
-        own_active = (us.z + per - 1) / per;
-        own0 = (int64_t)us.x * p.rows + r;
-    }
     // prefix: pre_active states, pre_step rows apart from pre0 on
     const int prow = b * p.rows + r;  // row of the whole batch
     int pre_active = 0, pre_step = p.pre_rows;
@@ -97,6 +87,17 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
         const int per = keys_per_split(base, p.pre_splits, 128, kMinSplitKeys);
         pre_active = (base + per - 1) / per;
         pre0 = (int64_t)h * p.pre_splits * p.pre_rows + prow;
+    }
+    // From here on what both kernels before this one wrote: they are complete (the split kernel waited
+    // for the other). Own keys: own_active states, rows apart from own0 on.
+    griddep_wait();
+    int own_active = 0;
+    int64_t own0 = 0;
+    if (ctx > base) {
+        const int4 us = __ldcg(&p.unit_slots[b * p.num_kv_heads + h]);
+        const int per = keys_per_split(us.z, us.y, 128, kMinSplitKeys);
+        own_active = (us.z + per - 1) / per;
+        own0 = (int64_t)us.x * p.rows + r;
     }
     const int total = pre_active + own_active;
     auto state_of = [&](int s) {  // split s: past the end, no weight
@@ -180,6 +181,34 @@ bool pairs_win(int64_t rows, const dflash_prefix_attn_problem* pr) {
     return small_ns > large_ns + 6000.0;
 }
 
+// SM pairs for the prefix. The sequences' own keys run on the SMs left over, from the start, and on all of
+// them once the prefix is done; a CTA of theirs takes 9 us and 1.3 us a tile, so that on an idle GPU at
+// the end most of its SMs wait for the longest. The count is the one that lets both end soonest, for own
+// keys half as many as the plan allows (fewer leave those SMs idle for a part, more run on after the
+// prefix). 32 single tokens over 65536 keys, up to 1000 of their own: 95 -> 80 us with 64 pairs of 76.
+int64_t pairs_for(int64_t blocks, int sm_count, const dflash_prefix_attn_problem* pr) {
+    const int64_t all = sm_count / 2;
+    const int units = (int)(blocks * pr->num_kv_heads);
+    const int64_t own_keys = (pr->max_context - pr->max_prefix) / 2 + pr->q_len;
+    const double own_sm_us =
+        (double)pr->batch * pr->num_kv_heads * (9.0 + 1.3 * (double)ceil_div(own_keys, 128));
+    int64_t best = all;
+    double best_us = 0;
+    for (int64_t pairs = all; pairs > 0 && pairs >= all / 2; --pairs) {
+        const PairShare share = pair_share(pr->max_prefix, units, (int)pairs);
+        double us = 10.0 + 1.2 * (double)share.per_pair;
+        // a share over a unit's end has a second start and epilogue
+        if (share.pitch == share.tiles && share.pitch % share.per_pair != 0) us += 1.2 * kPairSwitch;
+        const double left = own_sm_us - (double)(sm_count - 2 * pairs) * us;
+        if (left > 0) us += left / sm_count + 15.0;
+        if (pairs == all || us < best_us) {
+            best = pairs;
+            best_us = us;
+        }
+    }
+    return best;
+}
+
 // The plan that a problem has; a plan handed to forward must be the same bytes.
 int make_plan(const dflash_prefix_attn_problem* pr, dflash_prefix_attn_plan_t* plan) {
     if (!pr || pr->version != DFLASH_PAGED_STEP_VERSION) return DFLASH_ERR_INVALID_ARGUMENT;
@@ -234,7 +263,7 @@ int make_plan(const dflash_prefix_attn_problem* pr, dflash_prefix_attn_plan_t* p
         plan->prefix_kernel = DFLASH_PREFIX_KERNEL_PAIRS;
         const int64_t blocks = ceil_div(rows, kPairRows);
         plan->prefix_row_blocks = (int32_t)blocks;
-        plan->prefix_splits = plan->sm_count / 2;
+        plan->prefix_splits = (int32_t)pairs_for(blocks, plan->sm_count, pr);
         if (plan->prefix_splits < 1) return DFLASH_ERR_UNSUPPORTED;
         slots = plan->prefix_splits + blocks * pr->num_kv_heads;  // a segment's slot: pair + unit
         plan->prefix_slot_rows = kPairRows;

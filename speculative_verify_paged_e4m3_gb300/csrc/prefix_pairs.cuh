@@ -28,7 +28,7 @@ struct PairShare {
     int64_t per_pair;  // tiles per pair
 };
 
-__device__ __forceinline__ PairShare pair_share(int keys, int units, int pairs) {
+__host__ __device__ inline PairShare pair_share(int keys, int units, int pairs) {
     PairShare s;
     s.tiles = (keys + kPairTile - 1) / kPairTile;
     s.pitch = s.tiles;

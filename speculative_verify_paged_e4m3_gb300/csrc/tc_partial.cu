@@ -346,6 +346,13 @@ __device__ __forceinline__ void fused_merge(const PartialParams& p, uint8_t* sme
     }
 }
 
+// The sequences' own keys need nothing of the prefix kernel before them and run beside it. But who waits
+// for this grid must find that one complete too: the grid's last CTA stays until it is (every CTA doing
+// so would hold its SM for nothing).
+__device__ __forceinline__ void suffix_end() {
+    if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1) griddep_wait();
+}
+
 // kFused: the instance that merges the splits after the grid barrier (p.out set); the other
 // carries no merge code at all. kView: which keys and rows the launch covers (common.cuh).
 template <int RP, bool kFused, View kView>
@@ -418,7 +425,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     const int start = split * per;
     if (b < 0 || start >= n) {  // idle slot: the combine never reads it
         if constexpr (kFused) fused_merge<C::kThreads>(p, smem);
-        if constexpr (kView == View::kSuffix) griddep_wait();
+        if constexpr (kView == View::kSuffix) suffix_end();
         return;
     }
     const bool guessed = kView == View::kWhole && b == (int)blockIdx.z && split == rblk.xs && per == per_max;
@@ -1105,9 +1112,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         tmem_dealloc(tmem, C::kTmemCols);
     }
     if constexpr (kFused) fused_merge<C::kThreads>(p, smem);
-    // The sequences' own keys need nothing of the prefix kernel before them, and may run beside its
-    // last CTAs; whoever waits for this grid must find that one complete too.
-    if constexpr (kView == View::kSuffix) griddep_wait();
+    if constexpr (kView == View::kSuffix) suffix_end();
 }
 
 }  // namespace tc
