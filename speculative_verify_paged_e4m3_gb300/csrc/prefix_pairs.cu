@@ -20,7 +20,8 @@
 //    set the pace).
 //  * Warps: 0-7 softmax (thread = row, warps 0-3 the tile's first 48 keys, 4-7 the others), 8-9 decode
 //    K, 10-11 decode V, 12 issues the score products of the pair and 13 its PV (one thread each, in
-//    the leader SM alone), 14 copies the codes (TMA, three tiles of K and two of V ahead).
+//    the leader SM alone), 14 and 15 copy the codes of K and of V (TMA, three and two tiles
+//    ahead).
 //  * Probabilities are p = 2^(score - m) for a reference m that is set 2^4 above the first tile's
 //    maximum, and moves only when a row's probabilities of 48 keys sum to more than 2^15 (so that all
 //    are inside FP16): scores, exponentials and sums are one pass with no maximum in front of it. When
@@ -56,8 +57,8 @@ constexpr int kStages = 2;      // decoded tiles of K, and of V
 constexpr int kRawK = 3, kRawV = 2;  // tiles of codes on their way
 constexpr int kSoftWarps = 8, kDecodeWarps = 2;  // decoders per operand
 constexpr int kQkWarp = kSoftWarps + 2 * kDecodeWarps, kPvWarp = kQkWarp + 1;
-constexpr int kCopyWarp = kPvWarp + 1;
-constexpr int kThreads = 32 * (kCopyWarp + 1);  // 15 warps: 128 registers a thread
+constexpr int kCopyWarp = kPvWarp + 1;  // and the next one
+constexpr int kThreads = 32 * (kCopyWarp + 2);  // 16 warps: 128 registers a thread
 constexpr uint64_t kWaitLimitNs = 200ull * 1000 * 1000;
 constexpr float kHeadroom = 4.f;    // a reference is set 2^4 above the maximum that moves it
 constexpr float kMaxSum = 32768.f;  // a row's probabilities of a half tile sum to this at most
@@ -278,25 +279,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&sm.sfree[0]), 2 * kSoftWarps);
         mbar_init(smem_u32(&sm.sfree[1]), 2 * kSoftWarps);
         mbar_init(smem_u32(&sm.done), 2);  // one commit of each issuing warp
+        sm.abort = 0;
         fence_mbar_init();
     }
-    if (warp == kCopyWarp) {
-        // the copies touch this SM alone: they start before the pair has met
+    // The two copying warps (K, V): lane c < 6 looks up the page of the tile's 16-key chunk c, a tile
+    // ahead (the entry is not looked at before its tile's turn, so its load waits for nobody); lane 0
+    // issues. They touch this SM alone, and fill their rings before the pair has met.
+    const bool copies_k = warp == kCopyWarp;
+    bool clamped = false;
+    int copied = 0, copy_tile = 0, copy_page = 0;  // tiles issued; tile of the segment, its entry
+    bool copy_live = false;
+    auto logical = [&](int j) { return p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size; };
+    auto lookup = [&](int tile) {
+        const int j = tile * kTile + 16 * lane;
+        return lane < kTile / 16 && j < keys ? p.prefix_table[logical(j)] : 0;
+    };
+    auto copy_step = [&]() {  // the next tile of the pair's line; false: none left, or gave up
+        if (!copy_live) return false;
+        const int page = copy_page;
+        copy_page = lookup(seg.first + copy_tile + 1);
+        const int tile0 = (seg.first + copy_tile) * kTile, j = tile0 + 16 * lane;
+        const int chunks = min((keys - tile0) / 16, kTile / 16);  // of this tile
+        int row = 0;                                              // the chunk's row of the pool
+        if (lane < chunks)
+            row = clamp_page(page, p.num_pages, &clamped) * p.page_size +
+                  (j - logical(j) * p.page_size);
+        const int ring = copies_k ? kRawK : kRawV, st = copied % ring;
+        if (!ctx.wait_warp(&(copies_k ? sm.rkempty : sm.rvempty)[st], ((copied / ring) & 1) ^ 1))
+            return false;
+        const uint32_t bar = smem_u32(&(copies_k ? sm.rkfull : sm.rvfull)[st]);
+        const uint32_t dst =
+            smem_u32(smem + (copies_k ? kOffRawK : kOffRawV) + st * kRawStage);
+        // K: this SM's three chunks, whole rows; V: all six, this SM's half of the head dim
+        const int c0 = copies_k ? 3 * (int)rank : 0, most = copies_k ? 3 : kTile / 16;
+        const int n = min(max(chunks - c0, 0), most);
+        const uint32_t box = kRawStage / most;
+        const int x = seg.unit / p.blocks * kHeadDim + (copies_k ? 0 : (int)rank * (kHeadDim / 2));
+        if (lane == 0) mbar_arrive_expect_tx(bar, n * box);
+        for (int c = 0; c < n; ++c) {
+            const int y = __shfl_sync(0xffffffffu, row, c0 + c);
+            if (lane == 0) tma_load_2d(dst + c * box, copies_k ? &kmap : &vmap, x, y, bar);
+        }
+        ++copied;
+        if (++copy_tile == seg.count) {
+            copy_live = seg.next();
+            copy_tile = 0;
+            if (copy_live) copy_page = lookup(seg.first);
+        }
+        return true;
+    };
+    if (warp >= kCopyWarp) {
+        const int ring = copies_k ? kRawK : kRawV;
         if (lane == 0) {
-            prefetch_tensormap(&kmap);
-            prefetch_tensormap(&vmap);
-            for (int i = 0; i < kRawK; ++i) {
-                mbar_init(smem_u32(&sm.rkfull[i]), 1);
-                mbar_init(smem_u32(&sm.rkempty[i]), kDecodeWarps);
+            prefetch_tensormap(copies_k ? &kmap : &vmap);
+            for (int i = 0; i < ring; ++i) {
+                mbar_init(smem_u32(&(copies_k ? sm.rkfull : sm.rvfull)[i]), 1);
+                mbar_init(smem_u32(&(copies_k ? sm.rkempty : sm.rvempty)[i]), kDecodeWarps);
             }
-            for (int i = 0; i < kRawV; ++i) {
-                mbar_init(smem_u32(&sm.rvfull[i]), 1);
-                mbar_init(smem_u32(&sm.rvempty[i]), kDecodeWarps);
-            }
-            sm.abort = 0;
             fence_mbar_init();
         }
         __syncwarp();
+        copy_live = seg.next();
+        if (copy_live) copy_page = lookup(seg.first);
+        for (int i = 0; i < ring; ++i) copy_step();  // (the ring is empty: none of them waits)
     }
     if (warp == kQkWarp) {
         __syncwarp();
@@ -306,14 +351,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
-    if (warp == kCopyWarp) {  // arrives, and waits for the pair at the kernel's end only
-        asm volatile("bar.arrive 2, %0;" ::"n"(kThreads) : "memory");
-        cluster_arrive();
-    } else {
-        asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory");
-        cluster_arrive();
-        cluster_wait();
-    }
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
     tc_fence_after();
     // All 512 columns were allocated, so they start at column 0, lane 0: the addresses below are
     // constants. (Both SMs of the pair must agree, and always do: an allocation elsewhere would be
@@ -344,7 +384,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t stage_bytes = is_k ? kKStage : kVStage;
         const int key_shift = is_k ? 0 : 1;
         constexpr int kRounds = kHalfKeys / kDecodeWarps;  // keys of K, pairs of keys of V
-        static_assert(kRounds % 4 == 0 && kRounds * kDecodeWarps == kHalfKeys, "decoders");
+        static_assert(kRounds % 8 == 0 && kRounds * kDecodeWarps == kHalfKeys, "decoders");
         int rs = 0, rphase = 0;
         bool live = true;
         for (int g = 0; live && seg.next();) {
@@ -357,18 +397,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!live) break;
                 const uint8_t* src = src0 + rs * kRawStage;
                 uint8_t* dst = dst0 + s * stage_bytes;
-                // Keys past the prefix were not copied and become zeros. Four keys (pairs of V) a round,
+                // Keys past the prefix were not copied and become zeros. Eight keys (pairs of V) a round,
                 // and the same code for both operands: the roles share the instruction cache, and
                 // straight-line code for each of them was slower.
                 const int live_n = (keys - j0) >> key_shift;
 #pragma unroll 1
-                for (int n0 = 0; n0 < kRounds; n0 += 4) {
-                    uint2 v[4];
+                for (int n0 = 0; n0 < kRounds; n0 += 8) {
+                    uint2 v[8];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                    for (int k = 0; k < 8; ++k)
                         v[k] = *reinterpret_cast<const uint2*>(src + (n0 + k) * 256);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < 8; ++k) {
                         const uint32_t r = (n0 + k) << key_shift;  // key, less the lane's own bit
                         uint4 f;
                         e4m3x4_to_f16x4(v[k].x, f.x, f.y);
@@ -389,69 +429,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else if (warp == kCopyWarp) {
+    } else if (warp >= kCopyWarp) {
         // ------------------------------------------------------------------ copies
-        // Lane c < 6 looks up the page of the tile's 16-key chunk c, a tile ahead (the entry is not
-        // looked at before its tile's turn, so its load waits for nobody); lane 0 issues.
-        bool clamped = false;
-        auto logical = [&](int j) { return p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size; };
-        auto lookup = [&](int tile) {
-            const int j = tile * kTile + 16 * lane;
-            return lane < kTile / 16 && j < keys ? p.prefix_table[logical(j)] : 0;
-        };
-        int nk = 0, nv = 0;  // tiles of K and of V issued
-        bool live = true;
-        while (live && seg.next()) {
-            const int head = seg.unit / p.blocks;
-            int page = lookup(seg.first);
-            for (int i = 0; live && i < seg.count; ++i) {
-                const int page_next = lookup(seg.first + i + 1);
-                const int tile0 = (seg.first + i) * kTile, j = tile0 + 16 * lane;
-                const int chunks = min((keys - tile0) / 16, kTile / 16);  // of this tile
-                int row = 0;  // the chunk's row of the pool
-                if (lane < chunks)
-                    row = clamp_page(page, p.num_pages, &clamped) * p.page_size +
-                          (j - logical(j) * p.page_size);
-                const int ks = nk % kRawK, vs = nv % kRawV;
-                live = ctx.wait_warp(&sm.rkempty[ks], ((nk / kRawK) & 1) ^ 1);
-                if (!live) break;
-                {
-                    const int n = min(max(chunks - 3 * (int)rank, 0), 3);
-                    const uint32_t bar = smem_u32(&sm.rkfull[ks]);
-                    const uint32_t dst = smem_u32(smem + kOffRawK + ks * kRawStage);
-                    if (lane == 0) mbar_arrive_expect_tx(bar, n * 16 * kHeadDim);
-#pragma unroll
-                    for (int c = 0; c < 3; ++c) {
-                        const int y = __shfl_sync(0xffffffffu, row, 3 * rank + c);
-                        if (lane == 0 && c < n)
-                            tma_load_2d(dst + c * 16 * kHeadDim, &kmap, head * kHeadDim, y, bar);
-                    }
-                }
-                ++nk;
-                live = ctx.wait_warp(&sm.rvempty[vs], ((nv / kRawV) & 1) ^ 1);
-                if (!live) break;
-                {
-                    const uint32_t bar = smem_u32(&sm.rvfull[vs]);
-                    const uint32_t dst = smem_u32(smem + kOffRawV + vs * kRawStage);
-                    if (lane == 0) mbar_arrive_expect_tx(bar, chunks * 16 * (kHeadDim / 2));
-#pragma unroll
-                    for (int c = 0; c < kTile / 16; ++c) {
-                        const int y = __shfl_sync(0xffffffffu, row, c);
-                        if (lane == 0 && c < chunks)
-                            tma_load_2d(dst + c * 16 * (kHeadDim / 2), &vmap,
-                                        head * kHeadDim + (int)rank * (kHeadDim / 2), y, bar);
-                    }
-                }
-                ++nv;
-                page = page_next;
-            }
+        while (copy_step()) {
         }
         if (clamped) atomicOr(p.status, DFLASH_FLAG_PAGE_CLAMPED);
         // no copy may still be writing this SM's shared memory when it leaves
-        for (int t = max(nk - kRawK, 0); t < nk; ++t)
-            drain(&sm.rkfull[t % kRawK], (t / kRawK) & 1);
-        for (int t = max(nv - kRawV, 0); t < nv; ++t)
-            drain(&sm.rvfull[t % kRawV], (t / kRawV) & 1);
+        const int ring = copies_k ? kRawK : kRawV;
+        for (int t = max(copied - ring, 0); t < copied; ++t)
+            drain(&(copies_k ? sm.rkfull : sm.rvfull)[t % ring], (t / ring) & 1);
     } else if (warp == kQkWarp || warp == kPvWarp) {
         // ------------------------------------------------------------------ products
         // Issuing a product takes its thread about 50 clocks, a commit as long and a wait that is
@@ -741,7 +727,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kCopyWarp) cluster_wait();  // of the start
     cluster_arrive();
     cluster_wait();  // neither SM leaves while the other may still arrive here or read here
     if (warp == kQkWarp) {
