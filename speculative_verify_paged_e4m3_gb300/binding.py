@@ -496,6 +496,11 @@ TablesOut = collections.namedtuple("TablesOut", (
     "context_lens", "held_pages", "free_head", "token_starts", "positions", "slots"))
 
 
+class _MadeTables(TablesOut):
+    """Buffers that a PagedTables made: of the right types and shapes on its device."""
+    maker = None
+
+
 class PagedTables(_OnDevice):
     """The block-table entries, positions and cache slots of each step's new tokens, from request
     lengths on the GPU (dflash_paged_tables)."""
@@ -515,9 +520,11 @@ class PagedTables(_OnDevice):
         """Output buffers of one step."""
         def i32(n):
             return torch.empty(n, dtype=torch.int32, device=self.device)
-        return TablesOut(i32(self.batch), i32(self.batch), i32(1), i32(self.batch + 1),
-                         i32(self.max_tokens),
-                         torch.empty(self.max_tokens, dtype=torch.int64, device=self.device))
+        out = _MadeTables(i32(self.batch), i32(self.batch), i32(1), i32(self.batch + 1),
+                          i32(self.max_tokens),
+                          torch.empty(self.max_tokens, dtype=torch.int64, device=self.device))
+        out.maker = self
+        return out
 
     def __call__(self, cached_lens, new_lens, held_pages, free_pages, free_head, block_table,
                  prefix_table=None, prefix_pages=None, out=None, stream=None) -> TablesOut:
@@ -534,12 +541,13 @@ class PagedTables(_OnDevice):
         _want("free_head", free_head, i32, (1,), ix)
         _want("block_table", block_table, i32, (self.batch, self.max_pages_per_seq), ix)
         ctx, held, head, starts, positions, slots = out
-        _want("out.context_lens", ctx, i32, each, ix)
-        _want("out.held_pages", held, i32, each, ix)
-        _want("out.free_head", head, i32, (1,), ix)
-        _want("out.token_starts", starts, i32, (self.batch + 1,), ix)
-        _want("out.positions", positions, i32, (self.max_tokens,), ix)
-        _want("out.slots", slots, torch.int64, (self.max_tokens,), ix)
+        if getattr(out, "maker", None) is not self:
+            _want("out.context_lens", ctx, i32, each, ix)
+            _want("out.held_pages", held, i32, each, ix)
+            _want("out.free_head", head, i32, (1,), ix)
+            _want("out.token_starts", starts, i32, (self.batch + 1,), ix)
+            _want("out.positions", positions, i32, (self.max_tokens,), ix)
+            _want("out.slots", slots, torch.int64, (self.max_tokens,), ix)
         capacity, prefix, pages = 0, None, None
         if prefix_table is not None:
             capacity = min(prefix_table.numel(), self.max_pages_per_seq)

@@ -11,7 +11,9 @@
 // they are in flight the threads compute the token's rotary_dim / 2 cosines and sines, once for all
 // heads, into shared memory. A lane has four pairs, whole: in the half layout 4 elements of each half
 // (two 8-byte pieces), interleaved 8 in a row; lanes past the rotated part pass 8 elements through.
-// Bound by HBM for many tokens (each element is read and written once), by latency for few.
+// Bound by HBM for many tokens, by latency for few: 24571 tokens of 24 + 4 heads in bf16, 112 us, 6.3 TB/s
+// (93 % of the copy rate); with the cache write 16381 tokens of 24 + 4 + 4 heads, 86 us, 5.8 TB/s; 8 tokens
+// of one rank 2.4 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -28,6 +30,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCtasPerSm = 5;  // registers cut to fit: 24571 tokens 121 us with 4, 112 with 5, 114 with 6
 constexpr int64_t kMaxTokens = 0x7FFFFFFF;  // one CTA each
 
 struct RopeParams {
@@ -100,7 +103,7 @@ __device__ __forceinline__ void rotate(float (&a)[4], float (&b)[4], const float
 // kWrite: K and V rows go to the pools as E4M3; else K (if any) to k_out. kRows: rows a warp has in
 // flight.
 template <typename T, bool kHalf, bool kWrite, int kRows>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_kernel(const RopeParams p) {
     __shared__ __align__(16) float2 cs[kHeadDim / 2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rows = p.num_q_heads + p.num_kv_heads * (kWrite ? 2 : (p.k ? 1 : 0));
