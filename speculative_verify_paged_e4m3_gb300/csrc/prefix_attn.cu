@@ -234,6 +234,10 @@ int make_plan(const dflash_prefix_attn_problem* pr, dflash_prefix_attn_plan_t* p
     own.kernel = DFLASH_KERNEL_TCGEN05;
     const int rc = dflash_verify_attn_plan(&own, &plan->suffix);
     if (rc != DFLASH_OK) return rc;
+    // rows of the batch are counted in 32 bits from here on
+    if (pr->batch > kMaxBatch ||
+        (int64_t)pr->batch * pr->q_len * pr->num_q_heads > 0x7FFFFFFF / kPairRows)
+        return DFLASH_ERR_UNSUPPORTED;
     // With about as many units as SMs a slot per SM leaves the longest sequences unsplit: two of
     // them per SM instead, where they may be long (40 sequences of up to 4000 keys and 4 KV heads on
     // 152 SMs: the longest 32 tiles, then 12, and 13 us less in all; for up to 1000 keys a second
@@ -251,7 +255,6 @@ int make_plan(const dflash_prefix_attn_problem* pr, dflash_prefix_attn_plan_t* p
         sp.workspace_bytes =
             sp.ws_acc_offset + (size_t)sp.num_slots * sp.rows * kHeadDim * sizeof(float);
     }
-    if (pr->batch > kMaxBatch) return DFLASH_ERR_UNSUPPORTED;
     plan->version = DFLASH_PAGED_STEP_VERSION;
     plan->sm_count = plan->suffix.sm_count;
     const int64_t rows = (int64_t)pr->batch * plan->suffix.rows;

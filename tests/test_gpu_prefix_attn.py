@@ -191,6 +191,41 @@ def test_bad_pages_and_lengths_are_cut_and_flagged(kernel):
 
 
 @pytest_kernels
+def test_padded_slots_may_hold_anything(kernel):
+    """Q of a batch slot without a request, or of drafted tokens that see no key, is not looked at."""
+    inp = make(16, [700, 0, 640, 3, 650], 600)
+    want = oracle_forward(inp)
+    inp["q"][1] = float("nan")
+    inp["q"][1, :, 0] = float("inf")
+    inp["q"][3, :5] = float("-inf")  # 3 tokens in all: the first five rows of the block see none
+    dev = {k: v.cuda() for k, v in inp.items()}
+    out, lse = call(operator(inp, kernel=kernel), dev)
+    compare(to_np(out), to_np(lse), *want)
+
+
+@pytest_kernels
+@pytest.mark.parametrize("k_scale", [-0.012, 0.0, 1e-6, 0.4])
+def test_scales_of_any_size_and_sign(kernel, k_scale):
+    inp = make(17, [500, 430], 400)
+    inp["k_scale"] = torch.tensor([k_scale])
+    inp["v_scale"] = torch.tensor([-0.011])
+    check(inp, kernel)
+
+
+@pytest_kernels
+@pytest.mark.parametrize("batch,q_len,heads,longest", [
+    (200, 1, (6, 1), 90),    # more sequences than SMs
+    (70, 2, (8, 8), 90),     # more (sequence, KV head) units than SMs, one query head each
+    (2, 1, (1, 1), 90),      # two rows in all
+    (24, 4, (8, 4), 3000),   # two split slots an SM: one long sequence among short ones
+], ids=str)
+def test_many_and_few_units(kernel, batch, q_len, heads, longest):
+    lens = [64 + q_len + (7 * b) % 20 for b in range(batch)]
+    lens[batch // 2] = 64 + longest
+    check(make(batch, lens, 64, q_len, heads), kernel)
+
+
+@pytest_kernels
 def test_agrees_with_the_plain_attention(kernel):
     from gpu_helpers import gpu_forward
     inp = make(12, [2100, 2300, 2222, 2050], 2048, 8, (24, 4))
