@@ -385,6 +385,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int key_shift = is_k ? 0 : 1;
         constexpr int kRounds = kHalfKeys / kDecodeWarps;  // keys of K, pairs of keys of V
         static_assert(kRounds % 8 == 0 && kRounds * kDecodeWarps == kHalfKeys, "decoders");
+        uint32_t place[8];  // of a round's keys (less the lane's own bit), from the round's first
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t r = k << key_shift;
+            place[k] = r * 128 + (unit ^ ((r & 7) << 4));
+        }
         int rs = 0, rphase = 0;
         bool live = true;
         for (int g = 0; live && seg.next();) {
@@ -401,22 +407,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // and the same code for both operands: the roles share the instruction cache, and
                 // straight-line code for each of them was slower.
                 const int live_n = (keys - j0) >> key_shift;
+                auto decode = [&](auto whole_) {
+                    constexpr bool kWhole = decltype(whole_)::value;
 #pragma unroll 1
-                for (int n0 = 0; n0 < kRounds; n0 += 8) {
-                    uint2 v[8];
+                    for (int n0 = 0; n0 < kRounds; n0 += 8) {
+                        uint2 v[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        v[k] = *reinterpret_cast<const uint2*>(src + (n0 + k) * 256);
+                        for (int k = 0; k < 8; ++k)
+                            v[k] = *reinterpret_cast<const uint2*>(src + (n0 + k) * 256);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t r = (n0 + k) << key_shift;  // key, less the lane's own bit
-                        uint4 f;
-                        e4m3x4_to_f16x4(v[k].x, f.x, f.y);
-                        e4m3x4_to_f16x4(v[k].y, f.z, f.w);
-                        if (n0 >= live_n) f = make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4*>(dst + r * 128 + (unit ^ ((r & 7) << 4))) = f;
+                        for (int k = 0; k < 8; ++k) {
+                            uint4 f;
+                            e4m3x4_to_f16x4(v[k].x, f.x, f.y);
+                            e4m3x4_to_f16x4(v[k].y, f.z, f.w);
+                            if (!kWhole && n0 >= live_n) f = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4*>(dst + (n0 << key_shift) * 128 + place[k]) = f;
+                        }
                     }
-                }
+                };
+                if (live_n >= kRounds)
+                    decode(std::true_type{});
+                else
+                    decode(std::false_type{});
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) {
