@@ -199,6 +199,14 @@ struct Ctx {
             }
         }
     }
+    // Two barriers at once: their look-ups overlap.
+    __device__ bool wait2(uint64_t* bar_a, uint32_t parity_a, uint64_t* bar_b,
+                          uint32_t parity_b) const {
+        const uint32_t a = smem_u32(bar_a), b = smem_u32(bar_b);
+        const bool ra = mbar_test_wait(a, parity_a), rb = mbar_test_wait(b, parity_b);
+        if (ra & rb) return true;
+        return wait(bar_a, parity_a) && wait(bar_b, parity_b);
+    }
     // every lane waits and the warp agrees on the result
     __device__ bool wait_warp(uint64_t* bar, uint32_t parity) const {
         return __all_sync(0xffffffffu, wait(bar, parity));
@@ -468,8 +476,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             auto tile = [&](auto parity, int t) {
                 constexpr int kS = decltype(parity)::value;
                 // the softmax has read the scores of tile t - 2 out of this buffer
-                ok = ctx.wait(&sm.kfull[kS], (t >> 1) & 1) &&
-                     ctx.wait(&sm.sfree[kS], ((t >> 1) & 1) ^ 1);
+                ok = ctx.wait2(&sm.kfull[kS], (t >> 1) & 1, &sm.sfree[kS], ((t >> 1) & 1) ^ 1);
                 if (!ok) return;
                 tc_fence_after();
 #pragma unroll
@@ -498,10 +505,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bool ok = true;
             auto tile = [&](auto parity, int t, bool first) {
                 constexpr int kS = decltype(parity)::value;
-                ok = ctx.wait(&sm.vfull[kS], (t >> 1) & 1);
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {  // the two halves of P
-                    ok = ok && ctx.wait(&sm.pfull[hf], t & 1);
+                    ok = hf ? ctx.wait(&sm.pfull[1], t & 1)
+                            : ctx.wait2(&sm.vfull[kS], (t >> 1) & 1, &sm.pfull[0], t & 1);
                     if (!ok) return;
                     tc_fence_after();
 #pragma unroll
@@ -674,8 +681,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                 }
                 lsum += psum;
+                if (!alive) continue;
+                // the scores are read: their buffer is free before P is written
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_leader(smem_u32(&sm.sfree[t & 1]));
                 // this half of P is free once the products that read it in tile t - 1 are done
-                if (alive && i > 0)
+                if (i > 0)
                     alive = hf ? ctx.wait_warp(&sm.vempty[(t - 1) & 1], ((t - 1) >> 1) & 1)
                                : ctx.wait_warp(&sm.pdone, (t - 1) & 1);
                 if (!alive) continue;
@@ -686,10 +698,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    arrive_leader(smem_u32(&sm.pfull[hf]));
-                    arrive_leader(smem_u32(&sm.sfree[t & 1]));  // scores are read
-                }
+                if (lane == 0) arrive_leader(smem_u32(&sm.pfull[hf]));
             }
             g += seg.count;
             // ---- the segment's split state: (m, l), then the numerator through this warp's 8 KB of
