@@ -171,21 +171,22 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 
 // Which kernel takes less time over the longest prefix: blocks of 48 rows at 0.067 ns a block, key and
 // KV head over the whole GPU (1.3 us a 128-key tile and SM; at least HBM's 0.076 ns a key and KV head),
-// or blocks of 256 rows at 0.16 ns (1.17 us a 96-key tile and pair), whose start and end cost 6 us
-// more. Measured, 24/4 heads over 120000 keys: 96 rows 93 against 119 us, 144 rows 137 against 119, 384
-// rows 483 against 203; over 4096 keys: 288 rows 33 against 37 us, 768 rows 47 against 42.
+// or blocks of 256 rows at 0.136 ns (0.99 us a 96-key tile and pair), whose start and end cost 4 us
+// more. Measured, 24/4 heads over 120000 keys: 96 rows 84 against 92 us, 144 rows 135 against 94, 384
+// rows 483 against 171; 6/1 heads over 32768 keys: 144 rows 25 against 29 us, 192 rows 34 against 29.
 bool pairs_win(int64_t rows, const dflash_prefix_attn_problem* pr) {
     const double keys = (double)pr->max_prefix * pr->num_kv_heads;
     const double small_ns = 0.067 * keys * (double)ceil_div(rows, tc_max_rows());
-    const double large_ns = 0.16 * keys * (double)ceil_div(rows, kPairRows);
-    return small_ns > large_ns + 6000.0;
+    const double large_ns = 0.136 * keys * (double)ceil_div(rows, kPairRows);
+    return small_ns > large_ns + 4000.0;
 }
 
 // SM pairs for the prefix. The sequences' own keys run on the SMs left over, from the start, and on all of
 // them once the prefix is done; a CTA of theirs takes 9 us and 1.3 us a tile, so that on an idle GPU at
 // the end most of its SMs wait for the longest. The count is the one that lets both end soonest, for own
 // keys half as many as the plan allows (fewer leave those SMs idle for a part, more run on after the
-// prefix). 32 single tokens over 65536 keys, up to 1000 of their own: 95 -> 80 us with 64 pairs of 76.
+// prefix). The rates are the kernel's own: with 1.2 us a tile in place of 1.0, 32 single tokens over
+// 65536 keys took 84 us, now 74, and 16 x 8 tokens over 32768 keys 106, now 98.
 int64_t pairs_for(int64_t blocks, int sm_count, const dflash_prefix_attn_problem* pr) {
     const int64_t all = sm_count / 2;
     const int units = (int)(blocks * pr->num_kv_heads);
@@ -196,9 +197,9 @@ int64_t pairs_for(int64_t blocks, int sm_count, const dflash_prefix_attn_problem
     double best_us = 0;
     for (int64_t pairs = all; pairs > 0 && pairs >= all / 2; --pairs) {
         const PairShare share = pair_share(pr->max_prefix, units, (int)pairs);
-        double us = 10.0 + 1.2 * (double)share.per_pair;
+        double us = 10.0 + 1.0 * (double)share.per_pair;
         // a share over a unit's end has a second start and epilogue
-        if (share.pitch == share.tiles && share.pitch % share.per_pair != 0) us += 1.2 * kPairSwitch;
+        if (share.pitch == share.tiles && share.pitch % share.per_pair != 0) us += 1.0 * kPairSwitch;
         const double left = own_sm_us - (double)(sm_count - 2 * pairs) * us;
         if (left > 0) us += left / sm_count + 15.0;
         if (pairs == all || us < best_us) {

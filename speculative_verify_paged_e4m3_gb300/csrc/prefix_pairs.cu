@@ -9,15 +9,15 @@
 //
 //  * A pair of SMs carries 256 rows: 128 on each (tensor-memory lane = row), accumulator O [128,
 //    256] FP32 in each SM's tensor memory. One SM's 128 rows alone would need each decoded K and V
-//    byte written and read by that SM only: about 3500 clocks of shared-memory traffic per 2048 of
+//    byte written and read by that SM only: by count 3500 clocks of shared-memory traffic per 2048 of
 //    tensor work. With cta_group::2 the pair's second operand is split between the two SMs, so that
 //    each decodes and stores half of it (half of the tile's keys of K, half of the head dim of V).
 //  * Tiles of 96 keys: two score buffers of 96 columns and P (48 columns, two FP16 each) fit beside O
 //    in the 512 columns of tensor memory, and P needs no buffer of its own in shared memory. P does not
 //    share its columns with scores, so that no product overwrites what another one may still read; it
 //    is handed over in two halves of 48 keys, so that the softmax writes the next tile's first half
-//    while the products still read this one's second (in one piece that hand-over, 2000 clocks a tile,
-//    set the pace).
+//    while the products still read this one's second (in one piece a tile took 2020 clocks even with
+//    the decoders' and the softmax's work left out).
 //  * Warps: 0-7 softmax (thread = row, warps 0-3 the tile's first 48 keys, 4-7 the others), 8-9 decode
 //    K, 10-11 decode V, 12 issues the score products of the pair and 13 its PV (one thread each, in
 //    the leader SM alone), 14 and 15 copy the codes of K and of V (TMA, three and two tiles
@@ -31,6 +31,9 @@
 //    beside a sum of at least 2^-4, 2^-13 of it at worst over 2^17 keys.
 //  * Pairs take equal shares of all (KV head, row block) units' tiles (prefix_pairs.cuh); a share may
 //    end in the middle of a unit, the combine puts the parts together.
+//  * Bound by the tensor pipe and by what feeds it: a tile takes 1912 clocks (990 ns), its products by
+//    themselves 1565. 40 x 8 tokens of 24/4 heads over 131000 keys: 643 us, 1.60 PFLOP/s, 84 % of the
+//    bf16 library product's burst rate; the 16 x 8 tokens over 32768 keys 89 us.
 //  * Every wait is bounded (200 ms, then DFLASH_FLAG_KERNEL_TIMEOUT and a clean exit); both SMs of
 //    a pair leave together.
 #include <cuda.h>
@@ -461,9 +464,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == kQkWarp || warp == kPvWarp) {
         // ------------------------------------------------------------------ products
         // Issuing a product takes its thread about 50 clocks, a commit as long and a wait that is
-        // already over some 80: one thread needed 1700 clocks and more for the products, commits and
-        // waits of a tile whose products run in 1570. So one warp issues the scores and one PV; the
-        // tensor core takes from both. Stages and score buffers go by the tile's parity, a compile-time
+        // already over some 80. With the decoders' and the softmax's work left out a tile took 2040
+        // clocks with one issuing thread, 1796 with one for the scores and one for PV (and P in halves,
+        // eight softmax warps); its products alone run in 1565. The tensor core takes from both. Stages and score buffers go by the tile's parity, a compile-time
         // constant below: every descriptor is then a constant from the shared-memory base.
         static_assert(kStages == 2, "a tile's stage is its parity");
         using Even = std::integral_constant<int, 0>;

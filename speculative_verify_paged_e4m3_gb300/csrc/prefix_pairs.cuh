@@ -18,8 +18,9 @@ constexpr int kPairMinTiles = 4;   // least tiles worth a pair of their own
 // the unit moves on at each new segment, so the sum names it, and pairs + units slots are enough.
 // Equal shares of everything (pitch = tiles) let a pair's share run over a unit's end, which costs a
 // second epilogue, Q and pipeline fill, about kPairSwitch tiles. Where whole pairs for each unit
-// (pitch = a multiple of per_pair, the end of it empty) take fewer tiles than that, they are taken:
-// 64 rows' worth of single tokens over 65536 keys 69 -> 59 us.
+// (pitch = a multiple of per_pair, the end of it empty) cost no more than that, they are taken: 32
+// single tokens over 65536 keys 80 -> 74 us, 16 x 8 tokens over 32768 keys 107 -> 98 (24/4 heads, the
+// whole call, without and with).
 constexpr int kPairSwitch = 7;
 
 struct PairShare {
