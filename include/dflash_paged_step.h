@@ -61,7 +61,9 @@ extern "C" {
  * outside [0, num_pages) gives its tokens slot -1 (DFLASH_FLAG_PAGE_CLAMPED); context_lens above
  * max_context sets DFLASH_FLAG_CONTEXT_CLAMPED. held_pages outside [0, max_pages_per_seq] are cut
  * to that range, free_head below 0 counts as 0 and prefix_pages is cut to prefix_capacity.
- * Inputs and outputs are separate buffers, so a step can be repeated; a loop swaps them.
+ * Inputs and outputs are separate buffers (the same address twice is refused), so a step can be
+ * repeated; a loop swaps them. prefix_table may be the first row of block_table whose request holds
+ * the shared pages: entries below held_b are not written.
  */
 typedef struct {
     int32_t version;           /* DFLASH_PAGED_STEP_VERSION */

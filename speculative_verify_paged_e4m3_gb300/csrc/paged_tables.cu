@@ -205,9 +205,19 @@ extern "C" int dflash_paged_tables(const dflash_paged_tables_problem* pr,
     for (const void* w : words)
         if (!aligned(w, 4)) return DFLASH_ERR_INVALID_ARGUMENT;
     if (!aligned(slots, 8)) return DFLASH_ERR_INVALID_ARGUMENT;
-    // an output that is an input would be read while it is written
-    if (context_lens == cached_lens || held_out == held_pages || free_head_out == free_head)
-        return DFLASH_ERR_INVALID_ARGUMENT;
+    // an output that is another buffer would be read, or written twice, while it is written (but the
+    // table's first row may be the prefix's owner, whose entries are only read)
+    const void* ins[] = {cached_lens, new_lens,     held_pages,  free_pages,
+                         free_head,   prefix_table, prefix_pages};
+    const void* outs[] = {context_lens, held_out, free_head_out, token_starts,
+                          positions,    slots,    status,        block_table};
+    for (const void*& o : outs) {
+        for (const void* i : ins)
+            if (o == i && !(o == block_table && i == prefix_table))
+                return DFLASH_ERR_INVALID_ARGUMENT;
+        for (const void** before = outs; before != &o; ++before)
+            if (o == *before) return DFLASH_ERR_INVALID_ARGUMENT;
+    }
     TablesParams p = {*pr,          cached_lens,  new_lens,      held_pages,   free_pages,
                       free_head,    prefix_table, prefix_pages,  block_table,  context_lens,
                       held_out,     free_head_out, token_starts, positions,    slots,

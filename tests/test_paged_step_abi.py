@@ -74,6 +74,21 @@ def test_tables_refusals(B, kw, status):
     assert tables_call(B, **kw) == status
 
 
+TABLES_IN = ["cached", "new", "held", "free", "head", "ptable", "ppages"]
+TABLES_OUT = ["ctx", "held_out", "head_out", "starts", "positions", "slots", "status", "table"]
+
+
+@pytest.mark.parametrize("out", TABLES_OUT)
+@pytest.mark.parametrize("other", TABLES_IN + TABLES_OUT)
+def test_tables_refuse_an_output_that_is_another_buffer(B, out, other):
+    # (the table's first row may be the prefix's owner: its entries are read, not written)
+    if out == other or (out, other) == ("table", "ptable"):
+        return
+    names = ["cached", "new", "held", "free", "head", "ptable", "ppages", "table", "ctx",
+             "held_out", "head_out", "starts", "positions", "slots", "status"]
+    assert tables_call(B, bad={out: 0x10000 + 0x1000 * names.index(other)}) == -1
+
+
 def test_tables_null_problem(B):
     assert B.load_library().dflash_paged_tables(None, *([None] * 16)) == -1
 
