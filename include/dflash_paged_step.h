@@ -13,7 +13,7 @@
  * attention workspace if the step is to have a single word (dflash_verify_attn_read_flags reads
  * and clears either). Kernels run on the device that is current at the call; buffers and stream
  * belong to it. A buffer that a call writes overlaps no other buffer of the call unless the text
- * below says so.
+ * below says so (what starts at the same address is refused).
  */
 #ifndef DFLASH_PAGED_STEP_H
 #define DFLASH_PAGED_STEP_H

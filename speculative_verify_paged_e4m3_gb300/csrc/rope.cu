@@ -211,6 +211,19 @@ bool rows_ok(const void* x, int64_t stride, int heads) {
            stride <= (int64_t)1 << 40;
 }
 
+// An output at the address of another buffer (in place, q_out = q or k_out = k, is the caller's to
+// check) would be read, or written twice, while it is written.
+template <int kOuts, int kOthers>
+bool distinct(const void* const (&outs)[kOuts], const void* const (&others)[kOthers]) {
+    for (int i = 0; i < kOuts; ++i) {
+        for (int j = 0; j < kOthers; ++j)
+            if (outs[i] && outs[i] == others[j]) return false;
+        for (int j = 0; j < i; ++j)
+            if (outs[i] && outs[i] == outs[j]) return false;
+    }
+    return true;
+}
+
 bool finite(double x) { return x - x == 0.0; }
 
 int check_problem(const dflash_rope_problem* pr) {
@@ -307,6 +320,10 @@ int dflash_rope_apply(const dflash_rope_plan_t* plan, int64_t num_tokens, const 
         !positions || !aligned(positions, 4) || !phases || !aligned(phases, 8) ||
         (q == q_out && q_stride != q_out_stride) || (k && k == k_out && k_stride != k_out_stride))
         return DFLASH_ERR_INVALID_ARGUMENT;
+    const void* const outs[] = {q_out, k_out};
+    const void* const others[] = {positions, phases};
+    if (!distinct(outs, others) || q_out == k || (k && k_out == q))
+        return DFLASH_ERR_INVALID_ARGUMENT;
     RopeParams p = {};
     p.q = q;
     p.k = k;
@@ -346,6 +363,10 @@ int dflash_rope_kv_write(const dflash_rope_plan_t* plan, int64_t num_tokens, con
         !aligned(v_scale, 4) || !k_pool || !aligned(k_pool, 8) || !v_pool ||
         !aligned(v_pool, 8) || !status || !aligned(status, 4) ||
         (q == q_out && q_stride != q_out_stride))
+        return DFLASH_ERR_INVALID_ARGUMENT;
+    const void* const outs[] = {q_out, k_pool, v_pool, status};
+    const void* const others[] = {k, v, positions, slots, phases, k_scale, v_scale};
+    if (!distinct(outs, others) || k_pool == q || v_pool == q || status == q)
         return DFLASH_ERR_INVALID_ARGUMENT;
     RopeParams p = {};
     p.q = q;

@@ -193,6 +193,21 @@ def test_rope_write_refusals(B, bad):
         None) == -1
 
 
+@pytest.mark.parametrize("bad", [dict(ko=0x10000, kos=6 * 256), dict(qo=0x20000),
+                                 dict(ko=0x50000, kos=6 * 256), dict(qo=0x30000),
+                                 dict(ko=0x40000)])
+def test_rope_apply_refuses_an_output_that_is_another_buffer(B, bad):
+    assert rope_apply_status(B, **bad) == -1
+
+
+@pytest.mark.parametrize("bad", [dict(qo=0x20000), dict(qo=0x30000), dict(kp=0xb0000),
+                                 dict(kp=0x90000), dict(vp=0x90000), dict(kp=0x10000),
+                                 dict(kp=0x20000), dict(vp=0x30000), dict(vp=0x10000),
+                                 dict(status=0x40000), dict(status=0x50000)])
+def test_rope_write_refuses_an_output_that_is_another_buffer(B, bad):
+    test_rope_write_refusals(B, bad)
+
+
 # ---------------------------------------------------------------------------- shared prefix
 
 def prefix_problem(B, **kw):
