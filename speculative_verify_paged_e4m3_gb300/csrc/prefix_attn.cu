@@ -331,6 +331,14 @@ int dflash_prefix_attn_forward(const dflash_prefix_attn_plan_t* plan, const void
         !aligned(out, 8) || !aligned(lse, 4) || !aligned(prefix_table, 4) ||
         !aligned(prefix_len, 4) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
         return DFLASH_ERR_INVALID_ARGUMENT;
+    // an output or the workspace that is another buffer would be read while it is written
+    const void* ins[] = {q,          k_pool,      v_pool,       prefix_table, prefix_len,
+                         block_table, context_lens, k_scale,    v_scale};
+    const void* outs[] = {out, lse, workspace};
+    for (const void* o : outs)
+        for (const void* i : ins)
+            if (o == i) return DFLASH_ERR_INVALID_ARGUMENT;
+    if (out == lse || out == workspace || lse == workspace) return DFLASH_ERR_INVALID_ARGUMENT;
     if (workspace_bytes < plan->workspace_bytes) return DFLASH_ERR_WORKSPACE_TOO_SMALL;
     cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
     const dflash_verify_attn_plan_t& own = plan->suffix;

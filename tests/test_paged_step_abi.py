@@ -281,3 +281,15 @@ def test_prefix_forward_refuses_a_changed_plan(B, field, value):
     plan = B.dflash_prefix_attn_plan(prefix_problem(B))
     plan.suffix.num_slots += 1
     assert prefix_forward_status(B, plan, ws_bytes=1 << 40) == -1
+
+
+@pytest.mark.parametrize("out", ["out", "lse", "ws"])
+@pytest.mark.parametrize("other", ["q", "k", "v", "ptable", "plen", "table", "lens", "ks", "vs",
+                                   "out", "lse"])
+def test_prefix_forward_refuses_an_output_that_is_another_buffer(B, out, other):
+    if out == other:
+        return
+    plan = B.dflash_prefix_attn_plan(prefix_problem(B))
+    at = dict(zip(("q", "k", "v", "ptable", "plen", "table", "lens", "ks", "vs", "ws", "out", "lse"),
+                  range(0x100000, 0xd00000, 0x100000)))[other]
+    assert prefix_forward_status(B, plan, **{out: at}) == -1
