@@ -479,6 +479,17 @@ class _OnDevice:
         if rc != DFLASH_OK:
             raise DflashError(name, rc)
 
+    def _empty(self, shape, dtype, stream):
+        """A buffer for a launch on this stream, from that stream's memory: memory that was freed on the
+        current one may still be in use there."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        if isinstance(stream, int):
+            stream = (torch.cuda.ExternalStream(stream, device=self.device) if stream
+                      else torch.cuda.default_stream(self.device))
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
     def _status_word(self, status):
         """The given status word, or one of this operator's own."""
         if status is None:
@@ -516,13 +527,13 @@ class PagedTables(_OnDevice):
                                            0, 0)
         self.status = self._status_word(status)
 
-    def empty(self) -> TablesOut:
-        """Output buffers of one step."""
+    def empty(self, stream=None) -> TablesOut:
+        """Output buffers of one step, of the current stream's memory or the given one's."""
         def i32(n):
-            return torch.empty(n, dtype=torch.int32, device=self.device)
+            return self._empty(n, torch.int32, stream)
         out = _MadeTables(i32(self.batch), i32(self.batch), i32(1), i32(self.batch + 1),
                           i32(self.max_tokens),
-                          torch.empty(self.max_tokens, dtype=torch.int64, device=self.device))
+                          self._empty(self.max_tokens, torch.int64, stream))
         out.maker = self
         return out
 
@@ -532,7 +543,7 @@ class PagedTables(_OnDevice):
         empty(), made anew when not given)."""
         ix, i32, each = self._index, torch.int32, (self.batch,)
         if out is None:
-            out = self.empty()
+            out = self.empty(stream)
         num_free = free_pages.numel()
         _want("cached_lens", cached_lens, i32, each, ix)
         _want("new_lens", new_lens, i32, each, ix)
@@ -613,14 +624,14 @@ class Rotary(_OnDevice):
         (Hq, Hkv, D), T, dt, ix = self.shape, positions.numel(), self.dtype, self._index
         q_shape, k_shape = (T, Hq, D), (T, Hkv, D)
         if q_out is None:
-            q_out = torch.empty(q_shape, dtype=dt, device=self.device)
+            q_out = self._empty(q_shape, dt, stream)
         qs = _want_rows("q", q, dt, q_shape, ix)
         qo = _want_rows("q_out", q_out, dt, q_shape, ix)
         _want("positions", positions, torch.int32, (T,), ix)
         ks = ko = 0
         if k is not None:
             if k_out is None:
-                k_out = torch.empty(k_shape, dtype=dt, device=self.device)
+                k_out = self._empty(k_shape, dt, stream)
             ks = _want_rows("k", k, dt, k_shape, ix)
             ko = _want_rows("k_out", k_out, dt, k_shape, ix)
         elif k_out is not None:
@@ -637,7 +648,7 @@ class Rotary(_OnDevice):
         (Hq, Hkv, D), T, dt, ix = self.shape, positions.numel(), self.dtype, self._index
         q_shape, k_shape = (T, Hq, D), (T, Hkv, D)
         if q_out is None:
-            q_out = torch.empty(q_shape, dtype=dt, device=self.device)
+            q_out = self._empty(q_shape, dt, stream)
         qs = _want_rows("q", q, dt, q_shape, ix)
         qo = _want_rows("q_out", q_out, dt, q_shape, ix)
         ks = _want_rows("k", k, dt, k_shape, ix)
@@ -694,9 +705,9 @@ class SharedPrefixAttention(_OnDevice):
         pr, ix, i32, f32 = self.problem, self._index, torch.int32, torch.float32
         q_shape, pool_shape = self.q_shape, self.pool_shape
         if out is None:
-            out = torch.empty(q_shape, dtype=torch.float16, device=self.device)
+            out = self._empty(q_shape, torch.float16, stream)
         if lse is None:
-            lse = torch.empty(q_shape[:3], dtype=f32, device=self.device)
+            lse = self._empty(q_shape[:3], f32, stream)
         _want("q", q, torch.float16, q_shape, ix)
         _want("k_pool", k_pool, torch.uint8, pool_shape, ix)
         _want("v_pool", v_pool, torch.uint8, pool_shape, ix)
