@@ -490,6 +490,12 @@ class _OnDevice:
         with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device=self.device)
 
+    def _ready(self):
+        """Wait for what a constructor has put on the current stream: the first call may be on another.
+        (A capture cannot wait; made inside one, an operator is ready once the graph has run.)"""
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self.device).synchronize()
+
     def _status_word(self, status):
         """The given status word, or one of this operator's own."""
         if status is None:
@@ -526,6 +532,7 @@ class PagedTables(_OnDevice):
                                            max_pages_per_seq, num_pages, max_context, max_tokens,
                                            0, 0)
         self.status = self._status_word(status)
+        self._ready()
 
     def empty(self, stream=None) -> TablesOut:
         """Output buffers of one step, of the current stream's memory or the given one's."""
@@ -617,6 +624,7 @@ class Rotary(_OnDevice):
         # below 2^62: the same bits as int64
         self.phases = torch.tensor(list(phases), dtype=torch.int64, device=self.device)
         self.status = self._status_word(status)
+        self._ready()
 
     def apply(self, q, k, positions, q_out=None, k_out=None, stream=None):
         """(q_out, k_out): q [T, Hq, D] and k [T, Hkv, D] (or None) rotated to positions [T].
@@ -696,6 +704,7 @@ class SharedPrefixAttention(_OnDevice):
         self._workspace_bytes = workspace.numel() * workspace.element_size()
         self.q_shape = (batch, q_len, num_q_heads, head_dim)
         self.pool_shape = (num_pages, page_size, num_kv_heads, head_dim)
+        self._ready()
 
     def __call__(self, q, k_pool, v_pool, prefix_table, prefix_len, block_table, context_lens,
                  k_scale, v_scale, out=None, lse=None, stream=None):

@@ -1,5 +1,5 @@
 """The paged step's operators on a stream that is not the current one: results made by the call come
-from that stream's memory."""
+from that stream's memory, and an operator is ready when its constructor returns."""
 import pytest
 import torch
 
@@ -84,3 +84,26 @@ def test_results_on_the_default_stream_by_its_handle():
     got = call(stream=torch.cuda.default_stream().cuda_stream)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("make", [tables, rotary, write, attention])
+def test_an_operator_is_ready_when_it_is_made(make):
+    from speculative_verify_paged_e4m3_gb300 import binding as B
+    made = []
+
+    class Made(Exception):
+        pass
+
+    class Spy:  # the operator's class, the stream looked at as its constructor returns
+        def __getattr__(self, name):
+            def construct(*args, **kw):
+                torch.cuda._sleep(CLOCKS)
+                op = getattr(B, name)(*args, **kw)
+                made.append((op, torch.cuda.current_stream().query()))
+                raise Made
+            return construct
+    torch.cuda.synchronize()
+    with pytest.raises(Made):
+        make(Spy())
+    assert made[0][1]
+    assert made[0][0].read_flags() == 0
