@@ -205,7 +205,8 @@ int dflash_rope_kv_write(const dflash_rope_plan_t* plan, int64_t num_tokens, con
  *   prefix_table  int32 [floor(max_prefix / page_size)]; a row of block_table may serve
  *   prefix_len    one int32 (device), cut to [0, max_prefix] (DFLASH_FLAG_CONTEXT_CLAMPED)
  * A sequence that ends inside the prefix, or is empty (a padded batch slot, N = 0), sees the keys
- * that the causal rule gives it. Codes at or past a length are never used, whatever they hold; a NaN
+ * that the causal rule gives it. A row of q with a NaN or an infinity gives NaN, in its own row of
+ * out and lse alone, if it sees a key. Codes at or past a length are never used, whatever they hold; a NaN
  * code of V below the prefix length may make NaN of every row, those that do not see its key included
  * (kv_write makes one of a NaN element only).
  */

@@ -107,9 +107,17 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     };
     const float2 st0 = state_of(lane);
     float M = st0.x;
-    for (int s = 32 + lane; s < total; s += 32) M = fmaxf(M, state_of(s).x);
+    bool lost = isnan(st0.y);
+    for (int s = 32 + lane; s < total; s += 32) {
+        const float2 st = state_of(s);
+        M = fmaxf(M, st.x);
+        lost |= isnan(st.y);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    // scores that are not numbers leave no maximum but a sum that is not one either: such a row is not
+    // an empty one
+    if (__any_sync(0xffffffffu, lost)) M = NAN;
     float4 t0 = make_float4(0.f, 0.f, 0.f, 0.f), t1 = t0;
     float L = 0.f;
     if (M != -INFINITY) {

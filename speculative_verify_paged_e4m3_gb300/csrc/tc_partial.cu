@@ -766,6 +766,10 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(qv[e]));
                 amax = warp_max(amax);
+                if constexpr (kView != View::kWhole) {
+                    // (E4M3 has no infinity and would saturate one)
+                    if (amax == INFINITY) qv[0] = NAN;
+                }
                 // largest a with amax * 2^a <= 448 = 1.75 * 2^8 (amax >= 2^-24: a normal float)
                 int a = 0;
                 if (amax > 0.f) {

@@ -204,6 +204,23 @@ def test_padded_slots_may_hold_anything(kernel):
 
 
 @pytest_kernels
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_a_query_that_is_not_finite_spoils_its_own_row_alone(kernel, value):
+    inp = make(13, [900, 780, 811], 700)
+    want_out, want_lse = oracle_forward(inp)
+    bad = dict(inp, q=inp["q"].clone())
+    bad["q"][1, 3, 2, ::9] = value
+    dev = {k: v.cuda() for k, v in bad.items()}
+    out, lse = call(operator(bad, kernel=kernel), dev)
+    out, lse = to_np(out), to_np(lse)
+    assert np.isnan(out[1, 3, 2]).all() and np.isnan(lse[1, 3, 2])
+    keep = np.ones(out.shape[:3], bool)
+    keep[1, 3, 2] = False
+    out[~keep], lse[~keep] = want_out[~keep], want_lse[~keep]
+    compare(out, lse, want_out, want_lse)
+
+
+@pytest_kernels
 @pytest.mark.parametrize("k_scale", [-0.012, 0.0, 1e-6, 0.4])
 def test_scales_of_any_size_and_sign(kernel, k_scale):
     inp = make(17, [500, 430], 400)
