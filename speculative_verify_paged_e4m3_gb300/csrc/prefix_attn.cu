@@ -177,49 +177,89 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
         p.lse[orow] = (M == -INFINITY) ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
-// Which kernel takes less time over the longest prefix: blocks of 48 rows at 0.067 ns a block, key and
-// KV head over the whole GPU (1.3 us a 128-key tile and SM; at least HBM's 0.076 ns a key and KV head),
-// or blocks of 256 rows at 0.136 ns (0.99 us a 96-key tile and pair), whose start and end cost 4 us
-// more. Measured, 24/4 heads over 120000 keys: 96 rows 84 against 92 us, 144 rows 135 against 94, 384
-// rows 483 against 171; 6/1 heads over 32768 keys: 144 rows 25 against 29 us, 192 rows 34 against 29.
-bool pairs_win(int64_t rows, const dflash_prefix_attn_problem* pr) {
-    const double keys = (double)pr->max_prefix * pr->num_kv_heads;
-    const double small_ns = 0.067 * keys * (double)ceil_div(rows, tc_max_rows());
-    const double large_ns = 0.136 * keys * (double)ceil_div(rows, kPairRows);
-    return small_ns > large_ns + 4000.0;
+// Estimated times in us, over the longest prefix, for own keys half as many as the plan allows. A CTA of
+// the split kernel takes 9 us and 1.3 us a 128-key tile, a pair 10 us and 1.0 us a 96-key tile.
+constexpr double kRowsCtaUs = 9.0, kRowsTileUs = 1.3, kPairCtaUs = 10.0, kPairTileUs = 1.0;
+
+// SM time of all sequences' own keys.
+double own_sm_us(const dflash_prefix_attn_problem* pr) {
+    const int64_t keys = (pr->max_context - pr->max_prefix) / 2 + pr->q_len;
+    return (double)pr->batch * pr->num_kv_heads *
+           (kRowsCtaUs + kRowsTileUs * (double)ceil_div(keys, 128));
 }
 
-// SM pairs for the prefix. The sequences' own keys run on the SMs left over, from the start, and on all of
-// them once the prefix is done; a CTA of theirs takes 9 us and 1.3 us a tile, so that on an idle GPU at
-// the end most of its SMs wait for the longest. The count is the one that lets both end soonest, for own
-// keys half as many as the plan allows (fewer leave those SMs idle for a part, more run on after the
-// prefix). The rates are the kernel's own: with 1.2 us a tile in place of 1.0, 32 single tokens over
-// 65536 keys took 84 us, now 74, and 16 x 8 tokens over 32768 keys 106, now 98.
-int64_t pairs_for(int64_t blocks, int sm_count, const dflash_prefix_attn_problem* pr) {
+// Key splits of the prefix in blocks of 48 rows: one wave of CTAs.
+int64_t rows_splits(int64_t blocks, int sm_count, const dflash_prefix_attn_problem* pr) {
+    int64_t S = sm_count / (blocks * pr->num_kv_heads);
+    const int64_t cap = ceil_div(pr->max_prefix, kMinSplitKeys);
+    if (S > cap) S = cap;
+    return S < 1 ? 1 : S;
+}
+
+// Prefix and own keys in blocks of 48 rows. Own keys that the SMs left over have no time for start after
+// the prefix, another CTA's 9 us.
+double rows_us(int64_t blocks, int sm_count, const dflash_prefix_attn_problem* pr) {
+    const int64_t S = rows_splits(blocks, sm_count, pr);
+    int64_t per = ceil_div(pr->max_prefix, S);
+    if (per < kMinSplitKeys) per = kMinSplitKeys;
+    per = ceil_div(per, 128) * 128;
+    const int64_t ctas = blocks * pr->num_kv_heads * ceil_div(pr->max_prefix, per);
+    const int64_t keys = per < pr->max_prefix ? per : pr->max_prefix;
+    double us = kRowsCtaUs + kRowsTileUs * (double)ceil_div(keys, 128);
+    if (ctas > sm_count) us *= (double)ctas / sm_count;
+    const double hbm = kRowsCtaUs + 0.076e-3 * pr->max_prefix * pr->num_kv_heads;
+    if (us < hbm) us = hbm;
+    const int64_t spare = ctas < sm_count ? sm_count - ctas : 0;
+    const double left = own_sm_us(pr) - (double)spare * us;
+    return left > 0 ? us + left / sm_count + kRowsCtaUs : us;
+}
+
+// SM pairs for the prefix, and the time of prefix and own keys with them. The sequences' own keys run on
+// the SMs left over, from the start, and on all of them once the prefix is done, so that on an idle GPU at
+// the end most of its SMs wait for the longest. The count is the one that lets both end soonest (fewer
+// leave those SMs idle for a part, more run on after the prefix). The rates are the kernel's own: with 1.2
+// us a tile in place of 1.0, 32 single tokens over 65536 keys took 84 us, now 74, and 16 x 8 tokens over
+// 32768 keys 106, now 98.
+int64_t pairs_for(int64_t blocks, int sm_count, const dflash_prefix_attn_problem* pr,
+                  double* pairs_us) {
     const int64_t all = sm_count / 2;
     const int units = (int)(blocks * pr->num_kv_heads);
-    const int64_t own_keys = (pr->max_context - pr->max_prefix) / 2 + pr->q_len;
-    const double own_sm_us =
-        (double)pr->batch * pr->num_kv_heads * (9.0 + 1.3 * (double)ceil_div(own_keys, 128));
+    const double own = own_sm_us(pr);
     int64_t best = all;
     double best_us = 0;
     for (int64_t pairs = all; pairs > 0 && pairs >= all / 2; --pairs) {
         const PairShare share = pair_share(pr->max_prefix, units, (int)pairs);
-        double us = 10.0 + 1.0 * (double)share.per_pair;
+        double us = kPairCtaUs + kPairTileUs * (double)share.per_pair;
         // a share over a unit's end has a second start and epilogue
-        if (share.pitch == share.tiles && share.pitch % share.per_pair != 0) us += 1.0 * kPairSwitch;
-        const double left = own_sm_us - (double)(sm_count - 2 * pairs) * us;
+        if (share.pitch == share.tiles && share.pitch % share.per_pair != 0)
+            us += kPairTileUs * kPairSwitch;
+        const double left = own - (double)(sm_count - 2 * pairs) * us;
         if (left > 0) us += left / sm_count + 15.0;
         if (pairs == all || us < best_us) {
             best = pairs;
             best_us = us;
         }
     }
+    if (pairs_us) *pairs_us = best_us;
     return best;
 }
 
-// The plan that a problem has; a plan handed to forward must be the same bytes.
-int make_plan(const dflash_prefix_attn_problem* pr, dflash_prefix_attn_plan_t* plan) {
+// Which kernel takes less time. Measured, 24/4 heads over 120000 keys: 96 rows 84 against 92 us, 144 rows
+// 135 against 94, 384 rows 483 against 171; 6/1 heads over 32768 keys: 144 rows 25 against 29 us, 192 rows
+// 34 against 29. Over 610 random problems the choice costs 1.2 % over the better kernel's time in the mean,
+// 40 % at worst (a rule on the prefix alone, without the own keys: 2.3 %, 40 %).
+bool pairs_win(int64_t rows, int sm_count, const dflash_prefix_attn_problem* pr) {
+    if (pr->max_prefix == 0 || sm_count < 2) return false;
+    double pairs_us;
+    pairs_for(ceil_div(rows, kPairRows), sm_count, pr, &pairs_us);
+    return rows_us(ceil_div(rows, tc_max_rows()), sm_count, pr) > pairs_us + 1.0;
+}
+
+// The plan that a problem has; a plan handed to forward must be the same bytes. There `made` is that
+// plan: its kernel and pair count, which the estimates chose (2 us of host time), are taken from it once
+// they are in range, and everything else follows from them.
+int make_plan(const dflash_prefix_attn_problem* pr, const dflash_prefix_attn_plan_t* made,
+              dflash_prefix_attn_plan_t* plan) {
     if (!pr || pr->version != DFLASH_PAGED_STEP_VERSION) return DFLASH_ERR_INVALID_ARGUMENT;
     if (pr->batch < 1 || pr->max_prefix < 0 || pr->max_prefix > pr->max_context ||
         pr->flags != 0 || pr->kernel < DFLASH_PREFIX_KERNEL_AUTO ||
@@ -268,24 +308,32 @@ int make_plan(const dflash_prefix_attn_problem* pr, dflash_prefix_attn_plan_t* p
     plan->sm_count = plan->suffix.sm_count;
     const int64_t rows = (int64_t)pr->batch * plan->suffix.rows;
     plan->prefix_rows = (int32_t)rows;
-    const bool use_pairs = pr->kernel == DFLASH_PREFIX_KERNEL_PAIRS ||
-                           (pr->kernel == DFLASH_PREFIX_KERNEL_AUTO && pairs_win(rows, pr));
+    if (made && ((made->prefix_kernel != DFLASH_PREFIX_KERNEL_ROWS &&
+                  made->prefix_kernel != DFLASH_PREFIX_KERNEL_PAIRS) ||
+                 (pr->kernel != DFLASH_PREFIX_KERNEL_AUTO && made->prefix_kernel != pr->kernel) ||
+                 made->prefix_splits < 1 ||
+                 (made->prefix_kernel == DFLASH_PREFIX_KERNEL_PAIRS &&
+                  made->prefix_splits > plan->sm_count / 2)))
+        return DFLASH_ERR_INVALID_ARGUMENT;
+    const bool use_pairs = made ? made->prefix_kernel == DFLASH_PREFIX_KERNEL_PAIRS
+                                : pr->kernel == DFLASH_PREFIX_KERNEL_PAIRS ||
+                                      (pr->kernel == DFLASH_PREFIX_KERNEL_AUTO &&
+                                       pairs_win(rows, plan->sm_count, pr));
     int64_t slots;
     if (use_pairs) {
         plan->prefix_kernel = DFLASH_PREFIX_KERNEL_PAIRS;
         const int64_t blocks = ceil_div(rows, kPairRows);
         plan->prefix_row_blocks = (int32_t)blocks;
-        plan->prefix_splits = (int32_t)pairs_for(blocks, plan->sm_count, pr);
+        plan->prefix_splits =
+            made ? made->prefix_splits
+                 : (int32_t)pairs_for(blocks, plan->sm_count, pr, nullptr);
         if (plan->prefix_splits < 1) return DFLASH_ERR_UNSUPPORTED;
         slots = plan->prefix_splits + blocks * pr->num_kv_heads;  // a segment's slot: pair + unit
         plan->prefix_slot_rows = kPairRows;
     } else {
         plan->prefix_kernel = DFLASH_PREFIX_KERNEL_ROWS;
         const int64_t blocks = ceil_div(rows, tc_max_rows());
-        int64_t S = plan->sm_count / (blocks * pr->num_kv_heads);  // one wave
-        const int64_t cap = ceil_div(pr->max_prefix, kMinSplitKeys);
-        if (S > cap) S = cap;
-        if (S < 1) S = 1;
+        const int64_t S = rows_splits(blocks, plan->sm_count, pr);
         plan->prefix_row_blocks = (int32_t)blocks;
         plan->prefix_splits = (int32_t)S;
         slots = S * pr->num_kv_heads;
@@ -315,7 +363,7 @@ extern "C" {
 int dflash_prefix_attn_plan(const dflash_prefix_attn_problem* problem,
                             dflash_prefix_attn_plan_t* plan) {
     if (!problem || !plan) return DFLASH_ERR_INVALID_ARGUMENT;
-    return make_plan(problem, plan);
+    return make_plan(problem, nullptr, plan);
 }
 
 int dflash_prefix_attn_forward(const dflash_prefix_attn_plan_t* plan, const void* q,
@@ -327,7 +375,7 @@ int dflash_prefix_attn_forward(const dflash_prefix_attn_plan_t* plan, const void
     if (!plan || plan->version != DFLASH_PAGED_STEP_VERSION) return DFLASH_ERR_INVALID_ARGUMENT;
     dflash_prefix_attn_plan_t made;
     const dflash_prefix_attn_problem pr = plan->problem;
-    const int rc = make_plan(&pr, &made);
+    const int rc = make_plan(&pr, plan, &made);
     if (rc != DFLASH_OK) return rc;
     if (memcmp(&made, plan, sizeof(made)) != 0) return DFLASH_ERR_INVALID_ARGUMENT;
     const bool prefix = pr.max_prefix > 0;

@@ -293,3 +293,24 @@ def test_prefix_forward_refuses_an_output_that_is_another_buffer(B, out, other):
     at = dict(zip(("q", "k", "v", "ptable", "plen", "table", "lens", "ks", "vs", "ws", "out", "lse"),
                   range(0x100000, 0xd00000, 0x100000)))[other]
     assert prefix_forward_status(B, plan, **{out: at}) == -1
+
+
+@pytest.mark.parametrize("splits", [0, -1, 77, 152, 2 ** 31 - 1])
+def test_prefix_forward_refuses_more_pairs_than_the_gpu_has(B, splits):
+    plan = B.dflash_prefix_attn_plan(prefix_problem(B, kernel=2))
+    assert plan.prefix_kernel == 2 and 0 < plan.prefix_splits <= 76
+    plan.prefix_splits = splits
+    assert prefix_forward_status(B, plan, ws_bytes=1 << 40) == -1
+    plan = B.dflash_prefix_attn_plan(prefix_problem(B, kernel=2))
+    plan.prefix_kernel = 1  # not the kernel that the problem asks for
+    assert prefix_forward_status(B, plan, ws_bytes=1 << 40) == -1
+
+
+@pytest.mark.parametrize("batch,q_len,heads,prefix,kernel", [
+    (3, 8, (6, 1), 4099, 1), (2, 1, (24, 4), 300, 1), (40, 8, (24, 4), 131000, 2),
+    (32, 1, (24, 4), 65536, 2), (12, 8, (24, 4), 0, 1)])
+def test_prefix_kernel_is_chosen(B, batch, q_len, heads, prefix, kernel):
+    plan = B.dflash_prefix_attn_plan(prefix_problem(
+        B, batch=batch, q_len=q_len, num_q_heads=heads[0], num_kv_heads=heads[1],
+        max_pages_per_seq=9000, num_pages=9000, max_context=prefix + 500, max_prefix=prefix))
+    assert plan.prefix_kernel == kernel
