@@ -7,13 +7,14 @@
 // product would be 2^-6 rad off at position 2^18). The top 32 bits, signed, are within 2^-32 of the
 // fraction and become an angle in half turns for sincospi.
 //
-// One CTA per token, a warp per head row. The loads of the rows go out first, up to four a warp; while
-// they are in flight the threads compute the token's rotary_dim / 2 cosines and sines, once for all
+// One CTA per token, a warp per head row; several tokens a CTA where a token has no more rows than a CTA
+// warps (one rank's heads: a CTA's latency for 4 KB). The loads of the rows go out first, up to four a warp;
+// while they are in flight the threads compute the token's rotary_dim / 2 cosines and sines, once for all
 // heads, into shared memory. A lane has four pairs, whole: in the half layout 4 elements of each half
 // (two 8-byte pieces), interleaved 8 in a row; lanes past the rotated part pass 8 elements through.
 // Bound by HBM for many tokens, by latency for few: 24571 tokens of 24 + 4 heads in bf16, 112 us, 6.3 TB/s
-// (93 % of the copy rate); with the cache write 16381 tokens of 24 + 4 + 4 heads, 86 us, 5.8 TB/s; 8 tokens
-// of one rank 2.4 us.
+// (93 % of the copy rate); with the cache write 16381 tokens of 24 + 4 + 4 heads, 88 us, 5.7 TB/s; 8 tokens
+// of one rank 2.2 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -31,7 +32,13 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 5;  // registers cut to fit: 24571 tokens 121 us with 4, 112 with 5, 114 with 6
-constexpr int64_t kMaxTokens = 0x7FFFFFFF;  // one CTA each
+constexpr int kRows = 4;       // rows of a token that a warp has in flight
+// Tokens a CTA for at most 8 rows a token: one up to a wave of CTAs on 152 SMs, two up to three waves, then
+// four. One rank's 6 + 1 heads, 256 rotated elements, us with 1 / 2 / 4 tokens a CTA, rotary alone and with
+// the cache write: 600 tokens 2.3 / 2.3 / 2.4 and 2.7 / 2.9 / 3.9, 1500 tokens 3.5 / 3.2 / 3.4 and 4.3 /
+// 3.8 / 4.6, 16000 tokens 21.9 / 20.7 / 17.5 and 30.9 / 27.1 / 26.1.
+constexpr int64_t kTokensOne = 760, kTokensTwo = 4560;
+constexpr int64_t kMaxTokens = 0x7FFFFFFF;  // CTAs of a launch
 
 struct RopeParams {
     const void *q, *k, *v;
@@ -100,9 +107,65 @@ __device__ __forceinline__ void rotate(float (&a)[4], float (&b)[4], const float
     }
 }
 
-// kWrite: K and V rows go to the pools as E4M3; else K (if any) to k_out. kRows: rows a warp has in
-// flight.
-template <typename T, bool kHalf, bool kWrite, int kRows>
+// Cosine and sine of pair i at position pos, times the amplitude.
+__device__ __forceinline__ float2 turn_of(const RopeParams& p, int pos, int i) {
+    const uint64_t turn = (uint64_t)(int64_t)pos * p.phases[i];
+    float s, c;
+    // signed 2^-32 turns -> half turns
+    sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);
+    return make_float2(c * p.amplitude, s * p.amplitude);
+}
+
+// The cosines and sines of this lane's four pairs.
+__device__ __forceinline__ void lane_turns(const float2* cs, int lane, float (&c)[4], float (&s)[4]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float4 f = reinterpret_cast<const float4*>(cs)[2 * lane + i];
+        c[2 * i] = f.x;
+        s[2 * i] = f.y;
+        c[2 * i + 1] = f.z;
+        s[2 * i + 1] = f.w;
+    }
+}
+
+// The scale of a row's codes (1 for a row of Q).
+template <bool kWrite>
+__device__ __forceinline__ float scale_of(const RopeParams& p, int h) {
+    return !kWrite || h < 0 ? 1.f : (h < p.num_kv_heads ? *p.k_scale : *p.v_scale);
+}
+
+// Row r of token t: Q rows, then K's, then V's. Its two pieces (at, at + gap) turned, then rounded and
+// stored.
+template <typename T, bool kHalf, bool kWrite>
+__device__ __forceinline__ void put_row(const RopeParams& p, int64_t t, int64_t slot, int r, int at,
+                                        int gap, bool turned, const uint2& wa, const uint2& wb,
+                                        const float (&c)[4], const float (&s)[4], float scale) {
+    const int h = r - p.num_q_heads;
+    const bool is_q = h < 0, is_v = h >= p.num_kv_heads;
+    const int hk = is_v ? h - p.num_kv_heads : h;
+    float a[4], b[4];
+    unpack<T>(wa, a);
+    unpack<T>(wb, b);
+    // (elements past the rotated part are not multiplied: an infinity times a zero sine
+    // would be NaN)
+    if (!is_v && turned) rotate<kHalf>(a, b, c, s);
+    if (is_q || !kWrite) {
+        T* dst = (is_q ? static_cast<T*>(p.q_out) + t * p.q_out_stride + r * kHeadDim
+                       : static_cast<T*>(p.k_out) + t * p.k_out_stride + hk * kHeadDim) +
+                 at;
+        *reinterpret_cast<uint2*>(dst) = pack<T>(a);
+        *reinterpret_cast<uint2*>(dst + gap) = pack<T>(b);
+    } else if (slot < p.num_slots) {
+        uint8_t* dst = (is_v ? p.v_pool : p.k_pool) +
+                       (slot * p.num_kv_heads + hk) * kHeadDim + at;
+        *reinterpret_cast<uint32_t*>(dst) = e4m3x4(a, scale);
+        *reinterpret_cast<uint32_t*>(dst + gap) = e4m3x4(b, scale);
+    }
+}
+
+// One token a CTA, up to kRows rows of it a warp at a time. kWrite: K and V rows go to the pools as E4M3;
+// else K (if any) to k_out.
+template <typename T, bool kHalf, bool kWrite>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_kernel(const RopeParams p) {
     __shared__ __align__(16) float2 cs[kHeadDim / 2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -129,78 +192,104 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_kernel(const RopePa
             wb[i] = __ldcs(reinterpret_cast<const uint2*>(src + at + gap));
         }
         if (r0 == 0) {
-            if (tid < p.rotary_dim / 2) {
-                const uint64_t turn = (uint64_t)(int64_t)pos * p.phases[tid];
-                float s, c;
-                // signed 2^-32 turns -> half turns
-                sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);
-                cs[tid] = make_float2(c * p.amplitude, s * p.amplitude);
-            }
+            if (tid < p.rotary_dim / 2) cs[tid] = turn_of(p, pos, tid);
             __syncthreads();
             if (slot < 0) return;  // padding (the whole CTA agrees)
             if (kWrite && slot >= p.num_slots && tid == 0)
                 atomicOr(p.status, DFLASH_FLAG_SLOT_RANGE);
         }
         float c[4], s[4];
-        if (turned) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float4 f = reinterpret_cast<const float4*>(cs)[2 * lane + i];
-                c[2 * i] = f.x;
-                s[2 * i] = f.y;
-                c[2 * i + 1] = f.z;
-                s[2 * i + 1] = f.w;
-            }
-        }
+        if (turned) lane_turns(cs, lane, c, s);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            const int r = r0 + i * kWarps + warp, h = r - p.num_q_heads;
+            const int r = r0 + i * kWarps + warp;
             if (r >= rows) break;
-            const bool is_q = h < 0, is_v = h >= p.num_kv_heads;
-            const int hk = is_v ? h - p.num_kv_heads : h;
-            float a[4], b[4];
-            unpack<T>(wa[i], a);
-            unpack<T>(wb[i], b);
-            // (elements past the rotated part are not multiplied: an infinity times a zero sine
-            // would be NaN)
-            if (!is_v && turned) rotate<kHalf>(a, b, c, s);
-            if (is_q || !kWrite) {
-                T* dst = (is_q ? static_cast<T*>(p.q_out) + t * p.q_out_stride + r * kHeadDim
-                               : static_cast<T*>(p.k_out) + t * p.k_out_stride + hk * kHeadDim) +
-                         at;
-                *reinterpret_cast<uint2*>(dst) = pack<T>(a);
-                *reinterpret_cast<uint2*>(dst + gap) = pack<T>(b);
-            } else if (slot < p.num_slots) {
-                const float scale = is_v ? *p.v_scale : *p.k_scale;
-                uint8_t* dst = (is_v ? p.v_pool : p.k_pool) +
-                               (slot * p.num_kv_heads + hk) * kHeadDim + at;
-                *reinterpret_cast<uint32_t*>(dst) = e4m3x4(a, scale);
-                *reinterpret_cast<uint32_t*>(dst + gap) = e4m3x4(b, scale);
-            }
+            put_row<T, kHalf, kWrite>(p, t, slot, r, at, gap, turned, wa[i], wb[i], c, s,
+                                      scale_of<kWrite>(p, r - p.num_q_heads));
         }
     }
 }
 
-template <bool kWrite, int kRows>
-cudaError_t launch_rows(const dflash_rope_plan_t* plan, const RopeParams& p, cudaStream_t stream) {
-    const dflash_rope_problem& pr = plan->problem;
-    const bool half = pr.layout == DFLASH_ROPE_HALF;
-    void (*kernel)(RopeParams);
-    if (pr.dtype == DFLASH_FP16)
-        kernel = half ? rope_kernel<__half, true, kWrite, kRows>
-                      : rope_kernel<__half, false, kWrite, kRows>;
+// kTokens tokens a CTA, for at most kWarps rows a token: warp w has row w of each of them.
+template <typename T, bool kHalf, bool kWrite, int kTokens>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_tokens_kernel(const RopeParams p) {
+    __shared__ __align__(16) float2 cs[kTokens][kHeadDim / 2];
+    __shared__ int64_t slots[kTokens];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rows = p.num_q_heads + p.num_kv_heads * (kWrite ? 2 : (p.k ? 1 : 0));
+    const int64_t t0 = (int64_t)blockIdx.x * kTokens, last = p.num_tokens - 1;
+    const bool turned = lane < p.rotary_dim / 8;
+    const int at = kHalf && turned ? 4 * lane : 8 * lane;
+    const int gap = kHalf && turned ? p.rotary_dim / 2 : 4;
+    // (what is past the last row or token is read again and not stored)
+    const int r = min(warp, rows - 1), h = r - p.num_q_heads;
+    const T* src;
+    int64_t stride;
+    if (h < 0) {
+        src = static_cast<const T*>(p.q) + r * kHeadDim;
+        stride = p.q_stride;
+    } else if (h < p.num_kv_heads) {
+        src = static_cast<const T*>(p.k) + h * kHeadDim;
+        stride = p.k_stride;
+    } else {
+        src = static_cast<const T*>(p.v) + (h - p.num_kv_heads) * kHeadDim;
+        stride = p.v_stride;
+    }
+    uint2 wa[kTokens], wb[kTokens];
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        const T* row = src + min(t0 + i, last) * stride;
+        wa[i] = __ldcs(reinterpret_cast<const uint2*>(row + at));
+        wb[i] = __ldcs(reinterpret_cast<const uint2*>(row + at + gap));
+    }
+    const float scale = scale_of<kWrite>(p, h);
+    if (kWrite && tid < kTokens) {
+        const int64_t slot = p.slots[min(t0 + tid, last)];
+        if (slot >= p.num_slots) atomicOr(p.status, DFLASH_FLAG_SLOT_RANGE);
+        slots[tid] = slot;
+    }
+    constexpr int kPairs = kHeadDim / 2, kEach = kThreads / kPairs;
+    if (tid % kPairs < p.rotary_dim / 2) {
+#pragma unroll
+        for (int i = tid / kPairs; i < kTokens; i += kEach)
+            cs[i][tid % kPairs] = turn_of(p, p.positions[min(t0 + i, last)], tid % kPairs);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        const int64_t t = t0 + i;
+        if (t > last || warp >= rows) return;
+        const int64_t slot = kWrite ? slots[i] : 0;
+        if (slot < 0) continue;  // padding
+        float c[4], s[4];
+        if (turned) lane_turns(cs[i], lane, c, s);
+        put_row<T, kHalf, kWrite>(p, t, slot, r, at, gap, turned, wa[i], wb[i], c, s, scale);
+    }
+}
+
+template <typename T, bool kHalf, bool kWrite>
+cudaError_t launch_as(const RopeParams& p, cudaStream_t stream) {
+    const int rows = p.num_q_heads + p.num_kv_heads * (kWrite ? 2 : (p.k ? 1 : 0));
+    auto ctas = [&](int tokens) { return (unsigned)((p.num_tokens + tokens - 1) / tokens); };
+    if (rows > kWarps)
+        rope_kernel<T, kHalf, kWrite><<<ctas(1), kThreads, 0, stream>>>(p);
+    else if (p.num_tokens <= kTokensOne)
+        rope_tokens_kernel<T, kHalf, kWrite, 1><<<ctas(1), kThreads, 0, stream>>>(p);
+    else if (p.num_tokens <= kTokensTwo)
+        rope_tokens_kernel<T, kHalf, kWrite, 2><<<ctas(2), kThreads, 0, stream>>>(p);
     else
-        kernel = half ? rope_kernel<__nv_bfloat16, true, kWrite, kRows>
-                      : rope_kernel<__nv_bfloat16, false, kWrite, kRows>;
-    kernel<<<(unsigned)p.num_tokens, kThreads, 0, stream>>>(p);
+        rope_tokens_kernel<T, kHalf, kWrite, 4><<<ctas(4), kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
 template <bool kWrite>
 cudaError_t launch(const dflash_rope_plan_t* plan, const RopeParams& p, cudaStream_t stream) {
-    const int rows = p.num_q_heads + p.num_kv_heads * 2;
-    return rows <= kWarps ? launch_rows<kWrite, 1>(plan, p, stream)
-                          : launch_rows<kWrite, 4>(plan, p, stream);
+    const bool half = plan->problem.layout == DFLASH_ROPE_HALF;
+    if (plan->problem.dtype == DFLASH_FP16)
+        return half ? launch_as<__half, true, kWrite>(p, stream)
+                    : launch_as<__half, false, kWrite>(p, stream);
+    return half ? launch_as<__nv_bfloat16, true, kWrite>(p, stream)
+                : launch_as<__nv_bfloat16, false, kWrite>(p, stream);
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

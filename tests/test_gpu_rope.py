@@ -201,6 +201,42 @@ def test_kv_write(layout, d, scaling, T, heads, P, dtype, fused):
     assert r.read_flags() == 0
 
 
+@pytest.mark.parametrize("T", [759, 760, 761, 762, 4560, 4561, 4563, 9002])
+@pytest.mark.parametrize("layout,d,dtype", [("half", 256, torch.float16),
+                                            ("interleaved", 48, torch.bfloat16)])
+@pytest.mark.parametrize("heads", [(6, 1), (2, 3), (1, 1)])
+def test_many_tokens_of_few_heads_are_as_a_few_at_a_time(T, layout, d, dtype, heads):
+    Hq, Hkv = heads
+    q, k, v, pos = make(T + d, T, Hq, Hkv, dtype, 100000, True)
+    pages = -(-T // 16)
+    r, _, _ = rotary(Hq, Hkv, d, layout, dtype, page_size=16, num_pages=pages)
+    g = torch.Generator().manual_seed(T)
+    slots = torch.randperm(pages * 16, generator=g)[:T]
+    slots[::7] = -1
+    slots[T - 2] = pages * 16  # past the pool: no write, a flag
+    slots = slots.cuda()
+    one = torch.ones(1, device="cuda")
+
+    def run(parts):
+        pools = [torch.full((pages, 16, Hkv, D), 7, dtype=torch.uint8, device="cuda")
+                 for _ in range(2)]
+        qo = torch.full((T, Hq, D), 5.0, dtype=dtype, device="cuda")
+        qa = torch.empty((T, Hq, D), dtype=dtype, device="cuda")
+        ka = torch.empty((T, Hkv, D), dtype=dtype, device="cuda")
+        for part in torch.arange(T).split(parts):
+            s = slice(int(part[0]), int(part[-1]) + 1)
+            r.kv_write(q[s], k[s], v[s], pos[s], slots[s], one, one, *pools, q_out=qo[s])
+            r.apply(q[s], k[s], pos[s], q_out=qa[s], k_out=ka[s])
+        assert r.read_flags(clear=True) == 0x40
+        return [qo, qa, ka] + pools
+    for a, b in zip(run(T), run(500)):
+        assert torch.equal(a, b)
+    qa, ka = r.apply(q, k, pos)
+    qi, ki = q.contiguous().clone(), k.contiguous().clone()
+    r.apply(qi, ki, pos, q_out=qi, k_out=ki)
+    assert torch.equal(qa, qi) and torch.equal(ka, ki)
+
+
 def test_kv_write_special_values_and_slots_past_the_pool():
     r, _, _ = rotary(2, 1, 64, "half", torch.float16, page_size=16, num_pages=1)
     q, k, v, pos = make(1, 3, 2, 1, torch.float16, 9)
