@@ -13,7 +13,7 @@
 // heads, into shared memory. A lane has four pairs, whole: in the half layout 4 elements of each half
 // (two 8-byte pieces), interleaved 8 in a row; lanes past the rotated part pass 8 elements through.
 // Bound by HBM for many tokens, by latency for few: 24571 tokens of 24 + 4 heads in bf16, 112 us, 6.3 TB/s
-// (93 % of the copy rate); with the cache write 16381 tokens of 24 + 4 + 4 heads, 88 us, 5.7 TB/s; 8 tokens
+// (93 % of the copy rate); with the cache write 16381 tokens of 24 + 4 + 4 heads, 87 us, 5.8 TB/s; 8 tokens
 // of one rank 2.2 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -135,11 +135,11 @@ __device__ __forceinline__ float scale_of(const RopeParams& p, int h) {
 }
 
 // Row r of token t: Q rows, then K's, then V's. Its two pieces (at, at + gap) turned, then rounded and
-// stored.
-template <typename T, bool kHalf, bool kWrite>
+// stored, by the scale that scale_now(its head past Q's) gives.
+template <typename T, bool kHalf, bool kWrite, typename Scale>
 __device__ __forceinline__ void put_row(const RopeParams& p, int64_t t, int64_t slot, int r, int at,
                                         int gap, bool turned, const uint2& wa, const uint2& wb,
-                                        const float (&c)[4], const float (&s)[4], float scale) {
+                                        const float (&c)[4], const float (&s)[4], Scale scale_now) {
     const int h = r - p.num_q_heads;
     const bool is_q = h < 0, is_v = h >= p.num_kv_heads;
     const int hk = is_v ? h - p.num_kv_heads : h;
@@ -156,6 +156,7 @@ __device__ __forceinline__ void put_row(const RopeParams& p, int64_t t, int64_t 
         *reinterpret_cast<uint2*>(dst) = pack<T>(a);
         *reinterpret_cast<uint2*>(dst + gap) = pack<T>(b);
     } else if (slot < p.num_slots) {
+        const float scale = scale_now(h);
         uint8_t* dst = (is_v ? p.v_pool : p.k_pool) +
                        (slot * p.num_kv_heads + hk) * kHeadDim + at;
         *reinterpret_cast<uint32_t*>(dst) = e4m3x4(a, scale);
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_kernel(const RopePa
             const int r = r0 + i * kWarps + warp;
             if (r >= rows) break;
             put_row<T, kHalf, kWrite>(p, t, slot, r, at, gap, turned, wa[i], wb[i], c, s,
-                                      scale_of<kWrite>(p, r - p.num_q_heads));
+                                      [&](int hs) { return scale_of<kWrite>(p, hs); });
         }
     }
 }
@@ -263,7 +264,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_tokens_kernel(const
         if (slot < 0) continue;  // padding
         float c[4], s[4];
         if (turned) lane_turns(cs[i], lane, c, s);
-        put_row<T, kHalf, kWrite>(p, t, slot, r, at, gap, turned, wa[i], wb[i], c, s, scale);
+        put_row<T, kHalf, kWrite>(p, t, slot, r, at, gap, turned, wa[i], wb[i], c, s,
+                                  [&](int) { return scale; });
     }
 }
 
