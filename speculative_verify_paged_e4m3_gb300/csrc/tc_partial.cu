@@ -20,11 +20,15 @@
 //    2^-25 of the row maximum.
 //  * The probabilities, taken as p = 2^(s - m) * 2^score with s = 4 and a reference max m (so
 //    p <= 2^8, see below), are split the same way into three E4M3 terms p = h + m/16 + l/256
-//    (h and m truncated to 4 significant bits, residuals exact, l rounded: relative error about
-//    2^-12, finer than an FP16 P), stacked on N, so O^T accumulates three FP32 terms that are
-//    summed at the end. The shift s keeps the leading
-//    term out of E4M3's subnormal range down to p = 2^-10 of the reference: below 2^-6 the
-//    leading term only has a 2^-9 grid, and over 10^5 keys those roundings add up.
+//    (h and m cut to 4 significant bits on E4M3's grid, residuals exact, l rounded: relative error
+//    about 2^-12, finer than an FP16 P), stacked on N, so O^T accumulates three FP32 terms that are
+//    summed at the end. Below 2^-6 an E4M3 number is a multiple of 2^-9, so that beside a large
+//    probability small ones are known to a step of 2^-17 (l's 2^-9 over 256). Every h and m is a value
+//    that E4M3 has, so that what it leaves out is in the term after it: a conversion that rounds a
+//    term's value once more loses up to 2^-10 of h unseen, and 3500 keys 16 bits below a strong one gave
+//    0.099 for 0.070. l is offset within its last step by an amount of the key's own, 128 evenly spaced
+//    ones in a tile: 10^5 probabilities of about one size would otherwise all be rounded the same way
+//    (all of them to zero below 2^-18), and now err by 2^-25 each in the mean.
 //  * Softmax: keys on tensor-memory lanes (thread = key); RP/16 warpgroups of 16 query rows each.
 //    Each keeps, per row, a reference max that only moves when a score exceeds it by more than
 //    2^(8 - s) (then the warpgroup rescales its O columns in tensor memory), and FP32 row sums of
@@ -97,9 +101,9 @@ constexpr uint32_t kHalfOffset = 1024;               // 8 keys x 128 bytes
 constexpr uint64_t kWaitLimitNs = 200ull * 1000 * 1000;
 constexpr int kRowCache = 512;  // 16-key chunks of a split whose source row is looked up up front
 constexpr float kPShift = 4.f;         // s: probabilities are scaled by 2^s before the split
-// s of the shared-prefix views: a finer grid for small probabilities beside large ones, for more moves
-// of the reference. Scores of spread 4 on 5 % of the keys: output error 2.2e-4 to 2.5e-4 of its norm (2.1e-4
-// is the FP16 output's own rounding) against 2.6e-4 to 5.1e-4 with s = 4; 0 to 7 % more time.
+// s of the shared-prefix views, whose splits may hold 10^5 keys: a step a quarter as large beside a
+// strong key, for more moves of the reference (0 to 7 % more time). Scores of spread 4 on 5 % of the keys:
+// output error 2.1e-4 of its norm, the FP16 output's own rounding, with either s.
 constexpr float kViewShift = 6.f;
 constexpr float kLazyThreshold = 8.f;  // largest shifted probability exponent, 8 - s above the max
 
@@ -844,7 +848,12 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         if (lane < kGroupRows) sm.nmcur[g][wq][lane] = INFINITY;
         __syncwarp();
         const uint64_t k16th = pk2(0.0625f, 0.0625f), k256th = pk2(0.00390625f, 0.00390625f);
-        const uint64_t k16 = pk2(16.f, 16.f);
+        const uint64_t k16 = pk2(16.f, 16.f), km16 = pk2(-16.f, -16.f), k256 = pk2(256.f, 256.f);
+        const uint64_t kGrid = pk2(24576.f, 24576.f);  // 1.5 * 2^14: its last bit is 2^-9
+        // this key's offset of l: (0 .. 127 in bit-reversed order of the keys - 63.5) / 128 of 2^-9,
+        // inside half a step, so that a probability of zero stays zero
+        const float offset = ((float)(__brev((uint32_t)st) >> 25) - 63.5f) * 0x1p-16f;
+        const uint64_t offset2 = pk2(offset, offset);
         constexpr uint64_t kTrunc4 = 0xFFF00000FFF00000ull;  // sign, exponent, 3 mantissa bits
         for (int t = 0; t < ntiles; ++t) {
             const int tile0 = start + t * kTile;
@@ -929,12 +938,14 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                                              ? ex2(hi2(e[jj]))
                                              : 0.f;
                         pv[jj] = pk2(p0, p1);
-                        // h, m: truncations to 4 significant bits (mantissa masked), so p - h and
-                        // r - m are exact and the three terms sum to p up to l's final rounding
-                        const uint64_t hv = pv[jj] & kTrunc4;
-                        const uint64_t r = mul2(sub2(pv[jj], hv), k16);
-                        const uint64_t mv = r & kTrunc4;
-                        const uint64_t lv = mul2(sub2(r, mv), k16);
+                        // h, m: truncations to 4 significant bits (mantissa masked), brought to
+                        // multiples of 2^-9 by the addition of a number whose last bit that is: E4M3
+                        // has them, so p - h and 16 (p - h) - m are exact and the three terms sum to
+                        // p up to l's final rounding
+                        const uint64_t hv = sub2(add2(pv[jj] & kTrunc4, kGrid), kGrid);
+                        const uint64_t r = sub2(pv[jj], hv);
+                        const uint64_t mv = sub2(fma2(r & kTrunc4, k16, kGrid), kGrid);
+                        const uint64_t lv = fma2(mv, km16, fma2(r, k256, offset2));
                         ch[q] = f32x2_to_e4m3x2(hv);
                         cm[q] = f32x2_to_e4m3x2(mv);
                         cl[q] = f32x2_to_e4m3x2(lv);

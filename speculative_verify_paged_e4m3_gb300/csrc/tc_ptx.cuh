@@ -123,7 +123,9 @@ __device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float lo, float hi) {
 // A pair lives in a 64-bit register (low word = first element). Only used where every result is
 // exact or where the rounding does not matter: on this GPU the code generator may evaluate
 // chains of these operations without rounding each step (a Veltkamp split c - (c - x) with
-// c = x(2^20 + 1) came back as x), so they must not carry error-free-transformation tricks.
+// c = x(2^20 + 1) came back as x), so they must not carry error-free-transformation tricks. (Adding a
+// large constant and taking it off again does round; tests of small probabilities beside a strong key
+// hold every kernel that does so to it.)
 __device__ __forceinline__ uint64_t pk2(float lo, float hi) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
