@@ -22,13 +22,16 @@
 //    K, 10-11 decode V, 12 issues the score products of the pair and 13 its PV (one thread each, in
 //    the leader SM alone), 14 and 15 copy the codes of K and of V (TMA, three and two tiles
 //    ahead).
-//  * Probabilities are p = 2^(score - m) for a reference m that is set 2^4 above the first tile's
+//  * Probabilities are p = 2^(score - m) for a reference m that is set 2^4 below the first tile's
 //    maximum, and moves only when a row's probabilities of 48 keys sum to more than 2^15 (so that all
 //    are inside FP16): scores, exponentials and sums are one pass with no maximum in front of it. When
-//    it moves, the rows' O columns are rescaled in place and the tile is done again, which stalls the
-//    pair for more than a tile; with scores of spread 4 over 5 % of the keys the first tile's maximum
-//    alone was passed in most tiles. Below 2^-14 FP16 has a fixed grid of 2^-24: noise of 2^-25 a key
-//    beside a sum of at least 2^-4, 2^-13 of it at worst over 2^17 keys.
+//    one row's moves, those of the SM's other rows go up to 2^4 below what they have in that tile too
+//    (one after the other they made 16 x 8 tokens with scores of spread 4 on 5 % of 32768 keys 117 us, so
+//    109). The rows' O columns are rescaled in place and the tile is done again, which stalls the pair
+//    for more than a tile. Below 2^-14 FP16 has a fixed step of 2^-24, half of which each of N keys may
+//    lose, all the same way, beside a sum of at least 2^4: N 2^-29, 2^-12 of 2^17 keys. (With m 2^4 above the
+//    first maximum that case takes 100 us, but a strong key in front of 65536 others lost 2^-5: 0.060 for
+//    0.042, 21 bits below it. At its maximum plain scores cost the same, and 17 bits lost too much.)
 //  * Pairs take equal shares of all (KV head, row block) units' tiles (prefix_pairs.cuh); a share may
 //    end in the middle of a unit, the combine puts the parts together.
 //  * Bound by the tensor pipe and by what feeds it: a tile takes 1912 clocks (990 ns), its products by
@@ -63,7 +66,7 @@ constexpr int kQkWarp = kSoftWarps + 2 * kDecodeWarps, kPvWarp = kQkWarp + 1;
 constexpr int kCopyWarp = kPvWarp + 1;  // and the next one
 constexpr int kThreads = 32 * (kCopyWarp + 2);  // 16 warps: 128 registers a thread
 constexpr uint64_t kWaitLimitNs = 200ull * 1000 * 1000;
-constexpr float kHeadroom = 4.f;    // a reference is set 2^4 above the maximum that moves it
+constexpr float kMaxExp = 4.f;      // a reference is set 2^4 below the maximum that moves it
 constexpr float kMaxSum = 32768.f;  // a row's probabilities of a half tile sum to this at most
 
 // Shared memory: Q | K stages | V stages | codes of K | codes of V | Small. All operands are 128-byte swizzled: Q and K
@@ -651,8 +654,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     soft_sync();
                     mx = fmaxf(mx, sm.part[hf ^ 1][row]);
                     mx *= c;
-                    // (48 keys that sum to over 2^15 have one above 2^9)
-                    const float mo = -nm, mn = mx > mo + 9.f ? mx + kHeadroom : mo;
+                    // (48 keys that sum to over 2^15 have one above 2^9: that row's reference rises)
+                    const float mo = -nm, mn = fmaxf(mo, mx - kMaxExp);
                     const float alpha = mn == -INFINITY ? 1.f : ex2(mo - mn);
                     nm = -mn;
                     lsum *= alpha;

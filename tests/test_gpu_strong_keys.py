@@ -12,7 +12,8 @@ truncating accumulator's 2^-24 in each of at most 4096 products over 16 keys giv
 Beside that the fixed grid under the smallest normal probability: step 2^-17, sink at 2^4 or more. Equal
 keys are offset within their step by 128 evenly spaced fractions, so that the mean of 128 is within 2^-8 of a step,
 65536 * 2^-25 / 2^6 = 2^-15 (16384 keys at 2^4: 2^-15); for random keys the errors are independent, below half a
-step each: 6 standard deviations are 6 * 2^8 * 2^-18 / 2^6 < 2^-13 (2^7 and 2^4: 6 * 2^-15 < 2^-12). So
+step each: 6 standard deviations are 6 * 2^8 * 2^-18 / 2^6 < 2^-13 (2^7 and 2^4: 6 * 2^-15 < 2^-12). FP16 (the pair
+kernel), step 2^-24, sink at 2^4: 65536 * 2^-25 / 2^4 = 2^-13 if every key errs the same way. So
 2^-9 |out| + 2^-12. The log-sum-exp has the plain attention's 1e-5 max(1, |lse|).
 """
 import math
@@ -67,18 +68,21 @@ def check(out, lse, scores, values, n, q_len):
         assert (lse[:, i].double() - z).abs().max().item() <= 1e-5 * max(1.0, abs(z.item()))
 
 
-@pytest.mark.parametrize("kernel", [1], ids=["rows"])
+@pytest.mark.parametrize("kernel", [1, 2], ids=["rows", "pairs"])
 @pytest.mark.parametrize("spread", [False, True], ids=["equal", "spread"])
 @pytest.mark.parametrize("gap", GAPS)
 def test_over_a_shared_prefix(kernel, spread, gap):
-    """65536 shared keys, each row's in a single split."""
+    """65536 shared keys, each row's in a single split or segment."""
     from speculative_verify_paged_e4m3_gb300 import binding as B
-    n, P, Hq, Hkv, batch, q_len = 65536, 64, 32, 4, 40, 8
+    n, P, Hq, Hkv, batch, q_len = 65536, 64, 32, 4, 80, 8
     kp, vp, ks, scores, values = keys(n, gap, spread, P, Hkv)
     pages = n // P
     table = torch.arange(pages, dtype=torch.int32, device="cuda")
     att = B.SharedPrefixAttention(batch, q_len, Hq, Hkv, D, P, pages, pages, n, n, kernel=kernel)
-    assert att.plan.prefix_splits == 1
+    if kernel == 1:
+        assert att.plan.prefix_splits == 1
+    else:  # no fewer units than pairs: most segments are whole units
+        assert att.plan.prefix_row_blocks * Hkv >= att.plan.prefix_splits
     one = torch.ones(1, device="cuda")
     q = torch.ones((batch, q_len, Hq, D), dtype=torch.float16, device="cuda")
     out, lse = att(q, kp, vp, table, torch.tensor([n], dtype=torch.int32, device="cuda"),
