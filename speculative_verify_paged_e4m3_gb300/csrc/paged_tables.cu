@@ -228,9 +228,12 @@ extern "C" int dflash_paged_tables(const dflash_paged_tables_problem* pr,
     int64_t grid = by_tokens > by_rows ? by_tokens : by_rows;
     if (grid > 304) grid = 304;
     const size_t smem = 2 * (size_t)(pr->batch + 1) * sizeof(long long);
-    if (smem > 48 * 1024 &&
+    // 48 KB a launch gets without asking, the kernel's own arrays included. What is asked for is the most
+    // that any batch takes: a smaller amount would be one less for a call on another thread.
+    constexpr size_t kMostSmem = 2 * (size_t)(kMaxBatch + 1) * sizeof(long long);
+    if (smem > 32 * 1024 &&
         cudaFuncSetAttribute(paged_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem) != cudaSuccess) {
+                             (int)kMostSmem) != cudaSuccess) {
         cudaGetLastError();
         return DFLASH_ERR_CUDA;
     }
