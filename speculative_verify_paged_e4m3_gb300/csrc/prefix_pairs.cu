@@ -543,9 +543,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int hf = warp >> 2, row = tid & (kRows - 1);  // row of this SM's = tensor-memory lane
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         // D^-1/2 = 1/16, log2 units. Row maxima below are taken before this factor, so it has to be
-        // positive: a negative scale's sign goes into Q, a scale of zero becomes a tiny one.
+        // positive: a negative scale's sign goes into Q, a scale of zero becomes a tiny one (and one that
+        // is not a number stays so).
         const float c_signed = __ldg(p.k_scale) * 0.0625f * kLog2e;
-        const float c = fmaxf(fabsf(c_signed), 1e-30f);
+        const float c = fabsf(c_signed) < 1e-30f ? 1e-30f : fabsf(c_signed);
         const uint32_t q_sign = c_signed < 0.f ? 0x80008000u : 0u;
         const float vs = __ldg(p.v_scale);
         const uint64_t c2 = pk2(c, c);
