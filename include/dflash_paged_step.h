@@ -53,7 +53,8 @@ extern "C" {
  *   token_starts   [batch + 1] first token of each request, then their number
  *   positions      int32 [max_tokens]; 0 past the last token
  *   slots          int64 [max_tokens]; -1 past the last token, for a token without a page of its
- *                  own, and for a token inside the shared pages (those are read only)
+ *                  own, and for a token inside the shared pages (those are read only; its query is
+ *                  needed all the same: dflash_rope_kv_write_live with token_starts + batch)
  * Tokens past max_tokens have no position or slot (DFLASH_FLAG_TOKENS_DROPPED; their pages are
  * handed out all the same, and token_starts stops at max_tokens). Once the free list ends, the
  * requests' remaining pages in request order become -1 in the table, their tokens' slots -1, and
@@ -177,7 +178,9 @@ int dflash_rope_apply(const dflash_rope_plan_t* plan, int64_t num_tokens, const 
  * (page * page_size + offset in the page, as dflash_paged_tables gives it).
  *   k, v    [num_tokens, Hkv, head_dim], strides k_stride, v_stride
  *   slots   int64 [num_tokens]. A token with a negative slot is padding: nothing of it is written,
- *           q_out neither. A slot past the pool writes q_out alone (DFLASH_FLAG_SLOT_RANGE).
+ *           q_out neither (dflash_rope_kv_write_live tells padding from tokens that have a query
+ *           but no slot of their own). A slot past the pool writes q_out alone
+ *           (DFLASH_FLAG_SLOT_RANGE).
  *   k_pool, v_pool  as in dflash_verify_attn.h, 8-byte aligned
  *   k_scale, v_scale  one FP32 each (device)
  * Each element becomes the E4M3FN code of x / scale by the rule of dflash_verify_attn_kv_write (one
@@ -191,6 +194,22 @@ int dflash_rope_kv_write(const dflash_rope_plan_t* plan, int64_t num_tokens, con
                          const uint64_t* phases, const float* k_scale, const float* v_scale,
                          void* q_out, int64_t q_out_stride, void* k_pool, void* v_pool,
                          int32_t* status, void* cuda_stream);
+
+/*
+ * The same with the number of tokens that are not padding: num_live, one int32 (device), what
+ * dflash_paged_tables leaves in token_starts[batch]. A token below it with a negative slot has its
+ * query rotated and nothing written to the pools. Such tokens are ordinary: a request whose whole
+ * prompt is in the shared pages computes its last token's query again, at a position inside them.
+ * From num_live on, counted from this call's first token, a negative slot is padding, as above
+ * (num_live NULL: everywhere, as above).
+ */
+int dflash_rope_kv_write_live(const dflash_rope_plan_t* plan, int64_t num_tokens, const void* q,
+                              int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                              int64_t v_stride, const int32_t* positions, const int64_t* slots,
+                              const int32_t* num_live, const uint64_t* phases,
+                              const float* k_scale, const float* v_scale, void* q_out,
+                              int64_t q_out_stride, void* k_pool, void* v_pool, int32_t* status,
+                              void* cuda_stream);
 
 /* ------------------------------------------------------------------------------------------------
  * Attention of a batch over a shared prefix.

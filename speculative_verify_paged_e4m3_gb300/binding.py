@@ -65,6 +65,7 @@ EXPORTED = (
     "dflash_rope_plan",
     "dflash_rope_apply",
     "dflash_rope_kv_write",
+    "dflash_rope_kv_write_live",
     "dflash_prefix_attn_plan",
     "dflash_prefix_attn_forward",
     "dflash_verify_attn_status_string",
@@ -172,6 +173,8 @@ def load_library() -> ctypes.CDLL:
             lib.dflash_rope_apply.argtypes = [rp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64,
                                               vp]
             lib.dflash_rope_kv_write.argtypes = [rp, i64, vp, i64, vp, i64, vp, i64] + [vp] * 6 + [
+                i64] + [vp] * 4
+            lib.dflash_rope_kv_write_live.argtypes = [rp, i64, vp, i64, vp, i64, vp, i64] + [vp] * 7 + [
                 i64] + [vp] * 4
             xp = ctypes.POINTER(PrefixAttnPlan)
             lib.dflash_prefix_attn_plan.argtypes = [ctypes.POINTER(PrefixAttnProblem), xp]
@@ -603,13 +606,13 @@ _ROPE_DTYPES = {torch.float16: DFLASH_FP16, torch.bfloat16: DFLASH_BF16}
 class Rotary(_OnDevice):
     """Rotary positions of one model's heads: apply() rotates Q and K, kv_write() rotates Q and
     writes the rotated K and V into the paged E4M3 pools (dflash_rope_apply,
-    dflash_rope_kv_write)."""
+    dflash_rope_kv_write_live)."""
 
     def __init__(self, num_q_heads, num_kv_heads, head_dim, rotary_dim=None, layout="half",
                  dtype=torch.float16, base=10000.0, scaling="none", factor=1.0,
                  trained_context=1, beta_fast=32.0, beta_slow=1.0, low_turns=1.0, high_turns=4.0,
                  page_size=16, num_pages=1, device=None, status=None):
-        super().__init__(device, "dflash_rope_apply", "dflash_rope_kv_write")
+        super().__init__(device, "dflash_rope_apply", "dflash_rope_kv_write_live")
         if layout not in _ROPE_LAYOUTS or scaling not in _ROPE_SCALINGS:
             raise ValueError(f"unknown layout {layout!r} or scaling {scaling!r}")
         if dtype not in _ROPE_DTYPES:
@@ -650,9 +653,12 @@ class Rotary(_OnDevice):
         return q_out, k_out
 
     def kv_write(self, q, k, v, positions, slots, k_scale, v_scale, k_pool, v_pool, q_out=None,
-                 stream=None):
+                 stream=None, token_starts=None):
         """q_out: q [T, Hq, D] rotated to positions [T] (it may be q itself); the rotated k and v
-        [T, Hkv, D] go to the pools at slots [T]. A token with a negative slot is left alone."""
+        [T, Hkv, D] go to the pools at slots [T]. A token with a negative slot is padding and left
+        alone (its row of a q_out made here is not initialised). With token_starts (of PagedTables) only
+        tokens past its last entry are: those inside the shared pages have no slot to write to either,
+        but a query."""
         (Hq, Hkv, D), T, dt, ix = self.shape, positions.numel(), self.dtype, self._index
         q_shape, k_shape = (T, Hq, D), (T, Hkv, D)
         if q_out is None:
@@ -667,9 +673,16 @@ class Rotary(_OnDevice):
         _want("v_scale", v_scale, torch.float32, (1,), ix)
         _want("k_pool", k_pool, torch.uint8, self.pool_shape, ix)
         _want("v_pool", v_pool, torch.uint8, self.pool_shape, ix)
-        self._launch("dflash_rope_kv_write", stream, self._plan_ref, T, q.data_ptr(), qs,
+        live = None
+        if token_starts is not None:
+            n = token_starts.numel()
+            _want("token_starts", token_starts, torch.int32, (n,), ix)
+            if n < 1:
+                raise ValueError("token_starts: want at least one entry")
+            live = token_starts.data_ptr() + 4 * (n - 1)
+        self._launch("dflash_rope_kv_write_live", stream, self._plan_ref, T, q.data_ptr(), qs,
                      k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(), slots.data_ptr(),
-                     self.phases.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                     live, self.phases.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                      q_out.data_ptr(), qo, k_pool.data_ptr(), v_pool.data_ptr(),
                      self.status.data_ptr())
         return q_out

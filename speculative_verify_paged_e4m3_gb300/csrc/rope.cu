@@ -45,6 +45,7 @@ struct RopeParams {
     int64_t q_stride, k_stride, v_stride;
     const int32_t* positions;
     const int64_t* slots;
+    const int32_t* num_live;  // null: every token with a negative slot is padding
     const uint64_t* phases;
     const float *k_scale, *v_scale;
     void *q_out, *k_out;
@@ -128,6 +129,12 @@ __device__ __forceinline__ void lane_turns(const float2* cs, int lane, float (&c
     }
 }
 
+// Tokens from here on are padding if their slot is negative.
+template <bool kWrite>
+__device__ __forceinline__ int64_t live_tokens(const RopeParams& p) {
+    return kWrite && p.num_live ? *p.num_live : 0;
+}
+
 // The scale of a row's codes (1 for a row of Q).
 template <bool kWrite>
 __device__ __forceinline__ float scale_of(const RopeParams& p, int h) {
@@ -155,7 +162,7 @@ __device__ __forceinline__ void put_row(const RopeParams& p, int64_t t, int64_t 
                  at;
         *reinterpret_cast<uint2*>(dst) = pack<T>(a);
         *reinterpret_cast<uint2*>(dst + gap) = pack<T>(b);
-    } else if (slot < p.num_slots) {
+    } else if (slot >= 0 && slot < p.num_slots) {
         const float scale = scale_now(h);
         uint8_t* dst = (is_v ? p.v_pool : p.k_pool) +
                        (slot * p.num_kv_heads + hk) * kHeadDim + at;
@@ -172,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_kernel(const RopePa
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rows = p.num_q_heads + p.num_kv_heads * (kWrite ? 2 : (p.k ? 1 : 0));
     const int64_t t = blockIdx.x;
-    const int64_t slot = kWrite ? p.slots[t] : 0;
+    const int64_t slot = kWrite ? p.slots[t] : 0, live = live_tokens<kWrite>(p);
     const int pos = p.positions[t];
     const T* q = static_cast<const T*>(p.q) + t * p.q_stride;
     const T* k = static_cast<const T*>(p.k) + t * p.k_stride;
@@ -195,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_kernel(const RopePa
         if (r0 == 0) {
             if (tid < p.rotary_dim / 2) cs[tid] = turn_of(p, pos, tid);
             __syncthreads();
-            if (slot < 0) return;  // padding (the whole CTA agrees)
+            if (slot < 0 && t >= live) return;  // padding (the whole CTA agrees)
             if (kWrite && slot >= p.num_slots && tid == 0)
                 atomicOr(p.status, DFLASH_FLAG_SLOT_RANGE);
         }
@@ -244,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_tokens_kernel(const
         wb[i] = __ldcs(reinterpret_cast<const uint2*>(row + at + gap));
     }
     const float scale = scale_of<kWrite>(p, h);
+    const int64_t live = live_tokens<kWrite>(p);
     if (kWrite && tid < kTokens) {
         const int64_t slot = p.slots[min(t0 + tid, last)];
         if (slot >= p.num_slots) atomicOr(p.status, DFLASH_FLAG_SLOT_RANGE);
@@ -261,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_tokens_kernel(const
         const int64_t t = t0 + i;
         if (t > last || warp >= rows) return;
         const int64_t slot = kWrite ? slots[i] : 0;
-        if (slot < 0) continue;  // padding
+        if (slot < 0 && t >= live) continue;  // padding
         float c[4], s[4];
         if (turned) lane_turns(cs[i], lane, c, s);
         put_row<T, kHalf, kWrite>(p, t, slot, r, at, gap, turned, wa[i], wb[i], c, s,
@@ -442,6 +450,18 @@ int dflash_rope_kv_write(const dflash_rope_plan_t* plan, int64_t num_tokens, con
                          const uint64_t* phases, const float* k_scale, const float* v_scale,
                          void* q_out, int64_t q_out_stride, void* k_pool, void* v_pool,
                          int32_t* status, void* cuda_stream) {
+    return dflash_rope_kv_write_live(plan, num_tokens, q, q_stride, k, k_stride, v, v_stride,
+                                     positions, slots, nullptr, phases, k_scale, v_scale, q_out,
+                                     q_out_stride, k_pool, v_pool, status, cuda_stream);
+}
+
+int dflash_rope_kv_write_live(const dflash_rope_plan_t* plan, int64_t num_tokens, const void* q,
+                              int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                              int64_t v_stride, const int32_t* positions, const int64_t* slots,
+                              const int32_t* num_live, const uint64_t* phases,
+                              const float* k_scale, const float* v_scale, void* q_out,
+                              int64_t q_out_stride, void* k_pool, void* v_pool, int32_t* status,
+                              void* cuda_stream) {
     const int rc = check_plan(plan);
     if (rc != DFLASH_OK) return rc;
     const dflash_rope_problem& pr = plan->problem;
@@ -452,11 +472,11 @@ int dflash_rope_kv_write(const dflash_rope_plan_t* plan, int64_t num_tokens, con
         !positions || !aligned(positions, 4) || !slots || !aligned(slots, 8) || !phases ||
         !aligned(phases, 8) || !k_scale || !aligned(k_scale, 4) || !v_scale ||
         !aligned(v_scale, 4) || !k_pool || !aligned(k_pool, 8) || !v_pool ||
-        !aligned(v_pool, 8) || !status || !aligned(status, 4) ||
+        !aligned(v_pool, 8) || !status || !aligned(status, 4) || !aligned(num_live, 4) ||
         (q == q_out && q_stride != q_out_stride))
         return DFLASH_ERR_INVALID_ARGUMENT;
     const void* const outs[] = {q_out, k_pool, v_pool, status};
-    const void* const others[] = {k, v, positions, slots, phases, k_scale, v_scale};
+    const void* const others[] = {k, v, positions, slots, phases, k_scale, v_scale, num_live};
     if (!distinct(outs, others) || k_pool == q || v_pool == q || status == q)
         return DFLASH_ERR_INVALID_ARGUMENT;
     RopeParams p = {};
@@ -468,6 +488,7 @@ int dflash_rope_kv_write(const dflash_rope_plan_t* plan, int64_t num_tokens, con
     p.v_stride = v_stride;
     p.positions = positions;
     p.slots = slots;
+    p.num_live = num_live;
     p.phases = phases;
     p.k_scale = k_scale;
     p.v_scale = v_scale;
