@@ -114,16 +114,46 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
-// Arrive on the barrier at the same place in the leader's shared memory. What the arrival orders are
-// operands of the products (tensor memory, and shared memory through the async proxy), which the fences
-// before it cover; the default scope keeps it free of a cluster-wide fence of ordinary memory (with
-// .release.cluster an arrival took about 1200 clocks).
+// Arrive on the barrier at the same place in the leader's shared memory. For tensor memory: what it holds is
+// ordered by the tcgen05 fences around the arrival and the leader's wait, and the arrival has nothing to
+// release.
 __device__ __forceinline__ void arrive_leader(uint32_t bar) {
     asm volatile(
         "{\n\t.reg .b32 remote;\n\t"
         "mapa.shared::cluster.u32 remote, %0, 0;\n\t"
-        "mbarrier.arrive.shared::cluster.b64 _, [remote];\n\t}" ::"r"(bar)
+        "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [remote];\n\t}" ::"r"(bar)
         : "memory");
+}
+// The same behind stores to this SM's shared memory (already fenced for the async proxy). The release is
+// over the cluster, of shared memory alone, about 110 clocks a tile: 40 x 8 tokens over 131000 keys 735 us.
+// With a release of all memory on the arrival 809; with one of the CTA's scope, which promises the other SM
+// nothing, 692; passed on by an idle warp of the other SM 738.
+__device__ __forceinline__ void release_to_leader(uint32_t bar) {
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+    arrive_leader(bar);
+}
+// Look-ups of barriers that either SM, or the leader's commits, arrive on.
+__device__ __forceinline__ bool pair_test_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool pair_try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 // D += A B^T over 16 elements of K, FP16 operands: A from shared memory, or from tensor memory.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -192,10 +222,10 @@ struct Ctx {
     }
     __device__ bool wait(uint64_t* bar, uint32_t parity) const {
         const uint32_t a = smem_u32(bar);
-        if (mbar_try_wait(a, parity)) return true;
+        if (pair_try_wait(a, parity)) return true;
         const uint64_t t0 = globaltimer_ns();
         for (uint32_t it = 1;; ++it) {
-            if (mbar_try_wait(a, parity)) return true;
+            if (pair_try_wait(a, parity)) return true;
             if ((it & 7) == 0) {
                 if (aborted()) return false;
                 if (globaltimer_ns() - t0 > kWaitLimitNs) {
@@ -209,7 +239,7 @@ struct Ctx {
     __device__ bool wait2(uint64_t* bar_a, uint32_t parity_a, uint64_t* bar_b,
                           uint32_t parity_b) const {
         const uint32_t a = smem_u32(bar_a), b = smem_u32(bar_b);
-        const bool ra = mbar_test_wait(a, parity_a), rb = mbar_test_wait(b, parity_b);
+        const bool ra = pair_test_wait(a, parity_a), rb = pair_test_wait(b, parity_b);
         if (ra & rb) return true;
         return wait(bar_a, parity_a) && wait(bar_b, parity_b);
     }
@@ -446,7 +476,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    arrive_leader(smem_u32(&full[s]));
+                    release_to_leader(smem_u32(&full[s]));
                     mbar_arrive(smem_u32(&raw_empty[rs]));
                 }
                 if (++rs == raw_stages) {
@@ -590,7 +620,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) arrive_leader(smem_u32(&sm.qfull));
+            if (lane == 0) release_to_leader(smem_u32(&sm.qfull));
             // keys [0, limit) are visible to this thread's row
             const int limit = row0 + row < p.rows ? row_limit(p, row0 + row, keys) : keys;
             float nm = INFINITY;  // minus the reference maximum (log2 units); +inf: no key yet
