@@ -507,9 +507,9 @@ class _OnDevice:
             raise ValueError(f"status: want an int32 tensor on {self.device}")
         return status
 
-    def _read_flags(self, word, clear):
+    def _read_flags(self, word, clear, stream):
         with torch.cuda.device(self._index):
-            return dflash_verify_attn_read_flags(word, clear)
+            return dflash_verify_attn_read_flags(word, clear, stream)
 
 
 TablesOut = collections.namedtuple("TablesOut", (
@@ -591,9 +591,10 @@ class PagedTables(_OnDevice):
                      slots.data_ptr(), self.status.data_ptr())
         return out
 
-    def read_flags(self, clear=False) -> int:
-        """The sticky status word (synchronises)."""
-        return self._read_flags(self.status, clear)
+    def read_flags(self, clear=False, stream=None) -> int:
+        """The sticky status word behind what is on the stream, the current one or the given (waits for
+        it): flags of calls on other streams may still be to come."""
+        return self._read_flags(self.status, clear, stream)
 
 
 _ROPE_LAYOUTS = {"half": DFLASH_ROPE_HALF, "interleaved": DFLASH_ROPE_INTERLEAVED}
@@ -687,9 +688,10 @@ class Rotary(_OnDevice):
                      self.status.data_ptr())
         return q_out
 
-    def read_flags(self, clear=False) -> int:
-        """The sticky status word (synchronises)."""
-        return self._read_flags(self.status, clear)
+    def read_flags(self, clear=False, stream=None) -> int:
+        """The sticky status word behind what is on the stream, the current one or the given (waits for
+        it): flags of calls on other streams may still be to come."""
+        return self._read_flags(self.status, clear, stream)
 
 
 class SharedPrefixAttention(_OnDevice):
@@ -752,6 +754,7 @@ class SharedPrefixAttention(_OnDevice):
                      out.data_ptr(), lse.data_ptr())
         return out, lse
 
-    def read_flags(self, clear=False) -> int:
-        """The sticky status word (synchronises)."""
-        return self._read_flags(self.workspace, clear)
+    def read_flags(self, clear=False, stream=None) -> int:
+        """The sticky status word behind what is on the stream, the current one or the given (waits for
+        it): flags of calls on other streams may still be to come."""
+        return self._read_flags(self.workspace, clear, stream)
