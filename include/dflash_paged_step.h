@@ -221,7 +221,8 @@ int dflash_rope_kv_write_live(const dflash_rope_plan_t* plan, int64_t num_tokens
  * the whole batch, and only keys S .. N - 1 of each sequence through its block-table row (entries
  * from S / page_size on; the ones before are not read). Maxima, sums and numerators of both parts
  * are FP32 and merged by a combine pass.
- *   prefix_table  int32 [floor(max_prefix / page_size)]; a row of block_table may serve
+ *   prefix_table  int32 [floor(max_prefix / page_size)]; a row of block_table may serve. NULL if
+ *                 that is 0
  *   prefix_len    one int32 (device), cut to [0, max_prefix] (DFLASH_FLAG_CONTEXT_CLAMPED)
  * A sequence that ends inside the prefix, or is empty (a padded batch slot, N = 0), sees the keys
  * that the causal rule gives it. A row of q with a NaN or an infinity gives NaN, in its own row of

@@ -724,8 +724,8 @@ class SharedPrefixAttention(_OnDevice):
     def __call__(self, q, k_pool, v_pool, prefix_table, prefix_len, block_table, context_lens,
                  k_scale, v_scale, out=None, lse=None, stream=None):
         """(out, lse) of q over the pools. prefix_table: int32, the shared pages in order (at least
-        floor(max_prefix / page_size) entries); prefix_len: int32 [1]; both None when the plan's
-        max_prefix is 0."""
+        floor(max_prefix / page_size) entries, None if that is 0); prefix_len: int32 [1], None when
+        the plan's max_prefix is 0."""
         pr, ix, i32, f32 = self.problem, self._index, torch.int32, torch.float32
         q_shape, pool_shape = self.q_shape, self.pool_shape
         if out is None:
@@ -744,7 +744,8 @@ class SharedPrefixAttention(_OnDevice):
         if pr.max_prefix > 0:
             _want("prefix_len", prefix_len, i32, (1,), ix)
             pages = 0 if prefix_table is None else prefix_table.numel()
-            _want("prefix_table", prefix_table, i32, (pages,), ix)
+            if prefix_table is not None:
+                _want("prefix_table", prefix_table, i32, (pages,), ix)
             if pages < pr.max_prefix // pr.page_size:
                 raise ValueError("prefix_table has fewer pages than max_prefix fills")
         self._launch("dflash_prefix_attn_forward", stream, self._plan_ref, q.data_ptr(),

@@ -380,7 +380,8 @@ int dflash_prefix_attn_forward(const dflash_prefix_attn_plan_t* plan, const void
     if (memcmp(&made, plan, sizeof(made)) != 0) return DFLASH_ERR_INVALID_ARGUMENT;
     const bool prefix = pr.max_prefix > 0;
     if (!q || !k_pool || !v_pool || !block_table || !context_lens || !k_scale || !v_scale ||
-        !workspace || !out || !lse || (prefix && (!prefix_table || !prefix_len)))
+        !workspace || !out || !lse || (prefix && !prefix_len) ||
+        (!prefix_table && pr.max_prefix >= pr.page_size))  // (a shorter prefix has no whole page)
         return DFLASH_ERR_INVALID_ARGUMENT;
     if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) ||
         !aligned(workspace, 256) || !aligned(block_table, 4) || !aligned(context_lens, 4) ||

@@ -23,3 +23,16 @@ def test_refusals(B, bad, status):
     assert B.load_library().dflash_rope_kv_write_live(
         ctypes.byref(plan), a["T"], a["q"], a["qs"], a["k"], 512, a["v"], 512, a["pos"], a["slots"],
         a["live"], a["ph"], a["ks_"], a["vs_"], a["qo"], 1536, a["kp"], a["vp"], a["status"], None) == status
+
+
+@pytest.mark.parametrize("kernel", [1, 2])
+@pytest.mark.parametrize("max_prefix,page,table,length,status", [
+    (16, 16, 0, 1, -1), (15, 16, 0, 0, -1), (15, 16, 0, 1, -3), (0, 16, 0, 0, -3), (16, 16, 1, 1, -3)])
+def test_a_prefix_without_a_whole_page_needs_no_table(B, kernel, max_prefix, page, table, length, status):
+    """(Calls that pass the pointer checks are refused for their workspace, before any launch.)"""
+    plan = B.dflash_prefix_attn_plan(B.make_prefix_problem(4, 8, 6, 1, 256, page, 64, 256, 1024, max_prefix, -1,
+                                                           kernel))
+    at = [0x100000 * (i + 1) for i in range(12)]
+    assert B.load_library().dflash_prefix_attn_forward(
+        ctypes.byref(plan), at[0], at[1], at[2], at[3] * table, at[4] * length, at[5], at[6], at[7], at[8],
+        at[9], 1024, at[10], at[11], None) == status
