@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 }
 
 // Estimated times in us, over the longest prefix, for own keys half as many as the plan allows. A CTA of
-// the split kernel takes 9 us and 1.3 us a 128-key tile, a pair 10 us and 1.0 us a 96-key tile.
+// the split kernel takes 9 us and 1.3 us a 128-key tile, a pair 10 us and 1.05 us a 96-key tile.
 constexpr double kRowsCtaUs = 9.0, kRowsTileUs = 1.3, kPairCtaUs = 10.0, kPairTileUs = 1.0;
 
 // SM time of all sequences' own keys.

@@ -37,15 +37,17 @@ def built():
     build.build()
 
 
-def keys(n, gap, spread, P, Hkv):
+def keys(n, gap, spread, P, Hkv, stronger=()):
     """Pools of n keys in order (page p holds keys p P .. p P + P - 1), the scale of K, and the scores in
-    nats and the values as float64."""
+    nats and the values as float64. stronger: more strong keys, (position, c)."""
     g = torch.Generator().manual_seed(int(16 * gap) + n)
     c, v = torch.zeros(n), torch.ones(n)
     if spread:
         c = (0.04 * torch.randn(n, generator=g)).clamp(-0.2, 0.2)
         v = 1.0 + 0.25 * torch.randn(n, generator=g)
     c[0], v[0] = 1.0, 0.0
+    for j, x in stronger:
+        c[j] = x
     c, v = c.to(torch.float8_e4m3fn), v.to(torch.float8_e4m3fn)
     k_scale = torch.tensor([gap * math.log(2.0) / 16.0], device="cuda")
     pages = -(-n // P)
@@ -126,3 +128,31 @@ def test_in_the_plain_attention(mode, n, q_len, spread, gap):
     out, lse = att(q, kp, vp, table, torch.full((batch,), n, dtype=torch.int32, device="cuda"), ks,
                    one)
     check(out, lse, scores, values, n, q_len)
+
+
+@pytest.mark.parametrize("kernel", [0, 1, 2], ids=["plain", "rows", "pairs"])
+@pytest.mark.parametrize("step", [3.0, 9.0, 11.0, 14.0, 15.5, 21.0])
+def test_strong_keys_one_after_the_other(kernel, step):
+    """Each a quarter to 2 `step`s (bits) above the last: in the tile after it, in the same tile, far behind.
+    (Scores of up to 105 bits: 2^-17 of a probability.)"""
+    from speculative_verify_paged_e4m3_gb300 import binding as B
+    n, P, Hq, Hkv, batch, q_len = 16384, 64, 32, 4, 80, 1
+    kp, vp, ks, scores, values = keys(n, step, True, P, Hkv, [
+        (97, 2.0), (150, 3.0), (151, 3.25), (400, 3.5), (5000, 4.0), (5001, 0.0), (16383, 5.0)])
+    pages = n // P
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")
+    one = torch.ones(1, device="cuda")
+    q = torch.ones((batch, q_len, Hq, D), dtype=torch.float16, device="cuda")
+    lens = torch.full((batch,), n, dtype=torch.int32, device="cuda")
+    lens[::3] = 5003
+    rows = table.expand(batch, -1).contiguous()
+    if kernel:
+        att = B.SharedPrefixAttention(batch, q_len, Hq, Hkv, D, P, pages, pages, n, n, kernel=kernel)
+        out, lse = att(q, kp, vp, table, lens[1:2].clone(), rows, lens, ks, one)
+    else:
+        att = B.VerifyAttention(batch, q_len, Hq, Hkv, D, P, pages, pages, n)
+        out, lse = att(q, kp, vp, rows, lens, ks, one)
+    for b in (0, 1):
+        m = int(lens[b].item())
+        some = torch.arange(batch, device="cuda") % 3 == 0 if b == 0 else torch.arange(batch, device="cuda") % 3 > 0
+        check(out[some], lse[some], scores[:m], values[:m], m, q_len)
