@@ -220,7 +220,11 @@ int dflash_rope_kv_write_live(const dflash_rope_plan_t* plan, int64_t num_tokens
  * / page_size) * page_size keys, are then read once through prefix_table for the query rows of
  * the whole batch, and only keys S .. N - 1 of each sequence through its block-table row (entries
  * from S / page_size on; the ones before are not read). Maxima, sums and numerators of both parts
- * are FP32 and merged by a combine pass.
+ * are FP32 and merged by a combine pass. Probabilities are three E4M3 terms (ROWS, and the sequences'
+ * own keys) or FP16 (PAIRS): the output errs by 2.1e-4 to 2.2e-4 or 2.2e-4 to 3.0e-4 of its norm, of which
+ * its own rounding to FP16 is 2.1e-4. Probabilities far below a row's largest have a fixed step of 2^-23 of
+ * it, offset key by key so that the mean of many is right, or of 2^-28. AUTO takes the kernel that is
+ * estimated to be faster.
  *   prefix_table  int32 [floor(max_prefix / page_size)]; a row of block_table may serve. NULL if
  *                 that is 0
  *   prefix_len    one int32 (device), cut to [0, max_prefix] (DFLASH_FLAG_CONTEXT_CLAMPED)

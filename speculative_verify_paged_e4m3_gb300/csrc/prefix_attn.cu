@@ -178,7 +178,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 }
 
 // Estimated times in us, over the longest prefix, for own keys half as many as the plan allows. A CTA of
-// the split kernel takes 9 us and 1.3 us a 128-key tile, a pair 10 us and 1.05 us a 96-key tile.
+// the split kernel takes 9 us and 1.3 us a 128-key tile, a pair 10 us and 1.0 us a 96-key tile (1.07 by
+// itself; with 1.05 here, 32 single tokens over 65536 keys have a pair more, too few SMs are left to their own
+// keys, and 79 us are 85).
 constexpr double kRowsCtaUs = 9.0, kRowsTileUs = 1.3, kPairCtaUs = 10.0, kPairTileUs = 1.0;
 
 // SM time of all sequences' own keys.
@@ -217,9 +219,9 @@ double rows_us(int64_t blocks, int sm_count, const dflash_prefix_attn_problem* p
 // SM pairs for the prefix, and the time of prefix and own keys with them. The sequences' own keys run on
 // the SMs left over, from the start, and on all of them once the prefix is done, so that on an idle GPU at
 // the end most of its SMs wait for the longest. The count is the one that lets both end soonest (fewer
-// leave those SMs idle for a part, more run on after the prefix). The rates are the kernel's own: with 1.2
-// us a tile in place of 1.0, 32 single tokens over 65536 keys took 84 us, now 74, and 16 x 8 tokens over
-// 32768 keys 106, now 98.
+// leave those SMs idle for a part, more run on after the prefix). The rate matters: with 1.2 us a tile in place
+// of 1.0, 32 single tokens over 65536 keys take 85 us, not 79, and 16 x 8 tokens over 32768 keys 117, not
+// 111.
 int64_t pairs_for(int64_t blocks, int sm_count, const dflash_prefix_attn_problem* pr,
                   double* pairs_us) {
     const int64_t all = sm_count / 2;
@@ -244,10 +246,10 @@ int64_t pairs_for(int64_t blocks, int sm_count, const dflash_prefix_attn_problem
     return best;
 }
 
-// Which kernel takes less time. Measured, 24/4 heads over 120000 keys: 96 rows 84 against 92 us, 144 rows
-// 135 against 94, 384 rows 483 against 171; 6/1 heads over 32768 keys: 144 rows 25 against 29 us, 192 rows
-// 34 against 29. Over 610 random problems the choice costs 1.2 % over the better kernel's time in the mean,
-// 40 % at worst (a rule on the prefix alone, without the own keys: 2.3 %, 40 %).
+// Which kernel takes less time. Measured, 24/4 heads over 120000 keys: 96 rows 91 against 100 us, 144 rows
+// 138 against 105, 384 rows 496 against 196; 6/1 heads over 32768 keys: 144 rows 25 against 27 us, 192 rows
+// 35 against 28. Over 520 random problems the choice costs 1.4 % over the better kernel's time in the mean,
+// 37 % at worst.
 bool pairs_win(int64_t rows, int sm_count, const dflash_prefix_attn_problem* pr) {
     if (pr->max_prefix == 0 || sm_count < 2) return false;
     double pairs_us;

@@ -34,9 +34,10 @@
 //    0.042, 21 bits below it. At its maximum plain scores cost the same, and 17 bits lost too much.)
 //  * Pairs take equal shares of all (KV head, row block) units' tiles (prefix_pairs.cuh); a share may
 //    end in the middle of a unit, the combine puts the parts together.
-//  * Bound by the tensor pipe and by what feeds it: a tile takes 1912 clocks (990 ns), its products by
-//    themselves 1565. 40 x 8 tokens of 24/4 heads over 131000 keys: 643 us, 1.60 PFLOP/s, 84 % of the
-//    bf16 library product's burst rate; the 16 x 8 tokens over 32768 keys 89 us.
+//  * Bound by the tensor pipe and by what feeds it: a tile takes 1.07 us (0.99, 1912 clocks, before the two
+//    SMs' hand-overs were ordered over the cluster), its products by themselves 1565 clocks. 40 x 8 tokens
+//    of 24/4 heads over 131000 keys: 699 us, 1.47 PFLOP/s, 77 % of the bf16 library product's burst rate; 16 x 8
+//    tokens over 32768 keys 95 us, 106 with peaked scores.
 //  * Every wait is bounded (200 ms, then DFLASH_FLAG_KERNEL_TIMEOUT and a clean exit); both SMs of
 //    a pair leave together.
 #include <cuda.h>

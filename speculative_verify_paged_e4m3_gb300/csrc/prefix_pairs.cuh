@@ -19,7 +19,7 @@ constexpr int kPairMinTiles = 4;   // least tiles worth a pair of their own
 // Equal shares of everything (pitch = tiles) let a pair's share run over a unit's end, which costs a
 // second epilogue, Q and pipeline fill, about kPairSwitch tiles. Where whole pairs for each unit
 // (pitch = a multiple of per_pair, the end of it empty) cost no more than that, they are taken: 32
-// single tokens over 65536 keys 80 -> 74 us, 16 x 8 tokens over 32768 keys 107 -> 98 (24/4 heads, the
+// single tokens over 65536 keys 82 -> 79 us, 16 x 8 tokens over 32768 keys 118 -> 111 (24/4 heads, the
 // whole call, without and with).
 constexpr int kPairSwitch = 7;
 
