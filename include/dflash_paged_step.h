@@ -212,6 +212,37 @@ int dflash_rope_kv_write_live(const dflash_rope_plan_t* plan, int64_t num_tokens
                               void* cuda_stream);
 
 /* ------------------------------------------------------------------------------------------------
+ * Head norms in the same pass.
+ *
+ * Each head x of Q (and of K) is first normed over its head_dim elements,
+ *   x_i * (weight_offset + w_i) / sqrt(mean of x^2 + eps),
+ * then rotated as above; V is not normed. Sum and division are FP32, nothing is rounded between norm and
+ * rotation. (The squares' sum must stay below 2^128: bf16 elements below 2^60.)
+ */
+typedef struct {
+    const void* q_weight; /* device, head_dim elements of the plan's dtype, 16-byte aligned; NULL: Q
+                             is not normed */
+    const void* k_weight; /* the same for K */
+    float eps;            /* >= 0, finite */
+    float weight_offset;  /* finite; 1 for weights that are kept about zero, else 0 */
+} dflash_head_norm;       /* host struct; its fields are taken at the call */
+
+/* dflash_rope_apply and dflash_rope_kv_write_live with norms (norm NULL: without). */
+int dflash_norm_rope_apply(const dflash_rope_plan_t* plan, const dflash_head_norm* norm,
+                           int64_t num_tokens, const void* q, int64_t q_stride, const void* k,
+                           int64_t k_stride, const int32_t* positions, const uint64_t* phases,
+                           void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                           void* cuda_stream);
+int dflash_norm_rope_kv_write(const dflash_rope_plan_t* plan, const dflash_head_norm* norm,
+                              int64_t num_tokens, const void* q, int64_t q_stride, const void* k,
+                              int64_t k_stride, const void* v, int64_t v_stride,
+                              const int32_t* positions, const int64_t* slots,
+                              const int32_t* num_live, const uint64_t* phases,
+                              const float* k_scale, const float* v_scale, void* q_out,
+                              int64_t q_out_stride, void* k_pool, void* v_pool, int32_t* status,
+                              void* cuda_stream);
+
+/* ------------------------------------------------------------------------------------------------
  * Attention of a batch over a shared prefix.
  *
  * The result is dflash_verify_attn_forward's on the same q, pools, block_table and context_lens

@@ -1,5 +1,5 @@
-"""Thin ctypes binding over libdflash_verify_attn.so (the C ABI in include/dflash_verify_attn.h and
-include/dflash_paged_step.h).
+"""Thin ctypes binding over libdflash_verify_attn.so (the C ABI in include/dflash_verify_attn.h,
+include/dflash_paged_step.h and include/dflash_mx4_cache.h).
 
 Argument marshalling only: every step of the computation runs in the library's CUDA kernels.
 Functions carry the C names; tensors are torch CUDA tensors whose data pointers are passed
@@ -49,6 +49,10 @@ DFLASH_BF16 = 1
 DFLASH_PREFIX_KERNEL_AUTO = 0
 DFLASH_PREFIX_KERNEL_ROWS = 1
 DFLASH_PREFIX_KERNEL_PAIRS = 2
+DFLASH_E5M2 = 2
+DFLASH_KERNEL_MX4 = 3
+DFLASH_MX4_CHUNK_TOKENS = 16
+DFLASH_MX4_CHUNK_BYTES = 2176
 
 EXPORTED = (
     "dflash_verify_attn_plan",
@@ -68,6 +72,12 @@ EXPORTED = (
     "dflash_rope_kv_write_live",
     "dflash_prefix_attn_plan",
     "dflash_prefix_attn_forward",
+    "dflash_norm_rope_apply",
+    "dflash_norm_rope_kv_write",
+    "dflash_mx4_kv_write",
+    "dflash_mx4_read",
+    "dflash_mx4_attn_plan",
+    "dflash_mx4_attn_forward",
     "dflash_verify_attn_status_string",
 )
 
@@ -129,6 +139,11 @@ class PrefixAttnPlan(ctypes.Structure):
     ]
 
 
+class HeadNormArgs(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float)]
+
+
 class DflashError(RuntimeError):
     def __init__(self, fn: str, status: int):
         super().__init__(f"{fn}: {status_string(status)} ({status})")
@@ -179,6 +194,17 @@ def load_library() -> ctypes.CDLL:
             xp = ctypes.POINTER(PrefixAttnPlan)
             lib.dflash_prefix_attn_plan.argtypes = [ctypes.POINTER(PrefixAttnProblem), xp]
             lib.dflash_prefix_attn_forward.argtypes = [xp] + [vp] * 10 + [sz, vp, vp, vp]
+            np_ = ctypes.POINTER(HeadNormArgs)
+            lib.dflash_norm_rope_apply.argtypes = [rp, np_, i64, vp, i64, vp, i64, vp, vp, vp, i64,
+                                                   vp, i64, vp]
+            lib.dflash_norm_rope_kv_write.argtypes = [rp, np_, i64, vp, i64, vp, i64, vp,
+                                                      i64] + [vp] * 7 + [i64] + [vp] * 4
+            lib.dflash_mx4_kv_write.argtypes = [rp, np_, i64, vp, i64, vp, i64, vp,
+                                                i64] + [vp] * 5 + [i64] + [vp] * 4
+            lib.dflash_mx4_read.argtypes = [i32, i32, i32, i32, vp, vp, i64, vp, i32, vp, i64, vp,
+                                            i64, vp, vp]
+            lib.dflash_mx4_attn_plan.argtypes = [ctypes.POINTER(Problem), pp]
+            lib.dflash_mx4_attn_forward.argtypes = [pp] + [vp] * 6 + [sz, vp, vp, vp]
             lib.dflash_verify_attn_debug_dequant.argtypes = [vp, i64, vp, vp, vp, vp]
             lib.dflash_verify_attn_read_flags.argtypes = [vp, ctypes.POINTER(ctypes.c_int32),
                                                           ctypes.c_int, vp]
@@ -369,6 +395,13 @@ def dflash_prefix_attn_plan(problem: PrefixAttnProblem) -> PrefixAttnPlan:
     plan = PrefixAttnPlan()
     _check("dflash_prefix_attn_plan",
            load_library().dflash_prefix_attn_plan(ctypes.byref(problem), ctypes.byref(plan)))
+    return plan
+
+
+def dflash_mx4_attn_plan(problem: Problem) -> Plan:
+    plan = Plan()
+    _check("dflash_mx4_attn_plan",
+           load_library().dflash_mx4_attn_plan(ctypes.byref(problem), ctypes.byref(plan)))
     return plan
 
 
@@ -604,22 +637,35 @@ _ROPE_SCALINGS = {"none": DFLASH_ROPE_SCALE_NONE, "linear": DFLASH_ROPE_SCALE_LI
 _ROPE_DTYPES = {torch.float16: DFLASH_FP16, torch.bfloat16: DFLASH_BF16}
 
 
+class HeadNorm(collections.namedtuple("HeadNorm", ("q_weight", "k_weight", "eps",
+                                                   "weight_offset"), defaults=(1e-6, 0.0))):
+    """Norms of one layer's heads before their rotation: x * (weight_offset + weight) / sqrt(mean of
+    x^2 + eps). Weights [head_dim] of the rotary's dtype; one that is None leaves its operand without
+    a norm."""
+    __slots__ = ()
+
+
 class Rotary(_OnDevice):
     """Rotary positions of one model's heads: apply() rotates Q and K, kv_write() rotates Q and
-    writes the rotated K and V into the paged E4M3 pools (dflash_rope_apply,
-    dflash_rope_kv_write_live)."""
+    writes the rotated K and V into the paged E4M3 pools, mx4_write() into the 4-bit ones
+    (dflash_rope_apply, dflash_rope_kv_write_live, dflash_mx4_kv_write). Each takes a HeadNorm for
+    heads that are normed first."""
 
     def __init__(self, num_q_heads, num_kv_heads, head_dim, rotary_dim=None, layout="half",
                  dtype=torch.float16, base=10000.0, scaling="none", factor=1.0,
                  trained_context=1, beta_fast=32.0, beta_slow=1.0, low_turns=1.0, high_turns=4.0,
                  page_size=16, num_pages=1, device=None, status=None):
-        super().__init__(device, "dflash_rope_apply", "dflash_rope_kv_write_live")
+        super().__init__(device, "dflash_rope_apply", "dflash_rope_kv_write_live",
+                         "dflash_norm_rope_apply", "dflash_norm_rope_kv_write",
+                         "dflash_mx4_kv_write")
         if layout not in _ROPE_LAYOUTS or scaling not in _ROPE_SCALINGS:
             raise ValueError(f"unknown layout {layout!r} or scaling {scaling!r}")
         if dtype not in _ROPE_DTYPES:
             raise ValueError(f"dtype {dtype}: want float16 or bfloat16")
         self.dtype, self.shape = dtype, (num_q_heads, num_kv_heads, head_dim)
         self.pool_shape = (num_pages, page_size, num_kv_heads, head_dim)
+        self.mx4_pool_shape = (num_pages, page_size // DFLASH_MX4_CHUNK_TOKENS, num_kv_heads,
+                               DFLASH_MX4_CHUNK_BYTES)
         self.plan, phases = dflash_rope_plan(make_rope_problem(
             num_q_heads, num_kv_heads, head_dim, head_dim if rotary_dim is None else rotary_dim,
             _ROPE_LAYOUTS[layout], _ROPE_DTYPES[dtype], base, _ROPE_SCALINGS[scaling], factor,
@@ -630,9 +676,21 @@ class Rotary(_OnDevice):
         self.status = self._status_word(status)
         self._ready()
 
-    def apply(self, q, k, positions, q_out=None, k_out=None, stream=None):
-        """(q_out, k_out): q [T, Hq, D] and k [T, Hkv, D] (or None) rotated to positions [T].
-        q_out may be q itself, k_out k itself."""
+    def _norm_args(self, norm):
+        """The C struct of a HeadNorm (None of None)."""
+        if norm is None:
+            return None
+        D, ix = self.shape[2], self._index
+        if norm.q_weight is not None:
+            _want("norm.q_weight", norm.q_weight, self.dtype, (D,), ix)
+        if norm.k_weight is not None:
+            _want("norm.k_weight", norm.k_weight, self.dtype, (D,), ix)
+        return ctypes.byref(HeadNormArgs(_ptr(norm.q_weight), _ptr(norm.k_weight), norm.eps,
+                                         norm.weight_offset))
+
+    def apply(self, q, k, positions, q_out=None, k_out=None, stream=None, norm=None):
+        """(q_out, k_out): q [T, Hq, D] and k [T, Hkv, D] (or None), normed if a HeadNorm is given, rotated
+        to positions [T]. q_out may be q itself, k_out k itself."""
         (Hq, Hkv, D), T, dt, ix = self.shape, positions.numel(), self.dtype, self._index
         q_shape, k_shape = (T, Hq, D), (T, Hkv, D)
         if q_out is None:
@@ -648,18 +706,18 @@ class Rotary(_OnDevice):
             ko = _want_rows("k_out", k_out, dt, k_shape, ix)
         elif k_out is not None:
             raise ValueError("k_out without k")
-        self._launch("dflash_rope_apply", stream, self._plan_ref, T, q.data_ptr(), qs, _ptr(k), ks,
-                     positions.data_ptr(), self.phases.data_ptr(), q_out.data_ptr(), qo,
-                     _ptr(k_out), ko)
+        args = (T, q.data_ptr(), qs, _ptr(k), ks, positions.data_ptr(), self.phases.data_ptr(),
+                q_out.data_ptr(), qo, _ptr(k_out), ko)
+        if norm is None:
+            self._launch("dflash_rope_apply", stream, self._plan_ref, *args)
+        else:
+            self._launch("dflash_norm_rope_apply", stream, self._plan_ref, self._norm_args(norm),
+                         *args)
         return q_out, k_out
 
-    def kv_write(self, q, k, v, positions, slots, k_scale, v_scale, k_pool, v_pool, q_out=None,
-                 stream=None, token_starts=None):
-        """q_out: q [T, Hq, D] rotated to positions [T] (it may be q itself); the rotated k and v
-        [T, Hkv, D] go to the pools at slots [T]. A token with a negative slot is padding and left
-        alone (its row of a q_out made here is not initialised). With token_starts (of PagedTables) only
-        tokens past its last entry are: those inside the shared pages have no slot to write to either,
-        but a query."""
+    def _write_args(self, q, k, v, positions, slots, pool_shape, k_pool, v_pool, q_out, stream,
+                    token_starts):
+        """Checks of both cache writes: q_out, the arguments up to num_live, and q_out's stride."""
         (Hq, Hkv, D), T, dt, ix = self.shape, positions.numel(), self.dtype, self._index
         q_shape, k_shape = (T, Hq, D), (T, Hkv, D)
         if q_out is None:
@@ -670,10 +728,8 @@ class Rotary(_OnDevice):
         vs = _want_rows("v", v, dt, k_shape, ix)
         _want("positions", positions, torch.int32, (T,), ix)
         _want("slots", slots, torch.int64, (T,), ix)
-        _want("k_scale", k_scale, torch.float32, (1,), ix)
-        _want("v_scale", v_scale, torch.float32, (1,), ix)
-        _want("k_pool", k_pool, torch.uint8, self.pool_shape, ix)
-        _want("v_pool", v_pool, torch.uint8, self.pool_shape, ix)
+        _want("k_pool", k_pool, torch.uint8, pool_shape, ix)
+        _want("v_pool", v_pool, torch.uint8, pool_shape, ix)
         live = None
         if token_starts is not None:
             n = token_starts.numel()
@@ -681,11 +737,37 @@ class Rotary(_OnDevice):
             if n < 1:
                 raise ValueError("token_starts: want at least one entry")
             live = token_starts.data_ptr() + 4 * (n - 1)
-        self._launch("dflash_rope_kv_write_live", stream, self._plan_ref, T, q.data_ptr(), qs,
-                     k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(), slots.data_ptr(),
-                     live, self.phases.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                     q_out.data_ptr(), qo, k_pool.data_ptr(), v_pool.data_ptr(),
-                     self.status.data_ptr())
+        return q_out, (T, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+                       positions.data_ptr(), slots.data_ptr(), live,
+                       self.phases.data_ptr()), (q_out.data_ptr(), qo, k_pool.data_ptr(),
+                                                 v_pool.data_ptr(), self.status.data_ptr())
+
+    def kv_write(self, q, k, v, positions, slots, k_scale, v_scale, k_pool, v_pool, q_out=None,
+                 stream=None, token_starts=None, norm=None):
+        """q_out: q [T, Hq, D] rotated to positions [T] (it may be q itself); the rotated k and v
+        [T, Hkv, D] go to the pools at slots [T]. A token with a negative slot is padding and left
+        alone (its row of a q_out made here is not initialised). With token_starts (of PagedTables) only
+        tokens past its last entry are: those inside the shared pages have no slot to write to either,
+        but a query. With a HeadNorm q and k are normed before they are rotated."""
+        q_out, args, outs = self._write_args(q, k, v, positions, slots, self.pool_shape, k_pool,
+                                             v_pool, q_out, stream, token_starts)
+        _want("k_scale", k_scale, torch.float32, (1,), self._index)
+        _want("v_scale", v_scale, torch.float32, (1,), self._index)
+        scales = k_scale.data_ptr(), v_scale.data_ptr()
+        if norm is None:
+            self._launch("dflash_rope_kv_write_live", stream, self._plan_ref, *args, *scales, *outs)
+        else:
+            self._launch("dflash_norm_rope_kv_write", stream, self._plan_ref,
+                         self._norm_args(norm), *args, *scales, *outs)
+        return q_out
+
+    def mx4_write(self, q, k, v, positions, slots, k_pool, v_pool, q_out=None, norm=None,
+                  stream=None, token_starts=None):
+        """kv_write into the pools of an Mx4Cache, which need no scales."""
+        q_out, args, outs = self._write_args(q, k, v, positions, slots, self.mx4_pool_shape, k_pool,
+                                             v_pool, q_out, stream, token_starts)
+        self._launch("dflash_mx4_kv_write", stream, self._plan_ref, self._norm_args(norm), *args,
+                     *outs)
         return q_out
 
     def read_flags(self, clear=False, stream=None) -> int:
@@ -752,6 +834,120 @@ class SharedPrefixAttention(_OnDevice):
                      k_pool.data_ptr(), v_pool.data_ptr(), _ptr(prefix_table), _ptr(prefix_len),
                      block_table.data_ptr(), context_lens.data_ptr(), k_scale.data_ptr(),
                      v_scale.data_ptr(), self.workspace.data_ptr(), self._workspace_bytes,
+                     out.data_ptr(), lse.data_ptr())
+        return out, lse
+
+    def read_flags(self, clear=False, stream=None) -> int:
+        """The sticky status word behind what is on the stream, the current one or the given (waits for
+        it): flags of calls on other streams may still be to come."""
+        return self._read_flags(self.workspace, clear, stream)
+
+
+_MX4_READ_DTYPES = {torch.float16: DFLASH_FP16, torch.bfloat16: DFLASH_BF16,
+                    torch.float8_e5m2: DFLASH_E5M2}
+
+
+class Mx4Cache(_OnDevice):
+    """The pools of one layer's cache in 4 bits (include/dflash_mx4_cache.h has the format): empty()
+    makes them, Rotary.mx4_write fills them, Mx4Attention attends over them, read() gives the numbers of
+    cached tokens (dflash_mx4_read)."""
+
+    def __init__(self, num_kv_heads, head_dim, page_size, num_pages, device=None, status=None):
+        super().__init__(device, "dflash_mx4_read")
+        if num_kv_heads < 1 or num_pages < 1 or page_size < 1:
+            raise ValueError("num_kv_heads, page_size and num_pages: want at least 1")
+        if head_dim != 256 or page_size % DFLASH_MX4_CHUNK_TOKENS:
+            raise DflashError("Mx4Cache", DFLASH_ERR_UNSUPPORTED)
+        self._dims = num_kv_heads, head_dim, page_size, num_pages
+        self.pool_shape = (num_pages, page_size // DFLASH_MX4_CHUNK_TOKENS, num_kv_heads,
+                           DFLASH_MX4_CHUNK_BYTES)
+        self.status = self._status_word(status)
+        self._ready()
+
+    def empty(self):
+        """(k_pool, v_pool), all zeros."""
+        return tuple(torch.zeros(self.pool_shape, dtype=torch.uint8, device=self.device)
+                     for _ in range(2))
+
+    def read(self, k_pool, v_pool, slots, k_out=None, v_out=None, dtype=torch.float16, stream=None):
+        """(k_out, v_out) [T, Hkv, D]: the tokens at slots [T], as numbers of the outputs' dtype (dtype
+        for those made here): float16, bfloat16 or float8_e5m2. A pool that is None is left out. The
+        rows of a negative slot stay as they are (not initialised if made here)."""
+        (Hkv, D, _, _), T, ix = self._dims, slots.numel(), self._index
+        _want("slots", slots, torch.int64, (T,), ix)
+        given = next((o for o in (k_out, v_out) if o is not None), None)
+        if given is not None:
+            dtype = given.dtype
+        if dtype not in _MX4_READ_DTYPES:
+            raise ValueError(f"dtype {dtype}: want float16, bfloat16 or float8_e5m2")
+        args, outs = [], []
+        for name, pool, out in (("k", k_pool, k_out), ("v", v_pool, v_out)):
+            if pool is None:
+                if out is not None:
+                    raise ValueError(f"{name}_out without {name}_pool")
+                args += [None, 0]
+            else:
+                _want(f"{name}_pool", pool, torch.uint8, self.pool_shape, ix)
+                if out is None:
+                    out = self._empty((T, Hkv, D), dtype, stream)
+                args += [out.data_ptr(), _want_rows(f"{name}_out", out, dtype, (T, Hkv, D), ix)]
+            outs.append(out)
+        self._launch("dflash_mx4_read", stream, *self._dims, _ptr(k_pool), _ptr(v_pool), T,
+                     slots.data_ptr(), _MX4_READ_DTYPES[dtype], *args, self.status.data_ptr())
+        return tuple(outs)
+
+    def read_flags(self, clear=False, stream=None) -> int:
+        """The sticky status word behind what is on the stream, the current one or the given (waits for
+        it): flags of calls on other streams may still be to come."""
+        return self._read_flags(self.status, clear, stream)
+
+
+class Mx4Attention(_OnDevice):
+    """Verification attention over the pools of an Mx4Cache: VerifyAttention without scales
+    (dflash_mx4_attn_forward). A plan plus its workspace; calls that may overlap on the GPU need an
+    instance (or a workspace) each."""
+
+    def __init__(self, batch, q_len, num_q_heads, num_kv_heads, head_dim, page_size,
+                 max_pages_per_seq, num_pages, max_context, device=None, num_splits=0,
+                 workspace=None, flags=0):
+        super().__init__(device, "dflash_mx4_attn_forward")
+        self.problem = make_problem(batch, q_len, num_q_heads, num_kv_heads, head_dim, page_size,
+                                    max_pages_per_seq, num_pages, max_context, self.device.index,
+                                    num_splits, DFLASH_KERNEL_AUTO, flags)
+        self.plan = dflash_mx4_attn_plan(self.problem)
+        self._plan_ref = ctypes.byref(self.plan)
+        if workspace is None:
+            workspace = torch.zeros(self.plan.workspace_bytes, dtype=torch.uint8,
+                                    device=self.device)
+        elif (workspace.numel() * workspace.element_size() < self.plan.workspace_bytes
+              or workspace.device != self.device or not workspace.is_contiguous()):
+            raise ValueError("workspace: want plan.workspace_bytes contiguous bytes on "
+                             f"{self.device}")
+        self.workspace = workspace
+        self._workspace_bytes = workspace.numel() * workspace.element_size()
+        self.q_shape = (batch, q_len, num_q_heads, head_dim)
+        self.pool_shape = (num_pages, page_size // DFLASH_MX4_CHUNK_TOKENS, num_kv_heads,
+                           DFLASH_MX4_CHUNK_BYTES)
+        self._ready()
+
+    def __call__(self, q, k_pool, v_pool, block_table, context_lens, out=None, lse=None,
+                 stream=None):
+        """(out, lse) of q [B, q_len, Hq, D] over the pools."""
+        pr, ix, i32 = self.problem, self._index, torch.int32
+        if out is None:
+            out = self._empty(self.q_shape, torch.float16, stream)
+        if lse is None:
+            lse = self._empty(self.q_shape[:3], torch.float32, stream)
+        _want("q", q, torch.float16, self.q_shape, ix)
+        _want("k_pool", k_pool, torch.uint8, self.pool_shape, ix)
+        _want("v_pool", v_pool, torch.uint8, self.pool_shape, ix)
+        _want("block_table", block_table, i32, (pr.batch, pr.max_pages_per_seq), ix)
+        _want("context_lens", context_lens, i32, (pr.batch,), ix)
+        _want("out", out, torch.float16, self.q_shape, ix)
+        _want("lse", lse, torch.float32, self.q_shape[:3], ix)
+        self._launch("dflash_mx4_attn_forward", stream, self._plan_ref, q.data_ptr(),
+                     k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(),
+                     context_lens.data_ptr(), self.workspace.data_ptr(), self._workspace_bytes,
                      out.data_ptr(), lse.data_ptr())
         return out, lse
 

@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 
 SOURCES = ["api.cu", "simt_partial.cu", "tc_partial.cu", "combine.cu", "static_scratch.cu",
            "kv_write.cu", "paged_tables.cu", "rope.cu", "prefix_attn.cu",
-           "prefix_pairs.cu"]
+           "prefix_pairs.cu", "mx4_read.cu", "mx4_attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
           "-I", INCLUDE, "-I", CSRC]

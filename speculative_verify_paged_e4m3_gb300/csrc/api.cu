@@ -124,6 +124,46 @@ PartialParams partial_params(const dflash_verify_attn_plan_t* plan, const void* 
 
 }  // namespace
 
+// For the other kernels that work on such a plan.
+namespace dflash {
+
+int check_attn_plan(const dflash_verify_attn_plan_t* plan) { return check_plan(plan); }
+
+PartialParams attn_params(const dflash_verify_attn_plan_t* plan, const void* q, const void* k_pool,
+                          const void* v_pool, const int32_t* block_table,
+                          const int32_t* context_lens, const float* k_scale, const float* v_scale,
+                          void* workspace) {
+    return partial_params(plan, q, k_pool, v_pool, block_table, context_lens, k_scale, v_scale,
+                          workspace);
+}
+
+CombineParams combine_params(const dflash_verify_attn_plan_t* plan, const void* workspace,
+                             const int32_t* context_lens, void* out, float* lse) {
+    const dflash_verify_attn_problem& pr = plan->problem;
+    const char* ws = static_cast<const char*>(workspace);
+    CombineParams c;
+    c.ws_state = reinterpret_cast<const float2*>(ws + plan->ws_state_offset);
+    c.ws_acc = reinterpret_cast<const float*>(ws + plan->ws_acc_offset);
+    c.context_lens = context_lens;
+    c.out = static_cast<__half*>(out);
+    c.lse = lse;
+    c.batch = pr.batch;
+    c.q_len = pr.q_len;
+    c.num_q_heads = pr.num_q_heads;
+    c.num_kv_heads = pr.num_kv_heads;
+    c.group = pr.num_q_heads / pr.num_kv_heads;
+    c.rows = plan->rows;
+    c.max_context = pr.max_context;
+    c.num_splits = plan->num_splits;
+    c.num_slots = plan->num_slots;
+    c.tile_keys = plan->tile_keys;
+    c.min_split_keys = plan->min_split_keys;
+    c.pdl = (pr.flags & DFLASH_PROBLEM_PDL) && !plan->combine_fused ? 1 : 0;
+    return c;
+}
+
+}  // namespace dflash
+
 extern "C" {
 
 const char* dflash_verify_attn_status_string(int status) {
@@ -385,26 +425,7 @@ int dflash_verify_attn_combine(const dflash_verify_attn_plan_t* plan, const void
     if (!aligned(workspace, 256) || !aligned(out, 8) || !aligned(lse, 4))
         return DFLASH_ERR_INVALID_ARGUMENT;
     if (workspace_bytes < plan->workspace_bytes) return DFLASH_ERR_WORKSPACE_TOO_SMALL;
-    const dflash_verify_attn_problem& pr = plan->problem;
-    const char* ws = static_cast<const char*>(workspace);
-    CombineParams c;
-    c.ws_state = reinterpret_cast<const float2*>(ws + plan->ws_state_offset);
-    c.ws_acc = reinterpret_cast<const float*>(ws + plan->ws_acc_offset);
-    c.context_lens = context_lens;
-    c.out = static_cast<__half*>(out);
-    c.lse = lse;
-    c.batch = pr.batch;
-    c.q_len = pr.q_len;
-    c.num_q_heads = pr.num_q_heads;
-    c.num_kv_heads = pr.num_kv_heads;
-    c.group = pr.num_q_heads / pr.num_kv_heads;
-    c.rows = plan->rows;
-    c.max_context = pr.max_context;
-    c.num_splits = plan->num_splits;
-    c.num_slots = plan->num_slots;
-    c.tile_keys = plan->tile_keys;
-    c.min_split_keys = plan->min_split_keys;
-    c.pdl = (pr.flags & DFLASH_PROBLEM_PDL) && !plan->combine_fused ? 1 : 0;
+    const CombineParams c = combine_params(plan, workspace, context_lens, out, lse);
     if (launch_combine(c, static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess) {
         cudaGetLastError();
         return DFLASH_ERR_CUDA;

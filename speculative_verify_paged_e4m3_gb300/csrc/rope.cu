@@ -1,5 +1,5 @@
-// rope.cu -- rotary positions of Q and K, alone or with the E4M3 cache write
-// (dflash_paged_step.h has the definition).
+// rope.cu -- rotary positions of Q and K, alone or with the write into the E4M3 or the 4-bit cache, head
+// norms in the same pass (dflash_paged_step.h and dflash_mx4_cache.h have the definitions).
 //
 // Angles. Position t turns pair i by t * theta_i. With the frequency held as a 64-bit fraction of a
 // turn, f_i = theta_i / (2 pi) * 2^64, the low 64 bits of t * f_i are the fraction of a turn left
@@ -23,7 +23,8 @@
 #include <type_traits>
 
 #include "common.cuh"
-#include "dflash_paged_step.h"
+#include "dflash_mx4_cache.h"
+#include "mx4.cuh"
 #include "tc_ptx.cuh"
 
 namespace dflash {
@@ -40,6 +41,9 @@ constexpr int kRows = 4;       // rows of a token that a warp has in flight
 constexpr int64_t kTokensOne = 760, kTokensTwo = 4560;
 constexpr int64_t kMaxTokens = 0x7FFFFFFF;  // CTAs of a launch
 
+// Where the rows of K (and V) go: k_out, or the pools of either cache.
+enum class To { kRows, kE4m3, kMx4 };
+
 struct RopeParams {
     const void *q, *k, *v;
     int64_t q_stride, k_stride, v_stride;
@@ -55,6 +59,8 @@ struct RopeParams {
     int64_t num_tokens, num_slots;
     int num_q_heads, num_kv_heads, rotary_dim;
     float amplitude;
+    const void *q_weight, *k_weight;  // head norms; null: that operand is not normed
+    float eps, weight_offset;
 };
 
 // Four elements of a row (8 bytes).
@@ -130,29 +136,130 @@ __device__ __forceinline__ void lane_turns(const float2* cs, int lane, float (&c
 }
 
 // Tokens from here on are padding if their slot is negative.
-template <bool kWrite>
+template <To kTo>
 __device__ __forceinline__ int64_t live_tokens(const RopeParams& p) {
-    return kWrite && p.num_live ? *p.num_live : 0;
+    return kTo != To::kRows && p.num_live ? *p.num_live : 0;
 }
 
 // The scale of a row's codes (1 for a row of Q).
-template <bool kWrite>
+template <To kTo>
 __device__ __forceinline__ float scale_of(const RopeParams& p, int h) {
-    return !kWrite || h < 0 ? 1.f : (h < p.num_kv_heads ? *p.k_scale : *p.v_scale);
+    return kTo != To::kE4m3 || h < 0 ? 1.f : (h < p.num_kv_heads ? *p.k_scale : *p.v_scale);
 }
 
-// Row r of token t: Q rows, then K's, then V's. Its two pieces (at, at + gap) turned, then rounded and
-// stored, by the scale that scale_now(its head past Q's) gives.
-template <typename T, bool kHalf, bool kWrite, typename Scale>
+// A head's norm: its 256 elements lie in the warp, eight a lane (a from element `at` on, b from at + gap on).
+template <typename T>
+__device__ __forceinline__ void norm_row(const RopeParams& p, const void* weight, int at, int gap,
+                                         float (&a)[4], float (&b)[4]) {
+    float wa[4], wb[4];
+    const T* w = static_cast<const T*>(weight) + at;
+    unpack<T>(__ldg(reinterpret_cast<const uint2*>(w)), wa);
+    unpack<T>(__ldg(reinterpret_cast<const uint2*>(w + gap)), wb);
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum = fmaf(a[i], a[i], fmaf(b[i], b[i], sum));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float r = 1.f / sqrtf(sum * (1.f / kHeadDim) + p.eps);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        a[i] = a[i] * r * (p.weight_offset + wa[i]);
+        b[i] = b[i] * r * (p.weight_offset + wb[i]);
+    }
+}
+
+// The largest size of 2^kLog neighbouring lanes' elements, as bits.
+template <int kLog>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t m) {
+#pragma unroll
+    for (int o = 1; o < 1 << kLog; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+}
+__device__ __forceinline__ uint32_t size_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+// A row of K into its chunk: the warp brings it in order through its 256 floats of shared memory, so that
+// a lane has 8 elements in a row and four lanes a block, whatever the rotary layout.
+__device__ __forceinline__ void put_mx4_k(uint8_t* chunk, int tok, int lane, int at, int gap,
+                                          const float (&a)[4], const float (&b)[4], float* row) {
+    __syncwarp();  // the row before this one has been read
+    *reinterpret_cast<float4*>(row + at) = make_float4(a[0], a[1], a[2], a[3]);
+    *reinterpret_cast<float4*>(row + at + gap) = make_float4(b[0], b[1], b[2], b[3]);
+    __syncwarp();
+    const float4 u = reinterpret_cast<const float4*>(row)[2 * lane];
+    const float4 v = reinterpret_cast<const float4*>(row)[2 * lane + 1];
+    float x[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, size_bits(x[i]));
+    const int s = mx4::scale_of_max(lanes_max<2>(m));
+    const float inv = mx4::inverse_of_scale(s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] *= inv;
+    const uint32_t codes = s == mx4::kNanScale ? 0u : mx4::codes_of(x);
+    const int block = lane >> 2;
+    *reinterpret_cast<uint32_t*>(chunk + block * 256 + tok * 16 + (lane & 3) * 4) = codes;
+    if ((lane & 3) == 0)
+        chunk[mx4::kCodeBytes + tok * mx4::kBlocks + block] = (uint8_t)s;
+}
+
+// A row of V into its chunk: a lane has elements 4 lane + i and 4 lane + 128 + i (a and b), which share
+// bytes; eight lanes have a block of each half.
+__device__ __forceinline__ void put_mx4_v(uint8_t* chunk, int tok, int lane, const float (&a)[4],
+                                          const float (&b)[4]) {
+    uint32_t ma = 0, mb = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        ma = max(ma, size_bits(a[i]));
+        mb = max(mb, size_bits(b[i]));
+    }
+    const int sa = mx4::scale_of_max(lanes_max<3>(ma)), sb = mx4::scale_of_max(lanes_max<3>(mb));
+    const float ia = mx4::inverse_of_scale(sa), ib = mx4::inverse_of_scale(sb);
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = sa == mx4::kNanScale ? 0.f : a[i] * ia;
+        x[2 * i + 1] = sb == mx4::kNanScale ? 0.f : b[i] * ib;
+    }
+    const uint32_t codes = mx4::codes_of(x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        chunk[(4 * lane + i) * mx4::kTokens + tok] = (uint8_t)(codes >> (8 * i));
+    if ((lane & 7) == 0) {
+        uint8_t* scales = chunk + mx4::kCodeBytes + tok * mx4::kBlocks + (lane >> 3);
+        scales[0] = (uint8_t)sa;
+        scales[4] = (uint8_t)sb;
+    }
+}
+
+// This lane's two pieces (at, at + gap) of a row: whole pairs, or what makes whole bytes of V's chunk.
+struct Pieces {
+    int at, gap;
+};
+template <bool kHalf, To kTo>
+__device__ __forceinline__ Pieces pieces_of(int lane, bool turned, int rotary_dim, bool is_v) {
+    if (kTo == To::kMx4 && is_v) return {4 * lane, kHeadDim / 2};
+    return kHalf && turned ? Pieces{4 * lane, rotary_dim / 2} : Pieces{8 * lane, 4};
+}
+
+// Row r of token t: Q rows, then K's, then V's. Its two pieces (at, at + gap) normed and turned, then rounded
+// and stored, by the scale that scale_now(its head past Q's) gives. `row`: the warp's shared memory
+// (To::kMx4).
+template <typename T, bool kHalf, To kTo, bool kNorm, typename Scale>
 __device__ __forceinline__ void put_row(const RopeParams& p, int64_t t, int64_t slot, int r, int at,
                                         int gap, bool turned, const uint2& wa, const uint2& wb,
-                                        const float (&c)[4], const float (&s)[4], Scale scale_now) {
+                                        const float (&c)[4], const float (&s)[4], Scale scale_now,
+                                        float* row) {
+    constexpr bool kWrite = kTo != To::kRows;
     const int h = r - p.num_q_heads;
     const bool is_q = h < 0, is_v = h >= p.num_kv_heads;
     const int hk = is_v ? h - p.num_kv_heads : h;
     float a[4], b[4];
     unpack<T>(wa, a);
     unpack<T>(wb, b);
+    if constexpr (kNorm) {
+        const void* weight = is_q ? p.q_weight : p.k_weight;
+        if (!is_v && weight) norm_row<T>(p, weight, at, gap, a, b);
+    }
     // (elements past the rotated part are not multiplied: an infinity times a zero sine
     // would be NaN)
     if (!is_v && turned) rotate<kHalf>(a, b, c, s);
@@ -163,6 +270,16 @@ __device__ __forceinline__ void put_row(const RopeParams& p, int64_t t, int64_t 
         *reinterpret_cast<uint2*>(dst) = pack<T>(a);
         *reinterpret_cast<uint2*>(dst + gap) = pack<T>(b);
     } else if (slot >= 0 && slot < p.num_slots) {
+        if constexpr (kTo == To::kMx4) {
+            const int tok = (int)(slot % mx4::kTokens), lane = threadIdx.x & 31;
+            uint8_t* chunk = (is_v ? p.v_pool : p.k_pool) +
+                             mx4::chunk_offset(slot, p.num_kv_heads, hk);
+            if (is_v)
+                put_mx4_v(chunk, tok, lane, a, b);
+            else
+                put_mx4_k(chunk, tok, lane, at, gap, a, b, row);
+            return;
+        }
         const float scale = scale_now(h);
         uint8_t* dst = (is_v ? p.v_pool : p.k_pool) +
                        (slot * p.num_kv_heads + hk) * kHeadDim + at;
@@ -171,23 +288,25 @@ __device__ __forceinline__ void put_row(const RopeParams& p, int64_t t, int64_t 
     }
 }
 
-// One token a CTA, up to kRows rows of it a warp at a time. kWrite: K and V rows go to the pools as E4M3;
-// else K (if any) to k_out.
-template <typename T, bool kHalf, bool kWrite>
+// One token a CTA, up to kRows rows of it a warp at a time. K and V rows go to the pools;
+// To::kRows: K (if any) to k_out.
+template <typename T, bool kHalf, To kTo, bool kNorm>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_kernel(const RopeParams p) {
+    constexpr bool kWrite = kTo != To::kRows;
     __shared__ __align__(16) float2 cs[kHeadDim / 2];
+    __shared__ __align__(16) float staged[kTo == To::kMx4 ? kWarps : 1][kTo == To::kMx4 ? kHeadDim : 4];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rows = p.num_q_heads + p.num_kv_heads * (kWrite ? 2 : (p.k ? 1 : 0));
     const int64_t t = blockIdx.x;
-    const int64_t slot = kWrite ? p.slots[t] : 0, live = live_tokens<kWrite>(p);
+    const int64_t slot = kWrite ? p.slots[t] : 0, live = live_tokens<kTo>(p);
     const int pos = p.positions[t];
     const T* q = static_cast<const T*>(p.q) + t * p.q_stride;
     const T* k = static_cast<const T*>(p.k) + t * p.k_stride;
     const T* v = static_cast<const T*>(p.v) + t * p.v_stride;
-    // this lane's two pieces of a row
     const bool turned = lane < p.rotary_dim / 8;
-    const int at = kHalf && turned ? 4 * lane : 8 * lane;
-    const int gap = kHalf && turned ? p.rotary_dim / 2 : 4;
+    auto piece = [&](int h) {
+        return pieces_of<kHalf, kTo>(lane, turned, p.rotary_dim, h >= p.num_kv_heads);
+    };
     for (int r0 = 0; r0 < rows; r0 += kRows * kWarps) {
         uint2 wa[kRows], wb[kRows];
 #pragma unroll
@@ -196,8 +315,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_kernel(const RopePa
             const T* src = h < 0 ? q + r * kHeadDim
                                  : (h < p.num_kv_heads ? k + h * kHeadDim
                                                        : v + (h - p.num_kv_heads) * kHeadDim);
-            wa[i] = __ldcs(reinterpret_cast<const uint2*>(src + at));
-            wb[i] = __ldcs(reinterpret_cast<const uint2*>(src + at + gap));
+            const Pieces pc = piece(h);
+            wa[i] = __ldcs(reinterpret_cast<const uint2*>(src + pc.at));
+            wb[i] = __ldcs(reinterpret_cast<const uint2*>(src + pc.at + pc.gap));
         }
         if (r0 == 0) {
             if (tid < p.rotary_dim / 2) cs[tid] = turn_of(p, pos, tid);
@@ -212,25 +332,29 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_kernel(const RopePa
         for (int i = 0; i < kRows; ++i) {
             const int r = r0 + i * kWarps + warp;
             if (r >= rows) break;
-            put_row<T, kHalf, kWrite>(p, t, slot, r, at, gap, turned, wa[i], wb[i], c, s,
-                                      [&](int hs) { return scale_of<kWrite>(p, hs); });
+            const Pieces pc = piece(r - p.num_q_heads);
+            put_row<T, kHalf, kTo, kNorm>(p, t, slot, r, pc.at, pc.gap, turned, wa[i], wb[i], c, s,
+                                          [&](int hs) { return scale_of<kTo>(p, hs); },
+                                          staged[kTo == To::kMx4 ? warp : 0]);
         }
     }
 }
 
 // kTokens tokens a CTA, for at most kWarps rows a token: warp w has row w of each of them.
-template <typename T, bool kHalf, bool kWrite, int kTokens>
+template <typename T, bool kHalf, To kTo, bool kNorm, int kTokens>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_tokens_kernel(const RopeParams p) {
+    constexpr bool kWrite = kTo != To::kRows;
     __shared__ __align__(16) float2 cs[kTokens][kHeadDim / 2];
+    __shared__ __align__(16) float staged[kTo == To::kMx4 ? kWarps : 1][kTo == To::kMx4 ? kHeadDim : 4];
     __shared__ int64_t slots[kTokens];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rows = p.num_q_heads + p.num_kv_heads * (kWrite ? 2 : (p.k ? 1 : 0));
     const int64_t t0 = (int64_t)blockIdx.x * kTokens, last = p.num_tokens - 1;
     const bool turned = lane < p.rotary_dim / 8;
-    const int at = kHalf && turned ? 4 * lane : 8 * lane;
-    const int gap = kHalf && turned ? p.rotary_dim / 2 : 4;
     // (what is past the last row or token is read again and not stored)
     const int r = min(warp, rows - 1), h = r - p.num_q_heads;
+    const Pieces pc = pieces_of<kHalf, kTo>(lane, turned, p.rotary_dim, h >= p.num_kv_heads);
+    const int at = pc.at, gap = pc.gap;
     const T* src;
     int64_t stride;
     if (h < 0) {
@@ -250,8 +374,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_tokens_kernel(const
         wa[i] = __ldcs(reinterpret_cast<const uint2*>(row + at));
         wb[i] = __ldcs(reinterpret_cast<const uint2*>(row + at + gap));
     }
-    const float scale = scale_of<kWrite>(p, h);
-    const int64_t live = live_tokens<kWrite>(p);
+    const float scale = scale_of<kTo>(p, h);
+    const int64_t live = live_tokens<kTo>(p);
     if (kWrite && tid < kTokens) {
         const int64_t slot = p.slots[min(t0 + tid, last)];
         if (slot >= p.num_slots) atomicOr(p.status, DFLASH_FLAG_SLOT_RANGE);
@@ -272,34 +396,53 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_tokens_kernel(const
         if (slot < 0 && t >= live) continue;  // padding
         float c[4], s[4];
         if (turned) lane_turns(cs[i], lane, c, s);
-        put_row<T, kHalf, kWrite>(p, t, slot, r, at, gap, turned, wa[i], wb[i], c, s,
-                                  [&](int) { return scale; });
+        put_row<T, kHalf, kTo, kNorm>(p, t, slot, r, at, gap, turned, wa[i], wb[i], c, s,
+                                      [&](int) { return scale; },
+                                      staged[kTo == To::kMx4 ? warp : 0]);
     }
 }
 
-template <typename T, bool kHalf, bool kWrite>
+template <typename T, bool kHalf, To kTo, bool kNorm>
 cudaError_t launch_as(const RopeParams& p, cudaStream_t stream) {
-    const int rows = p.num_q_heads + p.num_kv_heads * (kWrite ? 2 : (p.k ? 1 : 0));
+    const int rows = p.num_q_heads + p.num_kv_heads * (kTo != To::kRows ? 2 : (p.k ? 1 : 0));
     auto ctas = [&](int tokens) { return (unsigned)((p.num_tokens + tokens - 1) / tokens); };
     if (rows > kWarps)
-        rope_kernel<T, kHalf, kWrite><<<ctas(1), kThreads, 0, stream>>>(p);
+        rope_kernel<T, kHalf, kTo, kNorm><<<ctas(1), kThreads, 0, stream>>>(p);
     else if (p.num_tokens <= kTokensOne)
-        rope_tokens_kernel<T, kHalf, kWrite, 1><<<ctas(1), kThreads, 0, stream>>>(p);
+        rope_tokens_kernel<T, kHalf, kTo, kNorm, 1><<<ctas(1), kThreads, 0, stream>>>(p);
     else if (p.num_tokens <= kTokensTwo)
-        rope_tokens_kernel<T, kHalf, kWrite, 2><<<ctas(2), kThreads, 0, stream>>>(p);
+        rope_tokens_kernel<T, kHalf, kTo, kNorm, 2><<<ctas(2), kThreads, 0, stream>>>(p);
     else
-        rope_tokens_kernel<T, kHalf, kWrite, 4><<<ctas(4), kThreads, 0, stream>>>(p);
+        rope_tokens_kernel<T, kHalf, kTo, kNorm, 4><<<ctas(4), kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
-template <bool kWrite>
-cudaError_t launch(const dflash_rope_plan_t* plan, const RopeParams& p, cudaStream_t stream) {
+template <To kTo, bool kNorm>
+cudaError_t launch_typed(const dflash_rope_plan_t* plan, const RopeParams& p, cudaStream_t stream) {
     const bool half = plan->problem.layout == DFLASH_ROPE_HALF;
     if (plan->problem.dtype == DFLASH_FP16)
-        return half ? launch_as<__half, true, kWrite>(p, stream)
-                    : launch_as<__half, false, kWrite>(p, stream);
-    return half ? launch_as<__nv_bfloat16, true, kWrite>(p, stream)
-                : launch_as<__nv_bfloat16, false, kWrite>(p, stream);
+        return half ? launch_as<__half, true, kTo, kNorm>(p, stream)
+                    : launch_as<__half, false, kTo, kNorm>(p, stream);
+    return half ? launch_as<__nv_bfloat16, true, kTo, kNorm>(p, stream)
+                : launch_as<__nv_bfloat16, false, kTo, kNorm>(p, stream);
+}
+
+// One launch; without a norm, by kernels that have none.
+template <To kTo>
+int launch(const dflash_rope_plan_t* plan, RopeParams& p, const dflash_head_norm* norm,
+           void* cuda_stream) {
+    cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+    cudaError_t e;
+    if (norm && (norm->q_weight || norm->k_weight)) {
+        p.q_weight = norm->q_weight;
+        p.k_weight = norm->k_weight;
+        p.eps = norm->eps;
+        p.weight_offset = norm->weight_offset;
+        e = launch_typed<kTo, true>(plan, p, stream);
+    } else {
+        e = launch_typed<kTo, false>(plan, p, stream);
+    }
+    return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -356,7 +499,77 @@ int check_plan(const dflash_rope_plan_t* plan) {
     return check_problem(&plan->problem);
 }
 
+// A norm's own fields, and its weights apart from what the call writes.
+template <int kOuts>
+bool norm_ok(const dflash_head_norm* norm, const void* const (&outs)[kOuts]) {
+    if (!norm) return true;
+    if (!finite(norm->eps) || norm->eps < 0.f || !finite(norm->weight_offset) ||
+        !aligned(norm->q_weight, 16) || !aligned(norm->k_weight, 16))
+        return false;
+    for (int i = 0; i < kOuts; ++i)
+        if (outs[i] && (outs[i] == norm->q_weight || outs[i] == norm->k_weight)) return false;
+    return true;
+}
+
 double clamp01(double x) { return x < 0.0 ? 0.0 : (x > 1.0 ? 1.0 : x); }
+
+// The cache writes: checks and launch. k_scale and v_scale are To::kE4m3's.
+template <To kTo>
+int write(const dflash_rope_plan_t* plan, const dflash_head_norm* norm, int64_t num_tokens,
+          const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+          int64_t v_stride, const int32_t* positions, const int64_t* slots,
+          const int32_t* num_live, const uint64_t* phases, const float* k_scale,
+          const float* v_scale, void* q_out, int64_t q_out_stride, void* k_pool, void* v_pool,
+          int32_t* status, void* cuda_stream) {
+    constexpr bool kScaled = kTo == To::kE4m3;
+    constexpr size_t kPoolAlign = kScaled ? 8 : 16;
+    const int rc = check_plan(plan);
+    if (rc != DFLASH_OK) return rc;
+    const dflash_rope_problem& pr = plan->problem;
+    if (!kScaled && pr.page_size % mx4::kTokens != 0) return DFLASH_ERR_UNSUPPORTED;
+    if (num_tokens < 0 || num_tokens > kMaxTokens) return DFLASH_ERR_INVALID_ARGUMENT;
+    if (num_tokens == 0) return DFLASH_OK;
+    if (!rows_ok(q, q_stride, pr.num_q_heads) || !rows_ok(k, k_stride, pr.num_kv_heads) ||
+        !rows_ok(v, v_stride, pr.num_kv_heads) || !rows_ok(q_out, q_out_stride, pr.num_q_heads) ||
+        !positions || !aligned(positions, 4) || !slots || !aligned(slots, 8) || !phases ||
+        !aligned(phases, 8) ||
+        (kScaled &&
+         (!k_scale || !aligned(k_scale, 4) || !v_scale || !aligned(v_scale, 4))) ||
+        !k_pool || !aligned(k_pool, kPoolAlign) || !v_pool || !aligned(v_pool, kPoolAlign) ||
+        !status || !aligned(status, 4) || !aligned(num_live, 4) ||
+        (q == q_out && q_stride != q_out_stride))
+        return DFLASH_ERR_INVALID_ARGUMENT;
+    const void* const outs[] = {q_out, k_pool, v_pool, status};
+    const void* const others[] = {k, v, positions, slots, phases, k_scale, v_scale, num_live};
+    if (!distinct(outs, others) || k_pool == q || v_pool == q || status == q ||
+        !norm_ok(norm, outs))
+        return DFLASH_ERR_INVALID_ARGUMENT;
+    RopeParams p = {};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.positions = positions;
+    p.slots = slots;
+    p.num_live = num_live;
+    p.phases = phases;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.q_out = q_out;
+    p.q_out_stride = q_out_stride;
+    p.k_pool = static_cast<uint8_t*>(k_pool);
+    p.v_pool = static_cast<uint8_t*>(v_pool);
+    p.status = status;
+    p.num_tokens = num_tokens;
+    p.num_slots = (int64_t)pr.num_pages * pr.page_size;
+    p.num_q_heads = pr.num_q_heads;
+    p.num_kv_heads = pr.num_kv_heads;
+    p.rotary_dim = pr.rotary_dim;
+    p.amplitude = plan->amplitude;
+    return launch<kTo>(plan, p, norm, cuda_stream);
+}
 
 }  // namespace
 }  // namespace dflash
@@ -407,6 +620,15 @@ int dflash_rope_apply(const dflash_rope_plan_t* plan, int64_t num_tokens, const 
                       int64_t q_stride, const void* k, int64_t k_stride, const int32_t* positions,
                       const uint64_t* phases, void* q_out, int64_t q_out_stride, void* k_out,
                       int64_t k_out_stride, void* cuda_stream) {
+    return dflash_norm_rope_apply(plan, nullptr, num_tokens, q, q_stride, k, k_stride, positions,
+                                  phases, q_out, q_out_stride, k_out, k_out_stride, cuda_stream);
+}
+
+int dflash_norm_rope_apply(const dflash_rope_plan_t* plan, const dflash_head_norm* norm,
+                           int64_t num_tokens, const void* q, int64_t q_stride, const void* k,
+                           int64_t k_stride, const int32_t* positions, const uint64_t* phases,
+                           void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                           void* cuda_stream) {
     const int rc = check_plan(plan);
     if (rc != DFLASH_OK) return rc;
     const dflash_rope_problem& pr = plan->problem;
@@ -421,7 +643,7 @@ int dflash_rope_apply(const dflash_rope_plan_t* plan, int64_t num_tokens, const 
         return DFLASH_ERR_INVALID_ARGUMENT;
     const void* const outs[] = {q_out, k_out};
     const void* const others[] = {positions, phases};
-    if (!distinct(outs, others) || q_out == k || (k && k_out == q))
+    if (!distinct(outs, others) || q_out == k || (k && k_out == q) || !norm_ok(norm, outs))
         return DFLASH_ERR_INVALID_ARGUMENT;
     RopeParams p = {};
     p.q = q;
@@ -439,9 +661,7 @@ int dflash_rope_apply(const dflash_rope_plan_t* plan, int64_t num_tokens, const 
     p.num_kv_heads = pr.num_kv_heads;
     p.rotary_dim = pr.rotary_dim;
     p.amplitude = plan->amplitude;
-    return launch<false>(plan, p, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
-               ? DFLASH_OK
-               : DFLASH_ERR_CUDA;
+    return launch<To::kRows>(plan, p, norm, cuda_stream);
 }
 
 int dflash_rope_kv_write(const dflash_rope_plan_t* plan, int64_t num_tokens, const void* q,
@@ -462,50 +682,34 @@ int dflash_rope_kv_write_live(const dflash_rope_plan_t* plan, int64_t num_tokens
                               const float* k_scale, const float* v_scale, void* q_out,
                               int64_t q_out_stride, void* k_pool, void* v_pool, int32_t* status,
                               void* cuda_stream) {
-    const int rc = check_plan(plan);
-    if (rc != DFLASH_OK) return rc;
-    const dflash_rope_problem& pr = plan->problem;
-    if (num_tokens < 0 || num_tokens > kMaxTokens) return DFLASH_ERR_INVALID_ARGUMENT;
-    if (num_tokens == 0) return DFLASH_OK;
-    if (!rows_ok(q, q_stride, pr.num_q_heads) || !rows_ok(k, k_stride, pr.num_kv_heads) ||
-        !rows_ok(v, v_stride, pr.num_kv_heads) || !rows_ok(q_out, q_out_stride, pr.num_q_heads) ||
-        !positions || !aligned(positions, 4) || !slots || !aligned(slots, 8) || !phases ||
-        !aligned(phases, 8) || !k_scale || !aligned(k_scale, 4) || !v_scale ||
-        !aligned(v_scale, 4) || !k_pool || !aligned(k_pool, 8) || !v_pool ||
-        !aligned(v_pool, 8) || !status || !aligned(status, 4) || !aligned(num_live, 4) ||
-        (q == q_out && q_stride != q_out_stride))
-        return DFLASH_ERR_INVALID_ARGUMENT;
-    const void* const outs[] = {q_out, k_pool, v_pool, status};
-    const void* const others[] = {k, v, positions, slots, phases, k_scale, v_scale, num_live};
-    if (!distinct(outs, others) || k_pool == q || v_pool == q || status == q)
-        return DFLASH_ERR_INVALID_ARGUMENT;
-    RopeParams p = {};
-    p.q = q;
-    p.k = k;
-    p.v = v;
-    p.q_stride = q_stride;
-    p.k_stride = k_stride;
-    p.v_stride = v_stride;
-    p.positions = positions;
-    p.slots = slots;
-    p.num_live = num_live;
-    p.phases = phases;
-    p.k_scale = k_scale;
-    p.v_scale = v_scale;
-    p.q_out = q_out;
-    p.q_out_stride = q_out_stride;
-    p.k_pool = static_cast<uint8_t*>(k_pool);
-    p.v_pool = static_cast<uint8_t*>(v_pool);
-    p.status = status;
-    p.num_tokens = num_tokens;
-    p.num_slots = (int64_t)pr.num_pages * pr.page_size;
-    p.num_q_heads = pr.num_q_heads;
-    p.num_kv_heads = pr.num_kv_heads;
-    p.rotary_dim = pr.rotary_dim;
-    p.amplitude = plan->amplitude;
-    return launch<true>(plan, p, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
-               ? DFLASH_OK
-               : DFLASH_ERR_CUDA;
+    return dflash_norm_rope_kv_write(plan, nullptr, num_tokens, q, q_stride, k, k_stride, v,
+                                     v_stride, positions, slots, num_live, phases, k_scale,
+                                     v_scale, q_out, q_out_stride, k_pool, v_pool, status,
+                                     cuda_stream);
+}
+
+int dflash_norm_rope_kv_write(const dflash_rope_plan_t* plan, const dflash_head_norm* norm,
+                              int64_t num_tokens, const void* q, int64_t q_stride, const void* k,
+                              int64_t k_stride, const void* v, int64_t v_stride,
+                              const int32_t* positions, const int64_t* slots,
+                              const int32_t* num_live, const uint64_t* phases,
+                              const float* k_scale, const float* v_scale, void* q_out,
+                              int64_t q_out_stride, void* k_pool, void* v_pool, int32_t* status,
+                              void* cuda_stream) {
+    return write<To::kE4m3>(plan, norm, num_tokens, q, q_stride, k, k_stride, v, v_stride,
+                            positions, slots, num_live, phases, k_scale, v_scale, q_out,
+                            q_out_stride, k_pool, v_pool, status, cuda_stream);
+}
+
+int dflash_mx4_kv_write(const dflash_rope_plan_t* plan, const dflash_head_norm* norm,
+                        int64_t num_tokens, const void* q, int64_t q_stride, const void* k,
+                        int64_t k_stride, const void* v, int64_t v_stride,
+                        const int32_t* positions, const int64_t* slots, const int32_t* num_live,
+                        const uint64_t* phases, void* q_out, int64_t q_out_stride, void* k_pool,
+                        void* v_pool, int32_t* status, void* cuda_stream) {
+    return write<To::kMx4>(plan, norm, num_tokens, q, q_stride, k, k_stride, v, v_stride,
+                           positions, slots, num_live, phases, nullptr, nullptr, q_out,
+                           q_out_stride, k_pool, v_pool, status, cuda_stream);
 }
 
 }  // extern "C"
