@@ -1,14 +1,37 @@
-// mx4_attn.cu -- attention of drafted tokens over the 4-bit cache (dflash_mx4_attn_*): the partial kernel and
-// its entry points. Splits, slots, split state and combine are those of the E4M3 attention.
+// mx4_attn.cu -- attention of drafted tokens over the 4-bit cache (dflash_mx4_attn_*): the tensor-core partial
+// kernel and its entry points. Splits, slots, split state and combine are those of the E4M3 attention.
 //
-// CUDA-core kernel: one CTA per (split, KV head, sequence) and block of up to 48 rows, 32 keys at a time, all in
-// FP32.
+// One CTA per (split, KV head, sequence) and block of up to 48 query rows. Both products have FP16 operands
+// (every number of the cache times a power of two is exact, Q is FP16, P is rounded to it) and FP32 sums, keys or
+// head-dim elements on the 128 lanes: S^T = K Q^T and O^T = V^T P^T. What bounds such a kernel is shared
+// memory: stored there as FP16, a tile of 128 keys would be written (128 KB) and read by the tensor core
+// (128 KB), 2048 clocks of 128 bytes, while its codes come from HBM in 1500. So neither K nor V goes there
+// decoded: both are the products' first operand, which may lie in tensor memory, and warps write it from
+// registers, a lane a key of K, or an element of the head (two: i and i + 128) of V. The cache's layout
+// is made for that (dflash_mx4_cache.h): a thread reads its codes in 16-byte pieces without bank
+// conflicts, and a chunk of 16 tokens comes by one bulk copy.
+//
+//  * Scales. A key of K is brought to 2^12 of its largest block's power and the rest, one power of two a
+//    key, goes into the factor of its scores. V's rest goes into the weights: with ev = the key's largest
+//    exponent (cut to +-40) the kernel takes p = 2^(s + ev - m), m the reference of s + ev, sums p 2^-ev
+//    for the denominator and multiplies p by v 2^-ev. A weight is so large only if its value is.
+//  * Probabilities are p 2^8 of a row's first maximum and move their reference past 2^15: below 2^-14
+//    FP16 has a fixed step, 2^-24, 2^-32 of the largest at least.
+//  * NaN. A key with a NaN scale in K or V gets a NaN factor or exponent: its probability is NaN in
+//    every row that sees it and 0, selected, in the others. V's own factor is then 0.
+//  * Warps: 0 and 2 copy K and V (five tiles ahead), 1 issues the products, 3 works out the factors of a
+//    tile's keys, 4-7 decode K, 8-11 V, the others are the softmax, four for 16 rows.
+//  * Every wait on another warp or on a copy is bounded: on a timeout the CTA sets
+//    DFLASH_FLAG_KERNEL_TIMEOUT, drains its copies and returns.
 #include <cuda_runtime.h>
 #include <math.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "dflash_mx4_cache.h"
 #include "mx4.cuh"
+#include "tc_ptx.cuh"
 
 namespace dflash {
 int check_attn_plan(const dflash_verify_attn_plan_t* plan);
@@ -20,187 +43,794 @@ CombineParams combine_params(const dflash_verify_attn_plan_t* plan, const void* 
                              const int32_t* context_lens, void* out, float* lse);
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream);
 
-namespace {
+namespace mx4 {
 
-constexpr int kThreads = 256;
-constexpr int kRows = 48;
-constexpr int kTile = 32;
-constexpr int kKStride = kHeadDim + 1;
-constexpr int kPStride = kTile + 1;
-constexpr size_t kSmem =
-    sizeof(float) * (kRows * kHeadDim + kTile * kKStride + kTile * kHeadDim + kRows * kPStride + kRows);
+using namespace ptx;
 
-__device__ __forceinline__ float warp_max(float v) {
+constexpr int kTile = 128;       // keys per tile = MMA M
+constexpr int kChunks = kTile / kTokens;
+constexpr int kMaxRP = 48;       // padded rows a CTA carries
+constexpr int kGroupRows = 16;
+constexpr int kStages = 5;       // tiles of codes of K, and of V, on their way
+constexpr int kInfos = 4;        // tiles of factors
+constexpr uint32_t kStageBytes = kChunks * kChunkBytes;
+constexpr uint64_t kWaitLimitNs = 200ull * 1000 * 1000;
+constexpr float kShift = 8.f;          // probabilities are 2^8 at the reference
+constexpr float kLazyThreshold = 15.f; // largest exponent of one
+constexpr int kFactorTop = 12;         // a key's largest block is brought to 2^12
+constexpr int kMaxEv = 40;
+constexpr int kKWarp = 4, kVWarp = 8, kSoftWarp = 12;
+
+// Shared memory: Q | P | codes of K | codes of V | factors | Small. Tensor memory: K [two head-dim
+// halves][64] | V [two halves of the keys][two of the head dim][32] | S [two tiles][RP] | O [two halves of
+// the head dim][RP].
+template <int RP>
+struct Cfg {
+    static constexpr int kGroups = RP / kGroupRows;
+    static constexpr int kSoftWarps = 4 * kGroups;
+    static constexpr int kThreads = 32 * (kSoftWarp + kSoftWarps);
+    static constexpr uint32_t kOffP = RP * kHeadDim * 2;
+    static constexpr uint32_t kOffK = kOffP + RP * kTile * 2;
+    static constexpr uint32_t kOffV = kOffK + kStages * kStageBytes;
+    static constexpr uint32_t kOffInfo = kOffV + kStages * kStageBytes;
+    static constexpr uint32_t kColK = 0, kColV = 128, kColS = 256, kColO = kColS + 2 * RP;
+    static constexpr uint32_t kTmemCols = 512;
+    static_assert(RP % kGroupRows == 0 && RP <= kMaxRP, "rows per CTA");
+    static_assert(kColO + 2 * RP <= kTmemCols, "tensor memory");
+    static_assert(kOffP % 1024 == 0 && kOffK % 128 == 0 && kOffInfo % 16 == 0, "alignment");
+};
+
+// Factors of a tile's keys: of their scores (in log2 units), V's exponent, and of V's blocks (FP16).
+struct Info {
+    float c[kTile];
+    float ev[kTile];
+    uint16_t f[kBlocks][kTile];
+};
+
+struct Small {
+    uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
+    uint64_t infofull[kInfos], infofree[kInfos];
+    uint64_t kafull[2], kafree[2], vafull[2], vafree[2];  // halves of the operands in tensor memory
+    uint64_t sfull[2], sfree[2], pfull, pfree, odone, qready;
+    uint32_t tmem_base;
+    int abort;
+    float rmax[kMaxRP / kGroupRows][4][kGroupRows];   // per-group, per-warp row maxima of a tile
+    float rsum[kMaxRP / kGroupRows][4][kGroupRows];   // per-group, per-warp row sums of the split
+    float mref[kMaxRP / kGroupRows][kGroupRows];      // the split state's max of each row
+    float nmcur[kMaxRP / kGroupRows][4][kGroupRows];  // each warp's copy of the shift minus the reference
+};
+
+template <int RP>
+constexpr uint32_t smem_bytes() {
+    return Cfg<RP>::kOffInfo + kInfos * sizeof(Info) + sizeof(Small);
+}
+static_assert(smem_bytes<kMaxRP>() <= 227 * 1024, "shared memory budget");
+static_assert(sizeof(Info) % 16 == 0, "factors are read in 16-byte pieces");
+
+// Byte offset of (row, 16-byte piece u of its 512 bytes) of Q: K-major with the 128-byte swizzle, 8-row groups
+// 1 KB apart, blocks of 64 elements rows * 128 bytes apart.
+__device__ __forceinline__ uint32_t q_off(int row, int u, int rows) {
+    return (u >> 3) * rows * 128 + (row >> 3) * 1024 + (row & 7) * 128 + (((u & 7) ^ (row & 7)) << 4);
+}
+// P: MN-major without swizzle, core matrices of 8 rows x 8 keys (a key's 8 rows are 16 bytes): key groups 128
+// bytes apart (the descriptor's leading offset), blocks of 8 rows 2 KB (its stride offset).
+__device__ __forceinline__ uint32_t p_off(int row_block, int key) {
+    return row_block * 2048 + (key >> 3) * 128 + (key & 7) * 16;
+}
+
+__device__ __forceinline__ float f32(uint32_t x) { return __uint_as_float(x); }
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a),
+                              *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// 2^e as FP16 bits, for e <= 13; 0 below 2^-14.
+__device__ __forceinline__ uint32_t f16_power(int e) { return e < -14 ? 0u : (uint32_t)(e + 15) << 10; }
+
+// D += A B^T over 16 elements of K, FP16: A in tensor memory (a lane a row, two elements a column).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// kChunkBytes from global to shared memory (both 16-byte aligned).
+__device__ __forceinline__ void copy_chunk(uint32_t dst, const uint8_t* src, uint32_t bar,
+                                           uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1], %2, [%3], %4;" ::"r"(dst),
+        "l"(src), "r"((uint32_t)kChunkBytes), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 7) == 0) {
+            if (*abort) return false;
+            if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
+        }
+    }
+}
+
+struct Ctx {
+    Small* sm;
+    int32_t* status;
+    __device__ bool wait(uint64_t* bar, uint32_t parity) const {
+        if (bar_wait(smem_u32(bar), parity, &sm->abort)) return true;
+        *reinterpret_cast<volatile int*>(&sm->abort) = 1;
+        atomicOr(status, DFLASH_FLAG_KERNEL_TIMEOUT);
+        return false;
+    }
+    // by a whole warp, whose lanes agree on the result
+    __device__ bool wait_warp(uint64_t* bar, uint32_t parity) const {
+        const bool ok = wait(bar, parity);
+        return __all_sync(0xffffffffu, ok);
+    }
+    __device__ bool aborted() const { return *reinterpret_cast<volatile int*>(&sm->abort) != 0; }
+};
+
+// This warp has done with what `bar` counts.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(bar));
+}
+// ... and its stores to tensor memory are complete.
+__device__ __forceinline__ void warp_arrive_tmem(uint64_t* bar) {
+    tmem_st_wait();
+    tc_fence_before();
+    warp_arrive(bar);
+}
+
+// Named barrier of one softmax group's 128 threads, optionally OR-reducing a vote. All four warps run every
+// tile (a failed wait skips work, never the loop), so each is always reached by all of them.
+__device__ __forceinline__ bool group_vote(int g, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred pv, pr;\n\t"
+        "setp.ne.u32 pv, %1, 0;\n\t"
+        "bar.red.or.pred pr, %2, 128, pv;\n\t"
+        "selp.u32 %0, 1, 0, pr;\n\t}"
+        : "=r"(r)
+        : "r"(v ? 1u : 0u), "r"(1 + g)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void group_bar(int g) {
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
+}
+
+// A transposed butterfly over the warp: each step trades half of the rows with the lane `off` away, so that
+// lane l ends with op over the lanes of row (l >> 1) & 15.
+template <typename Op>
+__device__ __forceinline__ float rows_reduce(float (&v)[kGroupRows], int lane, Op op) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
-}
-__device__ __forceinline__ float warp_sum(float v) {
+    for (int half = kGroupRows / 2, off = 16; half >= 1; half >>= 1, off >>= 1) {
+        const bool upper = (lane & off) != 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+        for (int j = 0; j < half; ++j) {
+            const float keep = upper ? v[j + half] : v[j];
+            const float send = upper ? v[j] : v[j + half];
+            v[j] = op(keep, __shfl_xor_sync(0xffffffffu, send, off));
+        }
+    }
+    return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
-__device__ __forceinline__ float code_number(uint32_t code) {
-    const uint32_t h = mx4::codes_to_f16x2<0>(code & 15u);
-    return __half2float(__ushort_as_half((unsigned short)(h & 0xFFFFu)));
+__device__ __forceinline__ int largest_byte(uint2 s) {
+    const uint32_t m4 = __vmaxu4(s.x, s.y);
+    const uint32_t m2 = __vmaxu4(m4, m4 >> 16);
+    return (int)(max(m2 & 255u, (m2 >> 8) & 255u));
 }
 
-__global__ void __launch_bounds__(kThreads, 1) mx4_partial_kernel(PartialParams p) {
-    extern __shared__ float smem[];
-    float* Qs = smem;
-    float* Ks = Qs + kRows * kHeadDim;
-    float* Vs = Ks + kTile * kKStride;
-    float* Ps = Vs + kTile * kHeadDim;
-    float* alpha_s = Ps + kRows * kPStride;
-    __shared__ float key_nan[kTile];  // NaN where a scale of V is
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// The warp's copies of one pool: tile after tile into its ring. Lane c < 8 copies chunk c of a tile; the block
+// table is looked up by all lanes for four tiles at a time, ahead.
+struct Copier {
+    const PartialParams& p;
+    const uint8_t* pool;
+    int b, h, start, end, lane;
+    bool clamped;
+    // pool chunk of the chunk that starts at key j (-1 past the end)
+    __device__ int64_t chunk_of(int j) {
+        if (j >= end) return -1;
+        const int lp = p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
+        const int phys = physical_page(p.block_table, b, p.max_pages_per_seq, lp, p.num_pages,
+                                       &clamped);
+        return (int64_t)phys * (p.page_size / kTokens) + (j - lp * p.page_size) / kTokens;
+    }
+    // the chunk that this lane's place among four tiles from tile t on has
+    __device__ int64_t ahead(int t) { return chunk_of(start + t * kTile + lane * kTokens); }
+};
+
+__device__ __forceinline__ void copy_tiles(const PartialParams& p, const Ctx& ctx, const uint8_t* pool,
+                                           uint8_t* ring, uint64_t* full, uint64_t* empty, int b,
+                                           int h, int start, int end, int ntiles, int drafted) {
+    const int lane = threadIdx.x & 31;
+    const uint64_t policy = l2_evict_first_policy();  // every page is read once
+    Copier c{p, pool, b, h, start, end, lane, false};
+    int64_t next = c.ahead(0), now = -1;
+    bool dep_done = false;
+    int t = 0;
+    for (; t < ntiles; ++t) {
+        if ((t & 3) == 0) {
+            now = next;
+            next = c.ahead(t + 4);
+        }
+        const int s = t % kStages;
+        if (!ctx.wait_warp(&empty[s], ((t / kStages) & 1) ^ 1)) break;
+        // keys from `drafted` on may be written by the kernel just before this one
+        if (!dep_done && start + (t + 1) * kTile > drafted) {
+            griddep_wait();
+            dep_done = true;
+        }
+        const int64_t chunk = __shfl_sync(0xffffffffu, now, (t & 3) * kChunks + (lane & 7));
+        const int n = min(kChunks, (end - start - t * kTile + kTokens - 1) / kTokens);
+        if (lane == 0) mbar_arrive_expect_tx(smem_u32(&full[s]), n * kChunkBytes);
+        __syncwarp();
+        if (lane < n)
+            copy_chunk(smem_u32(ring + s * kStageBytes + lane * kChunkBytes),
+                       pool + (chunk * p.num_kv_heads + h) * kChunkBytes, smem_u32(&full[s]), policy);
+    }
+    if (c.clamped) atomicOr(p.status, DFLASH_FLAG_PAGE_CLAMPED);
+    // no copy may still be writing shared memory when the CTA retires
+    __syncwarp();
+    if (lane == 0)
+        for (int u = t - kStages < 0 ? 0 : t - kStages; u < t; ++u)
+            mbar_wait(smem_u32(&full[u % kStages]), (u / kStages) & 1, &ctx.sm->abort, kWaitLimitNs);
+}
+
+template <int RP>
+__global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
+    mx4_partial_kernel(const PartialParams p) {
+    using C = Cfg<RP>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Info* const infos = reinterpret_cast<Info*>(smem + C::kOffInfo);
+    Small& sm = *reinterpret_cast<Small*>(smem + C::kOffInfo + kInfos * sizeof(Info));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const RowBlock rblk = row_block(p);
+    const int R = rblk.rows, row_lo = rblk.row_lo, G = p.group, slot = rblk.slot;
     griddep_launch_dependents();
-    const RowBlock rb = row_block(p);
-    const int G = p.group, R = rb.rows, row_lo = rb.row_lo, slot = rb.slot;
-    const UnitSlots us = locate_slots(p.context_lens, p.batch, p.num_kv_heads, p.num_splits,
-                                      p.num_slots, p.max_context, p.q_len, slot, true);
+    const UnitSlots us =
+        p.batch == 1 ? locate_slots_single(p.context_lens, p.num_kv_heads, p.num_splits,
+                                           p.max_context, p.q_len, blockIdx.y, false)
+                     : locate_slots(p.context_lens, p.batch, p.num_kv_heads, p.num_splits,
+                                    p.num_slots, p.max_context, p.q_len, slot, true);
     if (slot == 0 && tid == 0 && us.flags) atomicOr(p.status, us.flags);
     const int b = us.b, h = us.h, split = slot - us.first, n = us.n;
     if (b < 0) return;
-    const int per = keys_per_split(n, us.count, p.tile_keys, p.min_split_keys);
+    const int per = keys_per_split(n, us.count, kTile, p.min_split_keys);
     const int start = split * per;
-    if (start >= n) return;
+    if (start >= n) return;  // idle slot: the combine never reads it
     const int end = min(n, start + per);
-    griddep_wait();
-    for (int idx = tid; idx < kRows * kHeadDim; idx += kThreads) {
-        const int r = idx / kHeadDim, d = idx % kHeadDim;
-        float v = 0.f;
-        if (r < R) {
-            const int i = (row_lo + r) / G, g = (row_lo + r) % G;
-            const int64_t qrow = ((int64_t)b * p.q_len + i) * p.num_q_heads + h * G + g;
-            v = __half2float(p.q[qrow * kHeadDim + d]) * (0.0625f * kLog2e);
-            if (fabsf(v) == INFINITY) v = NAN;
+    const int ntiles = (end - start + kTile - 1) / kTile;
+    if (smem_u32(smem) & 1023u) {  // the swizzled layouts need a 1 KB aligned base
+        if (tid == 0) atomicOr(p.status, DFLASH_FLAG_KERNEL_TIMEOUT);
+        return;
+    }
+    const Ctx ctx{&sm, p.status};
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_u32(&sm.kfull[i]), 1);
+            mbar_init(smem_u32(&sm.vfull[i]), 1);
+            mbar_init(smem_u32(&sm.kempty[i]), 5);  // four decoders and the factors' warp
+            mbar_init(smem_u32(&sm.vempty[i]), 5);
         }
-        Qs[idx] = v;
+        for (int i = 0; i < kInfos; ++i) {
+            mbar_init(smem_u32(&sm.infofull[i]), 1);
+            mbar_init(smem_u32(&sm.infofree[i]), 4 + C::kSoftWarps);  // V's decoders, softmax
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sm.kafull[i]), 4);
+            mbar_init(smem_u32(&sm.kafree[i]), 1);
+            mbar_init(smem_u32(&sm.vafull[i]), 4);
+            mbar_init(smem_u32(&sm.vafree[i]), 1);
+            mbar_init(smem_u32(&sm.sfull[i]), 1);
+            mbar_init(smem_u32(&sm.sfree[i]), C::kSoftWarps);
+        }
+        mbar_init(smem_u32(&sm.pfull), C::kSoftWarps);
+        mbar_init(smem_u32(&sm.pfree), 1);
+        mbar_init(smem_u32(&sm.odone), 1);
+        mbar_init(smem_u32(&sm.qready), C::kSoftWarps);
+        sm.abort = 0;
+        fence_mbar_init();
     }
-    float m_run[kRows / 8], l_run[kRows / 8], acc[kRows];
-#pragma unroll
-    for (int m = 0; m < kRows / 8; ++m) {
-        m_run[m] = -INFINITY;
-        l_run[m] = 0.f;
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&sm.tmem_base), C::kTmemCols);
+        tmem_relinquish();
     }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+
+    if (warp == 0) {
+        copy_tiles(p, ctx, p.k_pool, smem + C::kOffK, sm.kfull, sm.kempty, b, h, start, end, ntiles,
+                   n - p.q_len);
+    } else if (warp == 2) {
+        copy_tiles(p, ctx, p.v_pool, smem + C::kOffV, sm.vfull, sm.vempty, b, h, start, end, ntiles,
+                   n - p.q_len);
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- products
+        // One thread, one loop over two streams of half tiles: S of the head dim's halves, O of the
+        // keys' halves. Neither waits for the other; O goes first where both are ready.
+        if (lane == 0 && ctx.wait(&sm.qready, 0)) {
+            const uint32_t idesc_s = idesc_f32acc(128, RP, 0, 0, 0, 0);
+            const uint32_t idesc_o = idesc_f32acc(128, RP, 0, 0, 0, 1);
+            const uint32_t q_base = smem_u32(smem), p_base = smem_u32(smem + C::kOffP);
+            const int halves = 2 * ntiles;
+            int us_ = 0, uo = 0;
+            uint64_t last = globaltimer_ns();
+            uint32_t idle = 0;
+            while (us_ < halves || uo < halves) {
+                bool progressed = false;
+                if (uo < halves) {
+                    const int t = uo >> 1, hv = uo & 1;
+                    if (mbar_test_wait(smem_u32(&sm.vafull[hv]), t & 1) &
+                        mbar_test_wait(smem_u32(&sm.pfull), t & 1)) {
+                        tc_fence_after();
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) acc[r] = 0.f;
-    bool page_clamped = false;
-    for (int t0 = start; t0 < end; t0 += kTile) {
-        __syncthreads();
-        {
-            const int kk = tid >> 3, part = tid & 7, j = t0 + kk;
-            if (part == 0) key_nan[kk] = 0.f;
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const uint64_t bd = smem_desc(p_base + (4 * hv + kk) * 256, 128, 2048,
+                                                          kSwizzleNone);
+#pragma unroll
+                            for (int mh = 0; mh < 2; ++mh)
+                                mma_ts(tmem + C::kColO + mh * RP,
+                                       tmem + C::kColV + hv * 64 + mh * 32 + kk * 8, bd, idesc_o,
+                                       (uo | kk) != 0);
+                        }
+                        mma_commit(smem_u32(&sm.vafree[hv]));
+                        if (hv) mma_commit(smem_u32(&sm.pfree));
+                        ++uo;
+                        progressed = true;
+                    }
+                }
+                if (us_ < halves) {
+                    const int t = us_ >> 1, hd = us_ & 1;
+                    if (mbar_test_wait(smem_u32(&sm.kafull[hd]), t & 1) &
+                        (hd ? true : mbar_test_wait(smem_u32(&sm.sfree[t & 1]), ((t >> 1) & 1) ^ 1))) {
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk) {
+                            const int ks = 8 * hd + kk;
+                            const uint64_t bd = smem_desc(
+                                q_base + (ks >> 2) * (RP * 128) + (ks & 3) * 32, 16, 1024,
+                                kSwizzle128B);
+                            mma_ts(tmem + C::kColS + (t & 1) * RP,
+                                   tmem + C::kColK + hd * 64 + kk * 8, bd, idesc_s, ks != 0);
+                        }
+                        mma_commit(smem_u32(&sm.kafree[hd]));
+                        if (hd) mma_commit(smem_u32(&sm.sfull[t & 1]));
+                        ++us_;
+                        progressed = true;
+                    }
+                }
+                if (progressed) {
+                    idle = 0;
+                    last = globaltimer_ns();
+                } else if ((++idle & 15) == 0) {
+                    if (ctx.aborted()) break;
+                    if (globaltimer_ns() - last > kWaitLimitNs) {
+                        *reinterpret_cast<volatile int*>(&sm.abort) = 1;
+                        atomicOr(p.status, DFLASH_FLAG_KERNEL_TIMEOUT);
+                        break;
+                    }
+                }
+            }
+        }
+        if (lane == 0) mma_commit(smem_u32(&sm.odone));  // tracks every product issued above
+    } else if (warp == 3) {
+        // ---------------------------------------------------------------- factors of a tile's keys
+        constexpr float kScore = 0.0625f * kLog2e / (1 << kFactorTop);  // D^-1/2 = 1/16
+        for (int t = 0; t < ntiles; ++t) {
+            const int s = t % kStages, is = t % kInfos;
+            if (!ctx.wait_warp(&sm.infofree[is], ((t / kInfos) & 1) ^ 1) ||
+                !ctx.wait_warp(&sm.kfull[s], (t / kStages) & 1) ||
+                !ctx.wait_warp(&sm.vfull[s], (t / kStages) & 1))
+                break;
+            Info& info = infos[is];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int key = lane + 32 * i;
+                const uint32_t at = (key / kTokens) * kChunkBytes + kCodeBytes + (key % kTokens) * kBlocks;
+                const uint2 ks = *reinterpret_cast<const uint2*>(smem + C::kOffK + s * kStageBytes + at);
+                const uint2 vs = *reinterpret_cast<const uint2*>(smem + C::kOffV + s * kStageBytes + at);
+                const bool valid = start + t * kTile + key < end;
+                const int ke = largest_byte(ks), ve = largest_byte(vs);
+                info.c[key] = ke == kNanScale ? NAN : __int_as_float(ke << 23) * kScore;
+                const int ev = max(-kMaxEv, min(kMaxEv, ve - 127));
+                info.ev[key] = !valid ? 0.f : (ve == kNanScale ? NAN : (float)ev);
+                // block j's factor is 2^(s - 127 - ev + 12): at most 2^13, and 0 for NaN, for blocks
+                // 2^26 below the key's largest and for keys past the split's end
+                const int base = 127 + ev - kFactorTop;
+#pragma unroll
+                for (int j = 0; j < kBlocks; ++j) {
+                    const int sj = (int)(((j < 4 ? vs.x : vs.y) >> (8 * (j & 3))) & 255u);
+                    const uint32_t f = f16_power(min(sj - base, kFactorTop + 1));
+                    info.f[j][key] = (uint16_t)(valid && sj != kNanScale ? f : 0u);
+                }
+            }
             __syncwarp();
-            if (j < end) {
-                const int phys = physical_page(p.block_table, b, p.max_pages_per_seq,
-                                               j / p.page_size, p.num_pages, &page_clamped);
-                const int64_t s = (int64_t)phys * p.page_size + j % p.page_size;
-                const int64_t at = mx4::chunk_offset(s, p.num_kv_heads, h);
-                const int tok = (int)(s % mx4::kTokens);
-                const int scale = mx4::kCodeBytes + tok * mx4::kBlocks + part;
-                const float kp = mx4::power_of_scale(p.k_pool[at + scale]);
-                float vp = mx4::power_of_scale(p.v_pool[at + scale]);
-                if (vp != vp) {
-                    key_nan[kk] = NAN;
-                    vp = 0.f;
-                }
-                for (int e = 0; e < 32; ++e) {
-                    const int d = part * 32 + e;
-                    const uint32_t kc = p.k_pool[at + part * 256 + tok * 16 + e / 2];
-                    const uint32_t vc = p.v_pool[at + (d % 128) * 16 + tok];
-                    Ks[kk * kKStride + d] = code_number(kc >> (4 * (e & 1))) * kp;
-                    Vs[kk * kHeadDim + d] = code_number(vc >> (4 * (d / 128))) * vp;
-                }
-            } else {
-                for (int e = 0; e < 32; ++e)
-                    Ks[kk * kKStride + part * 32 + e] = Vs[kk * kHeadDim + part * 32 + e] = 0.f;
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&sm.kempty[s]));
+                mbar_arrive(smem_u32(&sm.vempty[s]));
+                mbar_arrive(smem_u32(&sm.infofull[is]));
             }
         }
-        __syncthreads();
-        float s[kRows / 8];
+    } else if (warp < kVWarp) {
+        // ---------------------------------------------------------------- K: lane = key
+        const int key = (warp - kKWarp) * 32 + lane;
+        const uint32_t at = (key / kTokens) * kChunkBytes + (key % kTokens) * 16;
+        const uint32_t scales = (key / kTokens) * kChunkBytes + kCodeBytes + (key % kTokens) * kBlocks;
+        for (int t = 0; t < ntiles; ++t) {
+            const int s = t % kStages;
+            if (!ctx.wait_warp(&sm.kfull[s], (t / kStages) & 1)) break;
+            const uint8_t* stage = smem + C::kOffK + s * kStageBytes;
+            const uint2 sc = *reinterpret_cast<const uint2*>(stage + scales);
+            const int top = largest_byte(sc) - kFactorTop;
+            bool ok = true;
 #pragma unroll
-        for (int m = 0; m < kRows / 8; ++m) s[m] = key_nan[lane];
-        for (int d = 0; d < kHeadDim; ++d) {
-            const float kv = Ks[lane * kKStride + d];
+            for (int hd = 0; hd < 2; ++hd) {
+                uint4 w[4];
 #pragma unroll
-            for (int m = 0; m < kRows / 8; ++m)
-                s[m] = fmaf(Qs[(warp + 8 * m) * kHeadDim + d], kv, s[m]);
-        }
-        const int j = t0 + lane;
+                for (int j = 0; j < 4; ++j)
+                    w[j] = *reinterpret_cast<const uint4*>(stage + at + (4 * hd + j) * 256);
+                if (hd) warp_arrive(&sm.kempty[s]);
+                ok = ok && ctx.wait_warp(&sm.kafree[hd], (t & 1) ^ 1);
+                if (!ok) break;
+                tc_fence_after();
 #pragma unroll
-        for (int m = 0; m < kRows / 8; ++m) {
-            const int r = warp + 8 * m;
-            const bool valid = r < R && j < end && j <= n - p.q_len + (row_lo + r) / G;
-            const float sv = valid ? s[m] : -INFINITY;
-            const float mn = fmaxf(m_run[m], warp_max(sv));
-            float pj = 0.f, alpha = 1.f;
-            if (mn != -INFINITY) {
-                pj = valid ? exp2f(sv - mn) : 0.f;
-                alpha = exp2f(m_run[m] - mn);
-            } else if (valid && sv != sv) {
-                pj = NAN;
+                for (int j = 0; j < 4; ++j) {
+                    const int sj = (int)(((hd ? sc.y : sc.x) >> (8 * j)) & 255u);
+                    const uint32_t f = f16_power(sj - top) * 0x00010001u;
+                    const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+                    uint32_t o[16];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        o[4 * i] = mul_f16x2(codes_to_f16x2<0>(u[i]), f);
+                        o[4 * i + 1] = mul_f16x2(codes_to_f16x2<1>(u[i]), f);
+                        o[4 * i + 2] = mul_f16x2(codes_to_f16x2<2>(u[i]), f);
+                        o[4 * i + 3] = mul_f16x2(codes_to_f16x2<3>(u[i]), f);
+                    }
+                    tmem_st16(lane_base + C::kColK + hd * 64 + j * 16, o);
+                }
+                warp_arrive_tmem(&sm.kafull[hd]);
             }
-            l_run[m] = l_run[m] * alpha + warp_sum(pj);
-            m_run[m] = mn;
-            Ps[r * kPStride + lane] = pj;
-            if (lane == 0) alpha_s[r] = alpha;
+            if (!ok) break;
         }
-        __syncthreads();
+    } else if (warp < kSoftWarp) {
+        // ---------------------------------------------------------------- V: lane = element (and + 128)
+        const int quad = warp & 3, e = quad * 32 + lane;
+        for (int t = 0; t < ntiles; ++t) {
+            const int s = t % kStages, is = t % kInfos;
+            if (!ctx.wait_warp(&sm.vfull[s], (t / kStages) & 1) ||
+                !ctx.wait_warp(&sm.infofull[is], (t / kInfos) & 1))
+                break;
+            const uint8_t* stage = smem + C::kOffV + s * kStageBytes + e * kTokens;
+            const uint16_t* f0 = infos[is].f[quad];
+            const uint16_t* f1 = infos[is].f[4 + quad];
+            bool ok = true;
+#pragma unroll 1
+            for (int hv = 0; hv < 2; ++hv) {
+                ok = ctx.wait_warp(&sm.vafree[hv], (t & 1) ^ 1);
+                if (!ok) break;
+                tc_fence_after();
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) acc[r] *= alpha_s[r];
-        for (int kk = 0; kk < kTile; ++kk) {
-            const float v = Vs[kk * kHeadDim + tid];
+                for (int it = 0; it < 2; ++it) {  // two chunks: 32 keys, 16 columns of each half
+                    uint32_t lo[16], hi[16];
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) acc[r] = fmaf(Ps[r * kPStride + kk], v, acc[r]);
+                    for (int c2 = 0; c2 < 2; ++c2) {
+                        const int c = 4 * hv + 2 * it + c2;
+                        const uint4 w = *reinterpret_cast<const uint4*>(stage + c * kChunkBytes);
+                        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {  // 8 keys
+                            const uint4 a = *reinterpret_cast<const uint4*>(f0 + c * kTokens + 8 * q);
+                            const uint4 d = *reinterpret_cast<const uint4*>(f1 + c * kTokens + 8 * q);
+                            const uint32_t fa[4] = {a.x, a.y, a.z, a.w}, fb[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                // four keys' bytes: the two keys of a pair into one byte, low halves
+                                // (element e) and high halves (e + 128)
+                                const uint32_t x = u[2 * q + i], x4 = x >> 4;
+                                const uint32_t l = (x & 0x000F000Fu) | (x4 & 0x00F000F0u);
+                                const uint32_t g = (x4 & 0x000F000Fu) | ((x >> 8) & 0x00F000F0u);
+                                const int o = 8 * c2 + 4 * q + 2 * i;
+                                lo[o] = mul_f16x2(codes_to_f16x2<0>(l), fa[2 * i]);
+                                lo[o + 1] = mul_f16x2(codes_to_f16x2<2>(l), fa[2 * i + 1]);
+                                hi[o] = mul_f16x2(codes_to_f16x2<0>(g), fb[2 * i]);
+                                hi[o + 1] = mul_f16x2(codes_to_f16x2<2>(g), fb[2 * i + 1]);
+                            }
+                        }
+                    }
+                    tmem_st16(lane_base + C::kColV + hv * 64 + it * 16, lo);
+                    tmem_st16(lane_base + C::kColV + hv * 64 + 32 + it * 16, hi);
+                }
+                if (hv) {
+                    warp_arrive(&sm.vempty[s]);
+                    warp_arrive(&sm.infofree[is]);
+                }
+                warp_arrive_tmem(&sm.vafull[hv]);
+            }
+            if (!ok) break;
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax
+        const int sw = warp - kSoftWarp;
+        const int g = sw >> 2;            // rows [16 g, 16 g + 16)
+        const int wq = warp & 3;          // tensor-memory lane quadrant
+        const int st = (wq << 5) | lane;  // key of the tile
+        const int row0 = kGroupRows * g;
+        const int qoff = n - p.q_len;  // row r of the slot sees keys j <= qoff + r / G
+        griddep_wait();
+        {
+            constexpr int kRowsPerWarp = RP / C::kSoftWarps;  // 4
+            uint4 qraw[kRowsPerWarp];
+#pragma unroll
+            for (int k = 0; k < kRowsPerWarp; ++k) {
+                const int r = sw + C::kSoftWarps * k;
+                qraw[k] = make_uint4(0, 0, 0, 0);
+                if (r < R) {
+                    const int i = (row_lo + r) / G, gg = (row_lo + r) % G;
+                    const int64_t qrow = ((int64_t)b * p.q_len + i) * p.num_q_heads + h * G + gg;
+                    qraw[k] = *reinterpret_cast<const uint4*>(p.q + qrow * kHeadDim + lane * 8);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kRowsPerWarp; ++k) {
+                // a row with an infinity is a row of NaN (its scores could all be -inf, as if it saw
+                // no key): exponent field all ones in any of its halves
+                auto inf_in = [&](uint32_t x) {
+                    return (x & 0x7C00u) == 0x7C00u || (x & 0x7C000000u) == 0x7C000000u;
+                };
+                const bool bad = inf_in(qraw[k].x) || inf_in(qraw[k].y) || inf_in(qraw[k].z) ||
+                                 inf_in(qraw[k].w);
+                if (__any_sync(0xffffffffu, bad)) qraw[k].x = 0x7E007E00u;
+                *reinterpret_cast<uint4*>(smem + q_off(sw + C::kSoftWarps * k, lane, RP)) = qraw[k];
+            }
+            fence_async_smem();
+            warp_arrive(&sm.qready);
+        }
+        uint64_t lsum[kGroupRows / 2];
+        uint64_t nm[kGroupRows / 2];  // the shift minus each row's reference (+inf: none yet), in pairs
+        uint32_t rowmask = 0;
+#pragma unroll
+        for (int i = 0; i < kGroupRows; ++i) rowmask |= (uint32_t)(row0 + i < R) << i;
+#pragma unroll
+        for (int q = 0; q < kGroupRows / 2; ++q) {
+            lsum[q] = 0;
+            nm[q] = pk2(INFINITY, INFINITY);
+        }
+        if (lane < kGroupRows) sm.nmcur[g][wq][lane] = INFINITY;
+        __syncwarp();
+        bool alive = true;
+        for (int t = 0; t < ntiles; ++t) {
+            const int tile0 = start + t * kTile, j = tile0 + st, is = t % kInfos;
+            if (alive && !ctx.wait_warp(&sm.infofull[is], (t / kInfos) & 1)) alive = false;
+            const float c = infos[is].c[st], ev = infos[is].ev[st];
+            if (alive && !ctx.wait_warp(&sm.sfull[t & 1], (t >> 1) & 1)) alive = false;
+            tc_fence_after();
+            uint64_t y[kGroupRows / 2];
+            {
+                uint32_t a[16];
+                tmem_ld16(lane_base + C::kColS + (t & 1) * RP + row0, a);
+                tmem_ld_wait(a);
+#pragma unroll
+                for (int q = 0; q < kGroupRows / 2; ++q) y[q] = pk2(f32(a[2 * q]), f32(a[2 * q + 1]));
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0 && alive) {
+                mbar_arrive(smem_u32(&sm.sfree[t & 1]));
+                mbar_arrive(smem_u32(&sm.infofree[is]));
+            }
+            uint32_t validm = rowmask;  // bit i: key j visible to row row0 + i
+            if (!((tile0 + kTile <= end) && (tile0 + kTile - 1 <= qoff))) {
+                // row r of the slot sees key j iff r >= (j - qoff) G: the group's rows from `first` on
+                const int first = (j - qoff) * G - row_lo - row0;
+                if (j >= end)
+                    validm = 0;
+                else if (first > 0)
+                    validm &= first >= kGroupRows ? 0u : (0xFFFFFFFFu << first);
+            }
+            // exponents of the shifted weights: s c + ev + (shift - reference)
+            const uint64_t c2 = pk2(c, c), ev2 = pk2(ev, ev);
+            uint64_t e[kGroupRows / 2];
+            bool need = false;
+#pragma unroll
+            for (int q = 0; q < kGroupRows / 2; ++q) e[q] = fma2(y[q], c2, add2(nm[q], ev2));
+            const bool all_rows = validm == 0xFFFFu;
+#pragma unroll
+            for (int q = 0; q < kGroupRows / 2; ++q) {
+                need |= ((validm >> (2 * q)) & 1u) && lo2(e[q]) > kLazyThreshold;
+                need |= ((validm >> (2 * q + 1)) & 1u) && hi2(e[q]) > kLazyThreshold;
+            }
+            bool need_any = true;  // tile 0 sets the reference
+            if (t > 0) need_any = group_vote(g, need);
+            bool ok = true;
+            if (need_any) {
+                // exact tile maximum per row -> new reference; row sums and O rescaled. Lanes 2i and
+                // 2i + 1 derive row i's, the shuffles hand it to every lane. (The next tile's vote stands
+                // between these reads of the maxima and their next writing.)
+                float v[kGroupRows];
+#pragma unroll
+                for (int q = 0; q < kGroupRows / 2; ++q) {
+                    y[q] = fma2(y[q], c2, ev2);
+                    v[2 * q] = ((validm >> (2 * q)) & 1u) ? lo2(y[q]) : -INFINITY;
+                    v[2 * q + 1] = ((validm >> (2 * q + 1)) & 1u) ? hi2(y[q]) : -INFINITY;
+                }
+                const float vm = rows_reduce(v, lane, [](float a, float b2) { return fmaxf(a, b2); });
+                if ((lane & 1) == 0) sm.rmax[g][wq][lane >> 1] = vm;
+                group_bar(g);
+                const int ri = (lane >> 1) & (kGroupRows - 1);
+                const float mo = kShift - sm.nmcur[g][wq][ri];
+                const float tm = fmaxf(fmaxf(sm.rmax[g][0][ri], sm.rmax[g][1][ri]),
+                                       fmaxf(sm.rmax[g][2][ri], sm.rmax[g][3][ri]));
+                const float mn = fmaxf(mo, tm);
+                const float alpha_r = (mn == -INFINITY) ? 1.f : ex2(mo - mn);
+                const float nm_r = (mn == -INFINITY) ? INFINITY : kShift - mn;
+                __syncwarp();
+                if ((lane & 1) == 0) sm.nmcur[g][wq][ri] = nm_r;
+                float alpha[kGroupRows];
+#pragma unroll
+                for (int q = 0; q < kGroupRows / 2; ++q) {
+                    alpha[2 * q] = __shfl_sync(0xffffffffu, alpha_r, 4 * q);
+                    alpha[2 * q + 1] = __shfl_sync(0xffffffffu, alpha_r, 4 * q + 2);
+                    nm[q] = pk2(__shfl_sync(0xffffffffu, nm_r, 4 * q),
+                                __shfl_sync(0xffffffffu, nm_r, 4 * q + 2));
+                    lsum[q] = mul2(lsum[q], pk2(alpha[2 * q], alpha[2 * q + 1]));
+                    e[q] = add2(y[q], nm[q]);
+                }
+                if (t > 0) {
+                    ok = alive && ctx.wait_warp(&sm.pfree, (t - 1) & 1);  // O holds the tiles before
+                    if (ok) {
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int mh = 0; mh < 2; ++mh) {
+                            const uint32_t addr = lane_base + C::kColO + mh * RP + row0;
+                            uint32_t o[16];
+                            tmem_ld16(addr, o);
+                            tmem_ld_wait(o);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(f32(o[i]) * alpha[i]);
+                            tmem_st16(addr, o);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+            }
+            // weights, their sum without V's exponent, and their FP16 rounding
+            const float iev = ev == ev ? ex2(-ev) : 1.f;
+            const uint64_t iev2 = pk2(iev, iev);
+            uint32_t ph[kGroupRows / 2];
+            auto make_p = [&](auto all) {
+                constexpr bool kAll = decltype(all)::value;
+#pragma unroll
+                for (int q = 0; q < kGroupRows / 2; ++q) {
+                    const float p0 = (kAll || ((validm >> (2 * q)) & 1u)) ? ex2(lo2(e[q])) : 0.f;
+                    const float p1 = (kAll || ((validm >> (2 * q + 1)) & 1u)) ? ex2(hi2(e[q])) : 0.f;
+                    lsum[q] = fma2(pk2(p0, p1), iev2, lsum[q]);
+                    const __half2 r = __floats2half2_rn(p0, p1);
+                    ph[q] = *reinterpret_cast<const uint32_t*>(&r);
+                }
+            };
+            if (all_rows)
+                make_p(std::true_type{});
+            else
+                make_p(std::false_type{});
+            if (alive && ok && t > 0) ok = ctx.wait_warp(&sm.pfree, (t - 1) & 1);
+            if (!ok) alive = false;
+            if (!alive) continue;  // every warp still runs the remaining tiles' barriers
+            uint8_t* pbuf = smem + C::kOffP;
+            *reinterpret_cast<uint4*>(pbuf + p_off(2 * g, st)) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+            *reinterpret_cast<uint4*>(pbuf + p_off(2 * g + 1, st)) = make_uint4(ph[4], ph[5], ph[6], ph[7]);
+            fence_async_smem();
+            tc_fence_before();
+            warp_arrive(&sm.pfull);
+        }
+        // split state: the reference minus the shift, shifted sums and numerators
+        {
+            float v[kGroupRows];
+#pragma unroll
+            for (int q = 0; q < kGroupRows / 2; ++q) {
+                v[2 * q] = lo2(lsum[q]);
+                v[2 * q + 1] = hi2(lsum[q]);
+            }
+            const float sum = rows_reduce(v, lane, [](float a, float b2) { return a + b2; });
+            if ((lane & 1) == 0) sm.rsum[g][wq][lane >> 1] = sum;
+            if (lane == 0 && wq == 0) {
+#pragma unroll
+                for (int q = 0; q < kGroupRows / 2; ++q) {
+                    sm.mref[g][2 * q] = -lo2(nm[q]);
+                    sm.mref[g][2 * q + 1] = -hi2(nm[q]);
+                }
+            }
+        }
+        group_bar(g);
+        if (alive && !ctx.aborted() && wq == 0 && lane < kGroupRows && row0 + lane < R) {
+            const float L = sm.rsum[g][0][lane] + sm.rsum[g][1][lane] + sm.rsum[g][2][lane] +
+                            sm.rsum[g][3][lane];
+            // (a row of NaN may have no maximum; it is not an empty one)
+            const float m = L != L ? INFINITY : sm.mref[g][lane];
+            p.ws_state[(int64_t)slot * p.rows + row_lo + row0 + lane] = make_float2(m, L);
+        }
+        const bool ok = ctx.wait_warp(&sm.odone, 0);
+        tc_fence_after();
+        if (__all_sync(0xffffffffu, ok && !ctx.aborted())) {
+            constexpr float kBack = 1.f / (1 << kFactorTop);
+#pragma unroll 1
+            for (int mh = 0; mh < 2; ++mh) {
+                uint32_t o[16];
+                tmem_ld16(lane_base + C::kColO + mh * RP + row0, o);
+                tmem_ld_wait(o);
+                const int d = mh * 128 + st;
+#pragma unroll
+                for (int i = 0; i < kGroupRows; ++i) {
+                    const int r = row0 + i;
+                    if (r < R)
+                        p.ws_acc[((int64_t)slot * p.rows + row_lo + r) * kHeadDim + d] = f32(o[i]) * kBack;
+                }
+            }
         }
     }
-    if (page_clamped) atomicOr(p.status, DFLASH_FLAG_PAGE_CLAMPED);
-#pragma unroll
-    for (int m = 0; m < kRows / 8; ++m) {
-        const int r = warp + 8 * m;
-        // (a row of NaN is not an empty one)
-        const float mx = l_run[m] != l_run[m] ? INFINITY : m_run[m];
-        if (r < R && lane == 0)
-            p.ws_state[(int64_t)slot * p.rows + row_lo + r] = make_float2(mx, l_run[m]);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmemCols);
     }
-#pragma unroll
-    for (int r = 0; r < kRows; ++r)
-        if (r < R) p.ws_acc[((int64_t)slot * p.rows + row_lo + r) * kHeadDim + tid] = acc[r];
 }
 
-cudaError_t launch_partial(const PartialParams& p, cudaStream_t stream) {
-    if (!row_blocks_valid(p, kRows)) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(mx4_partial_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+template <int RP>
+cudaError_t launch_rp(const PartialParams& p, cudaStream_t stream) {
+    constexpr uint32_t smem = smem_bytes<RP>();
+    cudaError_t e = cudaFuncSetAttribute(mx4_partial_kernel<RP>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = partial_grid(p);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.blockDim = dim3(Cfg<RP>::kThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
-    if (p.pdl) {
+    if (p.pdl) {  // a programmatic dependent of the preceding kernel on the stream
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
-    return cudaLaunchKernelEx(&cfg, mx4_partial_kernel, p);
+    return cudaLaunchKernelEx(&cfg, mx4_partial_kernel<RP>, p);
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+int rows_pad(int rows) { return (rows + kGroupRows - 1) / kGroupRows * kGroupRows; }
+
+cudaError_t launch_partial(const PartialParams& p, cudaStream_t stream) {
+    if (!row_blocks_valid(p, kMaxRP)) return cudaErrorInvalidValue;
+    switch (rows_pad(p.block_rows)) {
+        case 16: return launch_rp<16>(p, stream);
+        case 32: return launch_rp<32>(p, stream);
+        default: return launch_rp<48>(p, stream);
+    }
+}
+
+static bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // The plan as the split and combine rules of the E4M3 kernel see it (the same tile and row blocks).
-dflash_verify_attn_plan_t as_split_plan(const dflash_verify_attn_plan_t& plan) {
+static dflash_verify_attn_plan_t as_split_plan(const dflash_verify_attn_plan_t& plan) {
     dflash_verify_attn_plan_t p = plan;
     p.kernel = DFLASH_KERNEL_TCGEN05;
     return p;
 }
 
-}  // namespace
+}  // namespace mx4
 }  // namespace dflash
 
 using namespace dflash;
@@ -219,8 +849,20 @@ int dflash_mx4_attn_plan(const dflash_verify_attn_problem* problem,
     const int rc = dflash_verify_attn_plan(&pr, plan);
     if (rc != DFLASH_OK) return rc;
     plan->kernel = DFLASH_KERNEL_MX4;
-    plan->threads = kThreads;
-    plan->smem_bytes = (int32_t)kSmem;
+    const int block_rows = (plan->rows + plan->row_blocks - 1) / plan->row_blocks;
+    switch (mx4::rows_pad(block_rows)) {
+        case 16:
+            plan->threads = mx4::Cfg<16>::kThreads;
+            plan->smem_bytes = (int32_t)mx4::smem_bytes<16>();
+            break;
+        case 32:
+            plan->threads = mx4::Cfg<32>::kThreads;
+            plan->smem_bytes = (int32_t)mx4::smem_bytes<32>();
+            break;
+        default:
+            plan->threads = mx4::Cfg<48>::kThreads;
+            plan->smem_bytes = (int32_t)mx4::smem_bytes<48>();
+    }
     plan->problem = *problem;
     return DFLASH_OK;
 }
@@ -230,14 +872,14 @@ int dflash_mx4_attn_forward(const dflash_verify_attn_plan_t* plan, const void* q
                             const int32_t* context_lens, void* workspace, size_t workspace_bytes,
                             void* out, float* lse, void* cuda_stream) {
     if (!plan || plan->kernel != DFLASH_KERNEL_MX4) return DFLASH_ERR_INVALID_ARGUMENT;
-    const dflash_verify_attn_plan_t split = as_split_plan(*plan);
+    const dflash_verify_attn_plan_t split = mx4::as_split_plan(*plan);
     const int rc = check_attn_plan(&split);
     if (rc != DFLASH_OK) return rc;
     if (!q || !k_pool || !v_pool || !block_table || !context_lens || !workspace || !out || !lse)
         return DFLASH_ERR_INVALID_ARGUMENT;
-    if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) ||
-        !aligned(workspace, 256) || !aligned(block_table, 4) || !aligned(context_lens, 4) ||
-        !aligned(out, 8) || !aligned(lse, 4))
+    if (!mx4::aligned(q, 16) || !mx4::aligned(k_pool, 16) || !mx4::aligned(v_pool, 16) ||
+        !mx4::aligned(workspace, 256) || !mx4::aligned(block_table, 4) || !mx4::aligned(context_lens, 4) ||
+        !mx4::aligned(out, 8) || !mx4::aligned(lse, 4))
         return DFLASH_ERR_INVALID_ARGUMENT;
     const void* const outs[] = {workspace, out, lse};
     const void* const others[] = {q, k_pool, v_pool, block_table, context_lens};
@@ -253,7 +895,7 @@ int dflash_mx4_attn_forward(const dflash_verify_attn_plan_t* plan, const void* q
     CombineParams c = combine_params(&split, workspace, context_lens, out, lse);
     c.pdl = 1;  // it waits for the partial kernel where it reads the split state
     cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-    if (launch_partial(p, stream) != cudaSuccess || launch_combine(c, stream) != cudaSuccess) {
+    if (mx4::launch_partial(p, stream) != cudaSuccess || launch_combine(c, stream) != cudaSuccess) {
         cudaGetLastError();
         return DFLASH_ERR_CUDA;
     }
