@@ -182,6 +182,7 @@ struct Ctx {
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(bar));
+    __syncwarp();
 }
 // ... and its stores to tensor memory are complete.
 __device__ __forceinline__ void warp_arrive_tmem(uint64_t* bar) {
@@ -437,7 +438,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                 !ctx.wait_warp(&sm.vfull[s], (t / kStages) & 1))
                 break;
             Info& info = infos[is];
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < 4; ++i) {
                 const int key = lane + 32 * i;
                 const uint32_t at = (key / kTokens) * kChunkBytes + kCodeBytes + (key % kTokens) * kBlocks;
@@ -477,14 +478,14 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
             const uint2 sc = *reinterpret_cast<const uint2*>(stage + scales);
             const int top = largest_byte(sc) - kFactorTop;
             bool ok = true;
-#pragma unroll
+#pragma unroll 1
             for (int hd = 0; hd < 2; ++hd) {
                 uint4 w[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     w[j] = *reinterpret_cast<const uint4*>(stage + at + (4 * hd + j) * 256);
                 if (hd) warp_arrive(&sm.kempty[s]);
-                ok = ok && ctx.wait_warp(&sm.kafree[hd], (t & 1) ^ 1);
+                ok = ctx.wait_warp(&sm.kafree[hd], (t & 1) ^ 1);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
@@ -523,7 +524,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                 ok = ctx.wait_warp(&sm.vafree[hv], (t & 1) ^ 1);
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                 for (int it = 0; it < 2; ++it) {  // two chunks: 32 keys, 16 columns of each half
                     uint32_t lo[16], hi[16];
 #pragma unroll
@@ -554,13 +555,11 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                     tmem_st16(lane_base + C::kColV + hv * 64 + it * 16, lo);
                     tmem_st16(lane_base + C::kColV + hv * 64 + 32 + it * 16, hi);
                 }
-                if (hv) {
-                    warp_arrive(&sm.vempty[s]);
-                    warp_arrive(&sm.infofree[is]);
-                }
                 warp_arrive_tmem(&sm.vafull[hv]);
             }
             if (!ok) break;
+            warp_arrive(&sm.vempty[s]);
+            warp_arrive(&sm.infofree[is]);
         }
     } else {
         // ---------------------------------------------------------------- softmax
