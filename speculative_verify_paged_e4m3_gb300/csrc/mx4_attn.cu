@@ -82,8 +82,7 @@ struct Cfg {
 
 // Factors of a tile's keys: of their scores (in log2 units), V's exponent, and of V's blocks (FP16).
 struct Info {
-    float c[kTile];
-    float ev[kTile];
+    float2 c[kTile];  // (score factor, V's exponent)
     uint16_t f[kBlocks][kTile];
 };
 
@@ -126,8 +125,8 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// 2^e as FP16 bits, for e <= 13; 0 below 2^-14.
-__device__ __forceinline__ uint32_t f16_power(int e) { return e < -14 ? 0u : (uint32_t)(e + 15) << 10; }
+// 2^e twice as FP16x2 bits, for e <= 13; 0 below 2^-14 (an exponent field of 0).
+__device__ __forceinline__ uint32_t f16x2_power(int e) { return (uint32_t)max(e + 15, 0) * 0x04000400u; }
 
 // D += A B^T over 16 elements of K, FP16: A in tensor memory (a lane a row, two elements a column).
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
@@ -444,19 +443,18 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                 const uint32_t at = (key / kTokens) * kChunkBytes + kCodeBytes + (key % kTokens) * kBlocks;
                 const uint2 ks = *reinterpret_cast<const uint2*>(smem + C::kOffK + s * kStageBytes + at);
                 const uint2 vs = *reinterpret_cast<const uint2*>(smem + C::kOffV + s * kStageBytes + at);
-                const bool valid = start + t * kTile + key < end;
                 const int ke = largest_byte(ks), ve = largest_byte(vs);
-                info.c[key] = ke == kNanScale ? NAN : __int_as_float(ke << 23) * kScore;
                 const int ev = max(-kMaxEv, min(kMaxEv, ve - 127));
-                info.ev[key] = !valid ? 0.f : (ve == kNanScale ? NAN : (float)ev);
-                // block j's factor is 2^(s - 127 - ev + 12): at most 2^13, and 0 for NaN, for blocks
-                // 2^26 below the key's largest and for keys past the split's end
-                const int base = 127 + ev - kFactorTop;
+                info.c[key] = make_float2(ke == kNanScale ? NAN : __int_as_float(ke << 23) * kScore,
+                                          ve == kNanScale ? NAN : (float)ev);
+                // block j's factor is 2^(s - 127 - ev + 12), at most 2^13 (finite for a NaN block and for
+                // whatever lies past the split's end: those weights are NaN and 0), and 0 for blocks
+                // 2^26 below the key's largest
+                const int base = 127 + ev - kFactorTop - 15;
 #pragma unroll
                 for (int j = 0; j < kBlocks; ++j) {
                     const int sj = (int)(((j < 4 ? vs.x : vs.y) >> (8 * (j & 3))) & 255u);
-                    const uint32_t f = f16_power(min(sj - base, kFactorTop + 1));
-                    info.f[j][key] = (uint16_t)(valid && sj != kNanScale ? f : 0u);
+                    info.f[j][key] = (uint16_t)(min(max(sj - base, 0), kFactorTop + 1 + 15) << 10);
                 }
             }
             __syncwarp();
@@ -491,7 +489,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int sj = (int)(((hd ? sc.y : sc.x) >> (8 * j)) & 255u);
-                    const uint32_t f = f16_power(sj - top) * 0x00010001u;
+                    const uint32_t f = f16x2_power(sj - top);
                     const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
                     uint32_t o[16];
 #pragma unroll
@@ -539,16 +537,17 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                             const uint32_t fa[4] = {a.x, a.y, a.z, a.w}, fb[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                // four keys' bytes: the two keys of a pair into one byte, low halves
-                                // (element e) and high halves (e + 128)
-                                const uint32_t x = u[2 * q + i], x4 = x >> 4;
-                                const uint32_t l = (x & 0x000F000Fu) | (x4 & 0x00F000F0u);
-                                const uint32_t g = (x4 & 0x000F000Fu) | ((x >> 8) & 0x00F000F0u);
+                                // four keys' bytes: the two keys of a pair into bytes 1 and 3, low halves
+                                // (element e) and high halves (e + 128); bytes 0 and 2 are not used
+                                constexpr uint32_t m = 0x0F000F00u;
+                                const uint32_t x = u[2 * q + i], x4 = x << 4;
+                                const uint32_t l = ((x << 8) & m) | (x4 & ~m);
+                                const uint32_t g = (x4 & m) | (x & ~m);
                                 const int o = 8 * c2 + 4 * q + 2 * i;
-                                lo[o] = mul_f16x2(codes_to_f16x2<0>(l), fa[2 * i]);
-                                lo[o + 1] = mul_f16x2(codes_to_f16x2<2>(l), fa[2 * i + 1]);
-                                hi[o] = mul_f16x2(codes_to_f16x2<0>(g), fb[2 * i]);
-                                hi[o + 1] = mul_f16x2(codes_to_f16x2<2>(g), fb[2 * i + 1]);
+                                lo[o] = mul_f16x2(codes_to_f16x2<1>(l), fa[2 * i]);
+                                lo[o + 1] = mul_f16x2(codes_to_f16x2<3>(l), fa[2 * i + 1]);
+                                hi[o] = mul_f16x2(codes_to_f16x2<1>(g), fb[2 * i]);
+                                hi[o + 1] = mul_f16x2(codes_to_f16x2<3>(g), fb[2 * i + 1]);
                             }
                         }
                     }
@@ -614,7 +613,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         for (int t = 0; t < ntiles; ++t) {
             const int tile0 = start + t * kTile, j = tile0 + st, is = t % kInfos;
             if (alive && !ctx.wait_warp(&sm.infofull[is], (t / kInfos) & 1)) alive = false;
-            const float c = infos[is].c[st], ev = infos[is].ev[st];
+            const float2 cev = infos[is].c[st];
+            const float c = cev.x, ev = cev.y;
             if (alive && !ctx.wait_warp(&sm.sfull[t & 1], (t >> 1) & 1)) alive = false;
             tc_fence_after();
             uint64_t y[kGroupRows / 2];
@@ -647,10 +647,17 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
 #pragma unroll
             for (int q = 0; q < kGroupRows / 2; ++q) e[q] = fma2(y[q], c2, add2(nm[q], ev2));
             const bool all_rows = validm == 0xFFFFu;
+            if (all_rows) {
+                float m = lo2(e[0]);
 #pragma unroll
-            for (int q = 0; q < kGroupRows / 2; ++q) {
-                need |= ((validm >> (2 * q)) & 1u) && lo2(e[q]) > kLazyThreshold;
-                need |= ((validm >> (2 * q + 1)) & 1u) && hi2(e[q]) > kLazyThreshold;
+                for (int q = 0; q < kGroupRows / 2; ++q) m = fmaxf(m, fmaxf(lo2(e[q]), hi2(e[q])));
+                need = m > kLazyThreshold;
+            } else {
+#pragma unroll
+                for (int q = 0; q < kGroupRows / 2; ++q) {
+                    need |= ((validm >> (2 * q)) & 1u) && lo2(e[q]) > kLazyThreshold;
+                    need |= ((validm >> (2 * q + 1)) & 1u) && hi2(e[q]) > kLazyThreshold;
+                }
             }
             bool need_any = true;  // tile 0 sets the reference
             if (t > 0) need_any = group_vote(g, need);
