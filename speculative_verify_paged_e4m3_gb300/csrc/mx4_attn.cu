@@ -19,8 +19,9 @@
 //    FP16 has a fixed step, 2^-24, 2^-32 of the largest at least.
 //  * NaN. A key with a NaN scale in K or V gets a NaN factor or exponent: its probability is NaN in
 //    every row that sees it and 0, selected, in the others. V's own factor is then 0.
-//  * Warps: 0 and 2 copy K and V (five tiles ahead), 1 issues the products, 3 works out the factors of a
-//    tile's keys, 4-7 decode K, 8-11 V, the others are the softmax, four for 16 rows.
+//  * Warps: 0 copies the codes (five tiles ahead), 1 and 2 issue the products of the scores and of the
+//    output, 3 works out the factors of a tile's keys, 4-7 decode K, 8-11 V, the others are the softmax, four
+//    for 16 rows.
 //  * Every wait on another warp or on a copy is bounded: on a timeout the CTA sets
 //    DFLASH_FLAG_KERNEL_TIMEOUT, drains its copies and returns.
 #include <cuda_runtime.h>
@@ -55,6 +56,7 @@ constexpr int kStages = 5;       // tiles of codes of K, and of V, on their way
 constexpr int kInfos = 4;        // tiles of factors
 constexpr uint32_t kStageBytes = kChunks * kChunkBytes;
 constexpr uint64_t kWaitLimitNs = 200ull * 1000 * 1000;
+constexpr uint32_t kSuspendNs = 20000;
 constexpr float kShift = 8.f;          // probabilities are 2^8 at the reference
 constexpr float kLazyThreshold = 15.f; // largest exponent of one
 constexpr int kFactorTop = 12;         // a key's largest block is brought to 2^12
@@ -148,15 +150,26 @@ __device__ __forceinline__ void copy_chunk(uint32_t dst, const uint8_t* src, uin
         : "memory");
 }
 
+// One try, for which the hardware may suspend the thread up to the hinted time.
+__device__ __forceinline__ bool try_wait_hint(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kSuspendNs)
+        : "memory");
+    return ok != 0;
+}
+
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (try_wait_hint(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 7) == 0) {
-            if (*abort) return false;
-            if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
-        }
+    while (true) {
+        if (try_wait_hint(bar, parity)) return true;
+        if (*abort) return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
     }
 }
 
@@ -231,60 +244,62 @@ __device__ __forceinline__ int largest_byte(uint2 s) {
     return (int)(max(m2 & 255u, (m2 >> 8) & 255u));
 }
 
-// The warp's copies of one pool: tile after tile into its ring. Lane c < 8 copies chunk c of a tile; the block
-// table is looked up by all lanes for four tiles at a time, ahead.
-struct Copier {
-    const PartialParams& p;
-    const uint8_t* pool;
-    int b, h, start, end, lane;
-    bool clamped;
-    // pool chunk of the chunk that starts at key j (-1 past the end)
-    __device__ int64_t chunk_of(int j) {
+// One warp's copies of both pools, tile after tile into their rings: lane c < 8 copies chunk c of K, lane 8 + c
+// of V. All lanes look up the block table, for four tiles at a time and ahead.
+__device__ __forceinline__ void copy_tiles(const PartialParams& p, const Ctx& ctx, uint8_t* k_ring,
+                                           uint8_t* v_ring, int b, int h, int start, int end,
+                                           int ntiles, int drafted) {
+    const int lane = threadIdx.x & 31;
+    Small& sm = *ctx.sm;
+    const uint64_t policy = l2_evict_first_policy();  // every page is read once
+    bool clamped = false;
+    // pool chunk that this lane's place among four tiles from tile t on has (-1 past the end)
+    auto ahead = [&](int t) -> int64_t {
+        const int j = start + t * kTile + lane * kTokens;
         if (j >= end) return -1;
         const int lp = p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
         const int phys = physical_page(p.block_table, b, p.max_pages_per_seq, lp, p.num_pages,
                                        &clamped);
         return (int64_t)phys * (p.page_size / kTokens) + (j - lp * p.page_size) / kTokens;
-    }
-    // the chunk that this lane's place among four tiles from tile t on has
-    __device__ int64_t ahead(int t) { return chunk_of(start + t * kTile + lane * kTokens); }
-};
-
-__device__ __forceinline__ void copy_tiles(const PartialParams& p, const Ctx& ctx, const uint8_t* pool,
-                                           uint8_t* ring, uint64_t* full, uint64_t* empty, int b,
-                                           int h, int start, int end, int ntiles, int drafted) {
-    const int lane = threadIdx.x & 31;
-    const uint64_t policy = l2_evict_first_policy();  // every page is read once
-    Copier c{p, pool, b, h, start, end, lane, false};
-    int64_t next = c.ahead(0), now = -1;
+    };
+    const bool is_v = lane >= kChunks;
+    const int c = lane & (kChunks - 1);
+    const uint8_t* pool = is_v ? p.v_pool : p.k_pool;
+    const uint32_t ring = smem_u32((is_v ? v_ring : k_ring) + c * kChunkBytes);
+    uint64_t* const full = is_v ? sm.vfull : sm.kfull;
+    int64_t next = ahead(0), now = -1;
     bool dep_done = false;
     int t = 0;
     for (; t < ntiles; ++t) {
         if ((t & 3) == 0) {
             now = next;
-            next = c.ahead(t + 4);
+            next = ahead(t + 4);
         }
         const int s = t % kStages;
-        if (!ctx.wait_warp(&empty[s], ((t / kStages) & 1) ^ 1)) break;
+        const uint32_t parity = ((t / kStages) & 1) ^ 1;
+        if (!ctx.wait_warp(&sm.kempty[s], parity) || !ctx.wait_warp(&sm.vempty[s], parity)) break;
         // keys from `drafted` on may be written by the kernel just before this one
         if (!dep_done && start + (t + 1) * kTile > drafted) {
             griddep_wait();
             dep_done = true;
         }
-        const int64_t chunk = __shfl_sync(0xffffffffu, now, (t & 3) * kChunks + (lane & 7));
+        const int64_t chunk = __shfl_sync(0xffffffffu, now, (t & 3) * kChunks + c);
         const int n = min(kChunks, (end - start - t * kTile + kTokens - 1) / kTokens);
-        if (lane == 0) mbar_arrive_expect_tx(smem_u32(&full[s]), n * kChunkBytes);
+        if (lane < 2)
+            mbar_arrive_expect_tx(smem_u32(lane ? &sm.vfull[s] : &sm.kfull[s]), n * kChunkBytes);
         __syncwarp();
-        if (lane < n)
-            copy_chunk(smem_u32(ring + s * kStageBytes + lane * kChunkBytes),
-                       pool + (chunk * p.num_kv_heads + h) * kChunkBytes, smem_u32(&full[s]), policy);
+        if (lane < 2 * kChunks && c < n)
+            copy_chunk(ring + s * kStageBytes, pool + (chunk * p.num_kv_heads + h) * kChunkBytes,
+                       smem_u32(&full[s]), policy);
     }
-    if (c.clamped) atomicOr(p.status, DFLASH_FLAG_PAGE_CLAMPED);
+    if (clamped) atomicOr(p.status, DFLASH_FLAG_PAGE_CLAMPED);
     // no copy may still be writing shared memory when the CTA retires
     __syncwarp();
     if (lane == 0)
-        for (int u = t - kStages < 0 ? 0 : t - kStages; u < t; ++u)
-            mbar_wait(smem_u32(&full[u % kStages]), (u / kStages) & 1, &ctx.sm->abort, kWaitLimitNs);
+        for (int u = t - kStages < 0 ? 0 : t - kStages; u < t; ++u) {
+            mbar_wait(smem_u32(&sm.kfull[u % kStages]), (u / kStages) & 1, &sm.abort, kWaitLimitNs);
+            mbar_wait(smem_u32(&sm.vfull[u % kStages]), (u / kStages) & 1, &sm.abort, kWaitLimitNs);
+        }
 }
 
 template <int RP>
@@ -337,7 +352,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         }
         mbar_init(smem_u32(&sm.pfull), C::kSoftWarps);
         mbar_init(smem_u32(&sm.pfree), 1);
-        mbar_init(smem_u32(&sm.odone), 1);
+        mbar_init(smem_u32(&sm.odone), 2);  // both threads that issue products
         mbar_init(smem_u32(&sm.qready), C::kSoftWarps);
         sm.abort = 0;
         fence_mbar_init();
@@ -353,80 +368,62 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
 
     if (warp == 0) {
-        copy_tiles(p, ctx, p.k_pool, smem + C::kOffK, sm.kfull, sm.kempty, b, h, start, end, ntiles,
-                   n - p.q_len);
-    } else if (warp == 2) {
-        copy_tiles(p, ctx, p.v_pool, smem + C::kOffV, sm.vfull, sm.vempty, b, h, start, end, ntiles,
-                   n - p.q_len);
-    } else if (warp == 1) {
+        copy_tiles(p, ctx, smem + C::kOffK, smem + C::kOffV, b, h, start, end, ntiles, n - p.q_len);
+    } else if (warp == 1 || warp == 2) {
         // ---------------------------------------------------------------- products
-        // One thread, one loop over two streams of half tiles: S of the head dim's halves, O of the
-        // keys' halves. Neither waits for the other; O goes first where both are ready.
-        if (lane == 0 && ctx.wait(&sm.qready, 0)) {
-            const uint32_t idesc_s = idesc_f32acc(128, RP, 0, 0, 0, 0);
-            const uint32_t idesc_o = idesc_f32acc(128, RP, 0, 0, 0, 1);
-            const uint32_t q_base = smem_u32(smem), p_base = smem_u32(smem + C::kOffP);
-            const int halves = 2 * ntiles;
-            int us_ = 0, uo = 0;
-            uint64_t last = globaltimer_ns();
-            uint32_t idle = 0;
-            while (us_ < halves || uo < halves) {
-                bool progressed = false;
-                if (uo < halves) {
-                    const int t = uo >> 1, hv = uo & 1;
-                    if (mbar_test_wait(smem_u32(&sm.vafull[hv]), t & 1) &
-                        mbar_test_wait(smem_u32(&sm.pfull), t & 1)) {
-                        tc_fence_after();
+        // One thread issues the scores, another the output: a product takes its thread some 50 clocks, the
+        // tensor core half of that (N 48: 24 with two threads, 46 with one), a commit or a wait 50 to 80. Each
+        // product's addresses are a base and a constant: worked out from the indices they took 145
+        // clocks a product. Both operands come in halves (of the head dim, of the keys), so that
+        // one is decoded while the other is read.
+        bool ok = lane == 0 && ctx.wait(&sm.qready, 0);
+        if (warp == 1 && lane == 0) {
+            constexpr uint32_t idesc = idesc_f32acc(128, RP, 0, 0, 0, 0);
+            // (a descriptor's address is in units of 16 bytes, in its lowest bits)
+            const uint64_t q_desc = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+#pragma unroll 1
+            for (int t = 0; ok && t < ntiles; ++t) {
+                const uint32_t d = tmem + C::kColS + (t & 1) * RP;
+                ok = ctx.wait(&sm.sfree[t & 1], ((t >> 1) & 1) ^ 1);
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            const uint64_t bd = smem_desc(p_base + (4 * hv + kk) * 256, 128, 2048,
-                                                          kSwizzleNone);
+                for (int hd = 0; hd < 2; ++hd) {
+                    ok = ok && ctx.wait(&sm.kafull[hd], t & 1);
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
-                            for (int mh = 0; mh < 2; ++mh)
-                                mma_ts(tmem + C::kColO + mh * RP,
-                                       tmem + C::kColV + hv * 64 + mh * 32 + kk * 8, bd, idesc_o,
-                                       (uo | kk) != 0);
-                        }
-                        mma_commit(smem_u32(&sm.vafree[hv]));
-                        if (hv) mma_commit(smem_u32(&sm.pfree));
-                        ++uo;
-                        progressed = true;
-                    }
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_ts(d, tmem + C::kColK + hd * 64 + kk * 8,
+                               q_desc + ((2 * hd + (kk >> 2)) * (RP * 128) + (kk & 3) * 32) / 16, idesc,
+                               hd || kk);
+                    mma_commit(smem_u32(&sm.kafree[hd]));
                 }
-                if (us_ < halves) {
-                    const int t = us_ >> 1, hd = us_ & 1;
-                    if (mbar_test_wait(smem_u32(&sm.kafull[hd]), t & 1) &
-                        (hd ? true : mbar_test_wait(smem_u32(&sm.sfree[t & 1]), ((t >> 1) & 1) ^ 1))) {
-                        tc_fence_after();
+                if (ok) mma_commit(smem_u32(&sm.sfull[t & 1]));
+            }
+        } else if (lane == 0) {
+            constexpr uint32_t idesc = idesc_f32acc(128, RP, 0, 0, 0, 1);
+            const uint64_t p_desc = smem_desc(smem_u32(smem + C::kOffP), 128, 2048, kSwizzleNone);
+#pragma unroll 1
+            for (int t = 0; ok && t < ntiles; ++t) {
+                ok = ctx.wait(&sm.pfull, t & 1);
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk) {
-                            const int ks = 8 * hd + kk;
-                            const uint64_t bd = smem_desc(
-                                q_base + (ks >> 2) * (RP * 128) + (ks & 3) * 32, 16, 1024,
-                                kSwizzle128B);
-                            mma_ts(tmem + C::kColS + (t & 1) * RP,
-                                   tmem + C::kColK + hd * 64 + kk * 8, bd, idesc_s, ks != 0);
-                        }
-                        mma_commit(smem_u32(&sm.kafree[hd]));
-                        if (hd) mma_commit(smem_u32(&sm.sfull[t & 1]));
-                        ++us_;
-                        progressed = true;
+                for (int hv = 0; hv < 2; ++hv) {
+                    ok = ok && ctx.wait(&sm.vafull[hv], t & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+                        for (int mh = 0; mh < 2; ++mh)
+                            mma_ts(tmem + C::kColO + mh * RP,
+                                   tmem + C::kColV + hv * 64 + mh * 32 + kk * 8,
+                                   p_desc + (4 * hv + kk) * 256 / 16, idesc, hv || kk || t != 0);
                     }
+                    mma_commit(smem_u32(&sm.vafree[hv]));
                 }
-                if (progressed) {
-                    idle = 0;
-                    last = globaltimer_ns();
-                } else if ((++idle & 15) == 0) {
-                    if (ctx.aborted()) break;
-                    if (globaltimer_ns() - last > kWaitLimitNs) {
-                        *reinterpret_cast<volatile int*>(&sm.abort) = 1;
-                        atomicOr(p.status, DFLASH_FLAG_KERNEL_TIMEOUT);
-                        break;
-                    }
-                }
+                if (ok) mma_commit(smem_u32(&sm.pfree));
             }
         }
-        if (lane == 0) mma_commit(smem_u32(&sm.odone));  // tracks every product issued above
+        if (lane == 0) mma_commit(smem_u32(&sm.odone));  // tracks every product this thread issued
     } else if (warp == 3) {
         // ---------------------------------------------------------------- factors of a tile's keys
         constexpr float kScore = 0.0625f * kLog2e / (1 << kFactorTop);  // D^-1/2 = 1/16
