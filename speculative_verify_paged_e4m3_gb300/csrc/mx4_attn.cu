@@ -140,6 +140,15 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         : "memory");
 }
 
+// One lane of a whole warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // kChunkBytes from global to shared memory (both 16-byte aligned).
 __device__ __forceinline__ void copy_chunk(uint32_t dst, const uint8_t* src, uint32_t bar,
                                            uint64_t policy) {
@@ -163,31 +172,43 @@ __device__ __forceinline__ bool try_wait_hint(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
-    if (try_wait_hint(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (true) {
-        if (try_wait_hint(bar, parity)) return true;
-        if (*abort) return false;
-        if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
-    }
-}
-
 struct Ctx {
     Small* sm;
     int32_t* status;
-    __device__ bool wait(uint64_t* bar, uint32_t parity) const {
-        if (bar_wait(smem_u32(bar), parity, &sm->abort)) return true;
+    __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
+        const uint32_t addr = smem_u32(bar);
+        if (try_wait_hint(addr, parity)) return true;
+        // (reading the clock between the tries keeps them apart: without, the waiting warps took the
+        // others' time, 131 us for 109)
+        const uint64_t t0 = globaltimer_ns();
+        while (true) {
+            if (try_wait_hint(addr, parity)) return true;
+            if (aborted()) return false;
+            if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+        }
         *reinterpret_cast<volatile int*>(&sm->abort) = 1;
         atomicOr(status, DFLASH_FLAG_KERNEL_TIMEOUT);
         return false;
     }
     // by a whole warp, whose lanes agree on the result
-    __device__ bool wait_warp(uint64_t* bar, uint32_t parity) const {
+    __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) const {
         const bool ok = wait(bar, parity);
         return __all_sync(0xffffffffu, ok);
     }
     __device__ bool aborted() const { return *reinterpret_cast<volatile int*>(&sm->abort) != 0; }
+};
+
+// Place of a tile in a ring of kN, and the parity of its phase there.
+template <int kN>
+struct Ring {
+    int i = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next() {
+        if (++i == kN) {
+            i = 0;
+            parity ^= 1;
+        }
+    }
 };
 
 // This warp has done with what `bar` counts.
@@ -270,13 +291,15 @@ __device__ __forceinline__ void copy_tiles(const PartialParams& p, const Ctx& ct
     int64_t next = ahead(0), now = -1;
     bool dep_done = false;
     int t = 0;
-    for (; t < ntiles; ++t) {
+    Ring<kStages> ring_at;
+#pragma unroll 1
+    for (; t < ntiles; ++t, ring_at.next()) {
         if ((t & 3) == 0) {
             now = next;
             next = ahead(t + 4);
         }
-        const int s = t % kStages;
-        const uint32_t parity = ((t / kStages) & 1) ^ 1;
+        const int s = ring_at.i;
+        const uint32_t parity = ring_at.parity ^ 1;
         if (!ctx.wait_warp(&sm.kempty[s], parity) || !ctx.wait_warp(&sm.vempty[s], parity)) break;
         // keys from `drafted` on may be written by the kernel just before this one
         if (!dep_done && start + (t + 1) * kTile > drafted) {
@@ -296,6 +319,7 @@ __device__ __forceinline__ void copy_tiles(const PartialParams& p, const Ctx& ct
     // no copy may still be writing shared memory when the CTA retires
     __syncwarp();
     if (lane == 0)
+#pragma unroll 1
         for (int u = t - kStages < 0 ? 0 : t - kStages; u < t; ++u) {
             mbar_wait(smem_u32(&sm.kfull[u % kStages]), (u / kStages) & 1, &sm.abort, kWaitLimitNs);
             mbar_wait(smem_u32(&sm.vfull[u % kStages]), (u / kStages) & 1, &sm.abort, kWaitLimitNs);
@@ -309,7 +333,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     Info* const infos = reinterpret_cast<Info*>(smem + C::kOffInfo);
     Small& sm = *reinterpret_cast<Small*>(smem + C::kOffInfo + kInfos * sizeof(Info));
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (the shuffle tells the compiler that a warp's roles, loops and addresses are the same in all its lanes)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const RowBlock rblk = row_block(p);
     const int R = rblk.rows, row_lo = rblk.row_lo, G = p.group, slot = rblk.slot;
     griddep_launch_dependents();
@@ -376,32 +401,41 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         // product's addresses are a base and a constant: worked out from the indices they took 145
         // clocks a product. Both operands come in halves (of the head dim, of the keys), so that
         // one is decoded while the other is read.
-        bool ok = lane == 0 && ctx.wait(&sm.qready, 0);
-        if (warp == 1 && lane == 0) {
+        const bool issuer = elect_one();
+        bool ok = issuer && ctx.wait(&sm.qready, 0);
+        using Even = std::integral_constant<int, 0>;
+        using Odd = std::integral_constant<int, 1>;
+        if (warp == 1 && issuer) {
             constexpr uint32_t idesc = idesc_f32acc(128, RP, 0, 0, 0, 0);
-            // (a descriptor's address is in units of 16 bytes, in its lowest bits)
-            const uint64_t q_desc = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
-#pragma unroll 1
-            for (int t = 0; ok && t < ntiles; ++t) {
-                const uint32_t d = tmem + C::kColS + (t & 1) * RP;
-                ok = ctx.wait(&sm.sfree[t & 1], ((t >> 1) & 1) ^ 1);
+            const uint32_t qb = smem_u32(smem);
+            auto tile = [&](auto parity, int t) {
+                constexpr int kS = decltype(parity)::value;
+                ok = ctx.wait(&sm.sfree[kS], ((t >> 1) & 1) ^ 1);
 #pragma unroll
                 for (int hd = 0; hd < 2; ++hd) {
-                    ok = ok && ctx.wait(&sm.kafull[hd], t & 1);
-                    if (!ok) break;
+                    ok = ok && ctx.wait(&sm.kafull[hd], kS);
+                    if (!ok) return;
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        mma_ts(d, tmem + C::kColK + hd * 64 + kk * 8,
-                               q_desc + ((2 * hd + (kk >> 2)) * (RP * 128) + (kk & 3) * 32) / 16, idesc,
-                               hd || kk);
+                        mma_ts(C::kColS + kS * RP, C::kColK + hd * 64 + kk * 8,
+                               smem_desc(qb + (2 * hd + (kk >> 2)) * (RP * 128) + (kk & 3) * 32, 16, 1024,
+                                         kSwizzle128B),
+                               idesc, hd || kk);
                     mma_commit(smem_u32(&sm.kafree[hd]));
                 }
-                if (ok) mma_commit(smem_u32(&sm.sfull[t & 1]));
+                mma_commit(smem_u32(&sm.sfull[kS]));
+            };
+#pragma unroll 1
+            for (int t = 0; ok && t < ntiles; ++t) {
+                if (t & 1)
+                    tile(Odd{}, t);
+                else
+                    tile(Even{}, t);
             }
-        } else if (lane == 0) {
+        } else if (issuer) {
             constexpr uint32_t idesc = idesc_f32acc(128, RP, 0, 0, 0, 1);
-            const uint64_t p_desc = smem_desc(smem_u32(smem + C::kOffP), 128, 2048, kSwizzleNone);
+            const uint32_t pb = smem_u32(smem + C::kOffP);
 #pragma unroll 1
             for (int t = 0; ok && t < ntiles; ++t) {
                 ok = ctx.wait(&sm.pfull, t & 1);
@@ -414,24 +448,26 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                     for (int kk = 0; kk < 4; ++kk) {
 #pragma unroll
                         for (int mh = 0; mh < 2; ++mh)
-                            mma_ts(tmem + C::kColO + mh * RP,
-                                   tmem + C::kColV + hv * 64 + mh * 32 + kk * 8,
-                                   p_desc + (4 * hv + kk) * 256 / 16, idesc, hv || kk || t != 0);
+                            mma_ts(C::kColO + mh * RP, C::kColV + hv * 64 + mh * 32 + kk * 8,
+                                   smem_desc(pb + (4 * hv + kk) * 256, 128, 2048, kSwizzleNone), idesc,
+                                   hv || kk || t != 0);
                     }
                     mma_commit(smem_u32(&sm.vafree[hv]));
                 }
                 if (ok) mma_commit(smem_u32(&sm.pfree));
             }
         }
-        if (lane == 0) mma_commit(smem_u32(&sm.odone));  // tracks every product this thread issued
+        if (issuer) mma_commit(smem_u32(&sm.odone));  // tracks every product this thread issued
     } else if (warp == 3) {
         // ---------------------------------------------------------------- factors of a tile's keys
         constexpr float kScore = 0.0625f * kLog2e / (1 << kFactorTop);  // D^-1/2 = 1/16
-        for (int t = 0; t < ntiles; ++t) {
-            const int s = t % kStages, is = t % kInfos;
-            if (!ctx.wait_warp(&sm.infofree[is], ((t / kInfos) & 1) ^ 1) ||
-                !ctx.wait_warp(&sm.kfull[s], (t / kStages) & 1) ||
-                !ctx.wait_warp(&sm.vfull[s], (t / kStages) & 1))
+        Ring<kStages> ring;
+        Ring<kInfos> iring;
+#pragma unroll 1
+        for (int t = 0; t < ntiles; ++t, ring.next(), iring.next()) {
+            const int s = ring.i, is = iring.i;
+            if (!ctx.wait_warp(&sm.infofree[is], iring.parity ^ 1) ||
+                !ctx.wait_warp(&sm.kfull[s], ring.parity) || !ctx.wait_warp(&sm.vfull[s], ring.parity))
                 break;
             Info& info = infos[is];
 #pragma unroll 1
@@ -466,28 +502,29 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         const int key = (warp - kKWarp) * 32 + lane;
         const uint32_t at = (key / kTokens) * kChunkBytes + (key % kTokens) * 16;
         const uint32_t scales = (key / kTokens) * kChunkBytes + kCodeBytes + (key % kTokens) * kBlocks;
-        for (int t = 0; t < ntiles; ++t) {
-            const int s = t % kStages;
-            if (!ctx.wait_warp(&sm.kfull[s], (t / kStages) & 1)) break;
+        Ring<kStages> ring;
+#pragma unroll 1
+        for (int t = 0; t < ntiles; ++t, ring.next()) {
+            const int s = ring.i;
+            if (!ctx.wait_warp(&sm.kfull[s], ring.parity)) break;
             const uint8_t* stage = smem + C::kOffK + s * kStageBytes;
             const uint2 sc = *reinterpret_cast<const uint2*>(stage + scales);
             const int top = largest_byte(sc) - kFactorTop;
             bool ok = true;
 #pragma unroll 1
             for (int hd = 0; hd < 2; ++hd) {
-                uint4 w[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[j] = *reinterpret_cast<const uint4*>(stage + at + (4 * hd + j) * 256);
-                if (hd) warp_arrive(&sm.kempty[s]);
+                const uint8_t* codes = stage + at + 4 * hd * 256;
+                uint4 next = *reinterpret_cast<const uint4*>(codes);
+                uint32_t scale = hd ? sc.y : sc.x;
                 ok = ctx.wait_warp(&sm.kafree[hd], (t & 1) ^ 1);
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                 for (int j = 0; j < 4; ++j) {
-                    const int sj = (int)(((hd ? sc.y : sc.x) >> (8 * j)) & 255u);
-                    const uint32_t f = f16x2_power(sj - top);
-                    const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+                    const uint32_t f = f16x2_power((int)(scale & 255u) - top);
+                    const uint32_t u[4] = {next.x, next.y, next.z, next.w};
+                    scale >>= 8;
+                    next = *reinterpret_cast<const uint4*>(codes + ((j + 1) & 3) * 256);
                     uint32_t o[16];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -501,14 +538,18 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                 warp_arrive_tmem(&sm.kafull[hd]);
             }
             if (!ok) break;
+            warp_arrive(&sm.kempty[s]);
         }
     } else if (warp < kSoftWarp) {
         // ---------------------------------------------------------------- V: lane = element (and + 128)
         const int quad = warp & 3, e = quad * 32 + lane;
-        for (int t = 0; t < ntiles; ++t) {
-            const int s = t % kStages, is = t % kInfos;
-            if (!ctx.wait_warp(&sm.vfull[s], (t / kStages) & 1) ||
-                !ctx.wait_warp(&sm.infofull[is], (t / kInfos) & 1))
+        Ring<kStages> ring;
+        Ring<kInfos> iring;
+#pragma unroll 1
+        for (int t = 0; t < ntiles; ++t, ring.next(), iring.next()) {
+            const int s = ring.i, is = iring.i;
+            if (!ctx.wait_warp(&sm.vfull[s], ring.parity) ||
+                !ctx.wait_warp(&sm.infofull[is], iring.parity))
                 break;
             const uint8_t* stage = smem + C::kOffV + s * kStageBytes + e * kTokens;
             const uint16_t* f0 = infos[is].f[quad];
@@ -607,6 +648,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         if (lane < kGroupRows) sm.nmcur[g][wq][lane] = INFINITY;
         __syncwarp();
         bool alive = true;
+#pragma unroll 1
         for (int t = 0; t < ntiles; ++t) {
             const int tile0 = start + t * kTile, j = tile0 + st, is = t % kInfos;
             if (alive && !ctx.wait_warp(&sm.infofull[is], (t / kInfos) & 1)) alive = false;
