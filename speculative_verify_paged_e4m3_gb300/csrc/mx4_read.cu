@@ -1,8 +1,10 @@
 // mx4_read.cu -- tokens of the 4-bit cache as numbers (dflash_mx4_read; dflash_mx4_cache.h has the
 // format).
 //
-// A CTA takes 16 tokens, a warp a row (token, head) of one pool at a time. Tokens that follow one another in
-// the cache share V's 16-byte pieces (a byte of each), which the L1 then holds for the CTA.
+// A CTA takes 16 tokens of one head, half of its warps K, half V. K's rows go a warp each, 8 elements a lane. V's
+// chunk has a token's bytes 16 apart, so that a thread takes four of them (elements 4j .. 4j + 3 and 128
+// more) for four tokens: a word each, if the four lie one after the other in a chunk, as tokens of a context
+// do, or two words shifted; else bytes.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -18,6 +20,7 @@ namespace {
 constexpr int kReadThreads = 256;
 constexpr int kReadWarps = kReadThreads / 32;
 constexpr int kReadTokens = 16;
+constexpr int kReadCtas = 6;  // an SM: registers cut to fit
 constexpr int64_t kMaxTokens = 0x7FFFFFFF;
 
 struct E5m2 {
@@ -33,93 +36,146 @@ struct ReadParams {
     int num_kv_heads;
 };
 
-// Four numbers, stored.
-template <typename T>
-__device__ __forceinline__ void store4(T* dst, const float (&x)[4]) {
+// Numbers, stored in one piece.
+template <typename T, int kN>
+__device__ __forceinline__ void store(T* dst, const float (&x)[kN]) {
+    static_assert(kN == 4 || kN == 8, "four or eight");
     if constexpr (std::is_same_v<T, E5m2>) {
-        uint32_t r;
-        asm("{\n\t.reg .b16 lo, hi;\n\t"
-            "cvt.rn.satfinite.e5m2x2.f32 lo, %2, %1;\n\t"
-            "cvt.rn.satfinite.e5m2x2.f32 hi, %4, %3;\n\t"
-            "mov.b32 %0, {lo, hi};\n\t}"
-            : "=r"(r)
-            : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]));
-        *reinterpret_cast<uint32_t*>(dst) = r;
+        uint32_t w[kN / 4];
+#pragma unroll
+        for (int i = 0; i < kN / 4; ++i)
+            asm("{\n\t.reg .b16 lo, hi;\n\t"
+                "cvt.rn.satfinite.e5m2x2.f32 lo, %2, %1;\n\t"
+                "cvt.rn.satfinite.e5m2x2.f32 hi, %4, %3;\n\t"
+                "mov.b32 %0, {lo, hi};\n\t}"
+                : "=r"(w[i])
+                : "f"(x[4 * i]), "f"(x[4 * i + 1]), "f"(x[4 * i + 2]), "f"(x[4 * i + 3]));
+        if constexpr (kN == 4)
+            *reinterpret_cast<uint32_t*>(dst) = w[0];
+        else
+            *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
     } else {
-        uint2 w;
-        if constexpr (std::is_same_v<T, __half>) {
-            const __half2 a = __floats2half2_rn(x[0], x[1]), b = __floats2half2_rn(x[2], x[3]);
-            w.x = *reinterpret_cast<const uint32_t*>(&a);
-            w.y = *reinterpret_cast<const uint32_t*>(&b);
-        } else {
-            const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]),
-                                 b = __floats2bfloat162_rn(x[2], x[3]);
-            w.x = *reinterpret_cast<const uint32_t*>(&a);
-            w.y = *reinterpret_cast<const uint32_t*>(&b);
+        uint32_t w[kN / 2];
+#pragma unroll
+        for (int i = 0; i < kN / 2; ++i) {
+            if constexpr (std::is_same_v<T, __half>) {
+                const __half2 r = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&r);
+            } else {
+                const __nv_bfloat162 r = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&r);
+            }
         }
-        *reinterpret_cast<uint2*>(dst) = w;
+        if constexpr (kN == 4)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+        else
+            *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
 // The four bytes of codes w as numbers, low halves to lo and high halves to hi.
-__device__ __forceinline__ void numbers(uint32_t w, float lo_power, float hi_power, float (&lo)[4],
-                                        float (&hi)[4]) {
+__device__ __forceinline__ void numbers(uint32_t w, float (&lo)[4], float (&hi)[4]) {
     const uint32_t h[4] = {mx4::codes_to_f16x2<0>(w), mx4::codes_to_f16x2<1>(w),
                            mx4::codes_to_f16x2<2>(w), mx4::codes_to_f16x2<3>(w)};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-        lo[i] = f.x * lo_power;
-        hi[i] = f.y * hi_power;
+        lo[i] = f.x;
+        hi[i] = f.y;
     }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kReadThreads) mx4_read_kernel(const ReadParams p) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kReadThreads, kReadCtas) mx4_read_kernel(const ReadParams p) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y;
     const int64_t t0 = (int64_t)blockIdx.x * kReadTokens;
-    const int rows = kReadTokens * p.num_kv_heads;
-    // (row r: token r % 16, so that the CTA's warps are in one head's chunk at a time)
-    for (int r = warp; r < rows; r += kReadWarps) {
-        const int64_t t = t0 + r % kReadTokens;
-        const int h = r / kReadTokens;
-        if (t >= p.num_tokens) continue;
-        const int64_t slot = p.slots[t];
-        if (slot < 0 || slot >= p.num_slots) {
-            if (slot >= 0 && h == 0 && lane == 0) atomicOr(p.status, DFLASH_FLAG_SLOT_RANGE);
-            continue;
+    __shared__ int64_t slots[kReadTokens];
+    if (tid < kReadTokens) {
+        int64_t s = t0 + tid < p.num_tokens ? p.slots[t0 + tid] : -1;
+        if (s >= p.num_slots) {
+            if (h == 0) atomicOr(p.status, DFLASH_FLAG_SLOT_RANGE);
+            s = -1;
         }
-        const int tok = (int)(slot % mx4::kTokens);
-        const int64_t at = mx4::chunk_offset(slot, p.num_kv_heads, h);
-        if (p.k_pool) {
-            const uint8_t* chunk = p.k_pool + at;
-            const int block = lane >> 2;
+        slots[tid] = s;
+    }
+    __syncthreads();
+    constexpr int kHalf = kReadWarps / 2;
+    if (warp < kHalf) {
+        if (!p.k_pool) return;
+#pragma unroll
+        for (int i = 0; i < kReadTokens / kHalf; ++i) {
+            const int r = warp + kHalf * i;
+            const int64_t slot = slots[r];
+            if (slot < 0) continue;
+            const int tok = (int)(slot % mx4::kTokens), block = lane >> 2;
+            const uint8_t* chunk = p.k_pool + mx4::chunk_offset(slot, p.num_kv_heads, h);
             const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(
                 chunk + block * 256 + tok * 16 + (lane & 3) * 4));
             const float power = mx4::power_of_scale(
                 __ldg(chunk + mx4::kCodeBytes + tok * mx4::kBlocks + block));
             float lo[4], hi[4];
-            numbers(w, power, power, lo, hi);
-            const float a[4] = {lo[0], hi[0], lo[1], hi[1]}, b[4] = {lo[2], hi[2], lo[3], hi[3]};
-            T* dst = static_cast<T*>(p.k_out) + t * p.k_stride + h * kHeadDim + 8 * lane;
-            store4(dst, a);
-            store4(dst + 4, b);
-        }
-        if (p.v_pool) {
-            const uint8_t* chunk = p.v_pool + at;
-            uint32_t w = 0;
+            numbers(w, lo, hi);
+            float x[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w |= (uint32_t)__ldg(chunk + (4 * lane + i) * mx4::kTokens + tok) << (8 * i);
-            const uint8_t* scales = chunk + mx4::kCodeBytes + tok * mx4::kBlocks + (lane >> 3);
-            float lo[4], hi[4];
-            numbers(w, mx4::power_of_scale(__ldg(scales)), mx4::power_of_scale(__ldg(scales + 4)), lo,
-                    hi);
-            T* dst = static_cast<T*>(p.v_out) + t * p.v_stride + h * kHeadDim + 4 * lane;
-            store4(dst, lo);
-            store4(dst + kHeadDim / 2, hi);
+            for (int k = 0; k < 4; ++k) {
+                x[2 * k] = lo[k] * power;
+                x[2 * k + 1] = hi[k] * power;
+            }
+            store(static_cast<T*>(p.k_out) + (t0 + r) * p.k_stride + h * kHeadDim + 8 * lane, x);
+        }
+        return;
+    }
+    if (!p.v_pool) return;
+    constexpr int kEach = 4;  // tokens, and elements of each half of the head, a thread
+    static_assert(kHalf * kEach == kReadTokens && kEach * 32 == kHeadDim / 2, "threads of a CTA");
+    const int e = kEach * lane, first = kEach * (warp - kHalf);
+    const int64_t* s = slots + first;
+    const bool run = s[0] >= 0 && s[1] == s[0] + 1 && s[2] == s[0] + 2 && s[3] == s[0] + 3 &&
+                     s[0] % mx4::kTokens <= mx4::kTokens - kEach;
+    uint32_t w[kEach] = {};  // the four tokens' bytes of element e + k
+    if (run) {
+        const int tok = (int)(s[0] % mx4::kTokens);
+        const uint8_t* at =
+            p.v_pool + mx4::chunk_offset(s[0], p.num_kv_heads, h) + e * mx4::kTokens + (tok & ~3);
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(at + k * mx4::kTokens);
+            w[k] = __ldg(q);
+            if (tok & 3) w[k] = __funnelshift_r(w[k], __ldg(q + 1), 8 * (tok & 3));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            if (s[i] < 0) continue;
+            const uint8_t* at = p.v_pool + mx4::chunk_offset(s[i], p.num_kv_heads, h) + e * mx4::kTokens +
+                                s[i] % mx4::kTokens;
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) w[k] |= (uint32_t)__ldg(at + k * mx4::kTokens) << (8 * i);
         }
     }
+    // token first + i, byte i of the words
+    auto put = [&](auto byte) {
+        constexpr int i = decltype(byte)::value;
+        if (s[i] < 0) return;
+        const uint8_t* scales = p.v_pool + mx4::chunk_offset(s[i], p.num_kv_heads, h) + mx4::kCodeBytes +
+                                s[i] % mx4::kTokens * mx4::kBlocks + e / mx4::kBlock;
+        const float pl = mx4::power_of_scale(__ldg(scales)), ph = mx4::power_of_scale(__ldg(scales + 4));
+        T* dst = static_cast<T*>(p.v_out) + (t0 + first + i) * p.v_stride + h * kHeadDim + e;
+        float a[kEach], b[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const uint32_t x = mx4::codes_to_f16x2<i>(w[k]);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
+            a[k] = f.x * pl;
+            b[k] = f.y * ph;
+        }
+        store(dst, a);
+        store(dst + kHeadDim / 2, b);
+    };
+    put(std::integral_constant<int, 0>{});
+    put(std::integral_constant<int, 1>{});
+    put(std::integral_constant<int, 2>{});
+    put(std::integral_constant<int, 3>{});
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -170,7 +226,7 @@ extern "C" int dflash_mx4_read(int32_t num_kv_heads, int32_t head_dim, int32_t p
     p.num_slots = (int64_t)num_pages * page_size;
     p.status = status;
     p.num_kv_heads = num_kv_heads;
-    const unsigned ctas = (unsigned)((num_tokens + kReadTokens - 1) / kReadTokens);
+    const dim3 ctas((unsigned)((num_tokens + kReadTokens - 1) / kReadTokens), num_kv_heads);
     cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
     if (dtype == DFLASH_FP16)
         mx4_read_kernel<__half><<<ctas, kReadThreads, 0, stream>>>(p);

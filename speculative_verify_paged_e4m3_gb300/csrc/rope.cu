@@ -30,9 +30,17 @@
 namespace dflash {
 namespace {
 
+// Where the rows of K (and V) go: k_out, or the pools of either cache.
+enum class To { kRows, kE4m3, kMx4 };
+
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 5;  // registers cut to fit: 24571 tokens 121 us with 4, 112 with 5, 114 with 6
+constexpr int kCtasMore = 4;   // with norms, or into the 4-bit cache: they do not fit 48 registers
+template <To kTo, bool kNorm>
+constexpr int ctas_per_sm() {
+    return kNorm || kTo == To::kMx4 ? kCtasMore : kCtasPerSm;
+}
 constexpr int kRows = 4;       // rows of a token that a warp has in flight
 // Tokens a CTA for at most 8 rows a token: one up to a wave of CTAs on 152 SMs, two up to three waves, then
 // four. One rank's 6 + 1 heads, 256 rotated elements, us with 1 / 2 / 4 tokens a CTA, rotary alone and with
@@ -40,9 +48,9 @@ constexpr int kRows = 4;       // rows of a token that a warp has in flight
 // 3.8 / 4.6, 16000 tokens 21.9 / 20.7 / 17.5 and 30.9 / 27.1 / 26.1.
 constexpr int64_t kTokensOne = 760, kTokensTwo = 4560;
 constexpr int64_t kMaxTokens = 0x7FFFFFFF;  // CTAs of a launch
-
-// Where the rows of K (and V) go: k_out, or the pools of either cache.
-enum class To { kRows, kE4m3, kMx4 };
+// Tokens from which V goes to the 4-bit cache by groups of 64, and up to which its CTAs and the tokens' are
+// launched together (256 heads: 5 CTAs a token).
+constexpr int64_t kVGroupFrom = 1024, kVGroupTo = 1 << 28;
 
 struct RopeParams {
     const void *q, *k, *v;
@@ -59,6 +67,7 @@ struct RopeParams {
     int64_t num_tokens, num_slots;
     int num_q_heads, num_kv_heads, rotary_dim;
     float amplitude;
+    int64_t v_ctas;                   // To::kMx4: first CTAs, which write V by groups of tokens (0: rows do)
     const void *q_weight, *k_weight;  // head norms; null: that operand is not normed
     float eps, weight_offset;
 };
@@ -147,20 +156,39 @@ __device__ __forceinline__ float scale_of(const RopeParams& p, int h) {
     return kTo != To::kE4m3 || h < 0 ? 1.f : (h < p.num_kv_heads ? *p.k_scale : *p.v_scale);
 }
 
-// A head's norm: its 256 elements lie in the warp, eight a lane (a from element `at` on, b from at + gap on).
+// Head norms. A head's 256 elements lie in the warp, eight a lane.
+__device__ __forceinline__ const void* norm_weight(const RopeParams& p, int h) {
+    return h < 0 ? p.q_weight : (h < p.num_kv_heads ? p.k_weight : nullptr);
+}
+// 1 / sqrt(mean of squares + eps) of several heads, their sums over the warp side by side.
+template <typename T, int kHeads>
+__device__ __forceinline__ void norm_factors(const RopeParams& p, const uint2 (&wa)[kHeads],
+                                             const uint2 (&wb)[kHeads], float (&r)[kHeads]) {
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) {
+        float a[4], b[4];
+        unpack<T>(wa[k], a);
+        unpack<T>(wb[k], b);
+        r[k] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[k] = fmaf(a[i], a[i], fmaf(b[i], b[i], r[k]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < kHeads; ++k) r[k] += __shfl_xor_sync(0xffffffffu, r[k], o);
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) r[k] = rsqrtf(fmaf(r[k], 1.f / kHeadDim, p.eps));
+}
+// The lane's pieces (elements from `at` and from at + gap on) times the factor and the weights. (Weights kept
+// in registers over the rows of Q cost more in warps than their loads: 24571 tokens 154 us, so 149.)
 template <typename T>
-__device__ __forceinline__ void norm_row(const RopeParams& p, const void* weight, int at, int gap,
+__device__ __forceinline__ void norm_row(const RopeParams& p, const void* weight, float r, int at, int gap,
                                          float (&a)[4], float (&b)[4]) {
     float wa[4], wb[4];
     const T* w = static_cast<const T*>(weight) + at;
     unpack<T>(__ldg(reinterpret_cast<const uint2*>(w)), wa);
     unpack<T>(__ldg(reinterpret_cast<const uint2*>(w + gap)), wb);
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum = fmaf(a[i], a[i], fmaf(b[i], b[i], sum));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float r = 1.f / sqrtf(sum * (1.f / kHeadDim) + p.eps);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         a[i] = a[i] * r * (p.weight_offset + wa[i]);
@@ -202,32 +230,133 @@ __device__ __forceinline__ void put_mx4_k(uint8_t* chunk, int tok, int lane, int
         chunk[mx4::kCodeBytes + tok * mx4::kBlocks + block] = (uint8_t)s;
 }
 
-// A row of V into its chunk: a lane has elements 4 lane + i and 4 lane + 128 + i (a and b), which share
-// bytes; eight lanes have a block of each half.
-__device__ __forceinline__ void put_mx4_v(uint8_t* chunk, int tok, int lane, const float (&a)[4],
-                                          const float (&b)[4]) {
+// A lane's elements 4 lane + i and 4 lane + 128 + i of a row of V: their codes (byte i), and the scale bytes of
+// the two blocks.
+struct VCodes {
+    uint32_t codes;
+    int sa, sb;
+};
+__device__ __forceinline__ VCodes v_codes(const float (&a)[4], const float (&b)[4]) {
     uint32_t ma = 0, mb = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         ma = max(ma, size_bits(a[i]));
         mb = max(mb, size_bits(b[i]));
     }
-    const int sa = mx4::scale_of_max(lanes_max<3>(ma)), sb = mx4::scale_of_max(lanes_max<3>(mb));
-    const float ia = mx4::inverse_of_scale(sa), ib = mx4::inverse_of_scale(sb);
+    VCodes v;
+    v.sa = mx4::scale_of_max(lanes_max<3>(ma));
+    v.sb = mx4::scale_of_max(lanes_max<3>(mb));
+    const float ia = mx4::inverse_of_scale(v.sa), ib = mx4::inverse_of_scale(v.sb);
     float x[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        x[2 * i] = sa == mx4::kNanScale ? 0.f : a[i] * ia;
-        x[2 * i + 1] = sb == mx4::kNanScale ? 0.f : b[i] * ib;
+        x[2 * i] = v.sa == mx4::kNanScale ? 0.f : a[i] * ia;
+        x[2 * i + 1] = v.sb == mx4::kNanScale ? 0.f : b[i] * ib;
     }
-    const uint32_t codes = mx4::codes_of(x);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        chunk[(4 * lane + i) * mx4::kTokens + tok] = (uint8_t)(codes >> (8 * i));
+    v.codes = mx4::codes_of(x);
+    return v;
+}
+__device__ __forceinline__ void put_v_scales(uint8_t* chunk, int tok, int lane, const VCodes& v) {
     if ((lane & 7) == 0) {
         uint8_t* scales = chunk + mx4::kCodeBytes + tok * mx4::kBlocks + (lane >> 3);
-        scales[0] = (uint8_t)sa;
-        scales[4] = (uint8_t)sb;
+        scales[0] = (uint8_t)v.sa;
+        scales[4] = (uint8_t)v.sb;
+    }
+}
+
+// A row of V into its chunk: eight lanes have a block of each half, a lane four bytes, 16 apart.
+__device__ __forceinline__ void put_mx4_v(uint8_t* chunk, int tok, int lane, const float (&a)[4],
+                                          const float (&b)[4]) {
+    const VCodes v = v_codes(a, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        chunk[(4 * lane + i) * mx4::kTokens + tok] = (uint8_t)(v.codes >> (8 * i));
+    put_v_scales(chunk, tok, lane, v);
+}
+
+// V of many tokens: a CTA takes 64 tokens of one head, has their codes in shared memory by words of four
+// tokens ([group of four][byte of the row]), and writes what is a whole chunk (16 slots in a row, as tokens of
+// a prompt have) in 16-byte pieces, the rest byte by byte. Row by row, a token's bytes are 128 stores of
+// one, and the L2 takes a sector for each.
+constexpr int kVGroup = 64;
+template <typename T>
+__device__ __forceinline__ void put_v_group(const RopeParams& p, int64_t group, uint32_t* words,
+                                            int64_t* slots, uint64_t* masks) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = (int)(group % p.num_kv_heads);
+    const int64_t t0 = group / p.num_kv_heads * kVGroup;
+    const int n = (int)min((int64_t)kVGroup, p.num_tokens - t0);
+    uint32_t* const bits = reinterpret_cast<uint32_t*>(masks);  // slots that end a run: starts, and none
+    if (tid < kVGroup) {
+        auto slot_of = [&](int i) -> int64_t {
+            const int64_t s = i >= 0 && i < n ? p.slots[t0 + i] : -1;
+            return s < p.num_slots ? s : -1;
+        };
+        const int64_t s = slot_of(tid);
+        slots[tid] = s;
+        const bool start = s < 0 || s % mx4::kTokens == 0 || tid == 0 || slot_of(tid - 1) != s - 1;
+        const uint32_t m = __ballot_sync(0xffffffffu, start);
+        if (lane == 0) bits[warp] = m;
+    }
+    __syncthreads();
+    const T* v = static_cast<const T*>(p.v) + h * kHeadDim + 4 * lane;
+#pragma unroll
+    for (int g = 0; g < kVGroup / 4 / kWarps; ++g) {
+        const int tg = warp * (kVGroup / 4 / kWarps) + g;
+        uint2 wa[4], wb[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const T* row = v + (t0 + min(4 * tg + i, n - 1)) * p.v_stride;
+            wa[i] = __ldcs(reinterpret_cast<const uint2*>(row));
+            wb[i] = __ldcs(reinterpret_cast<const uint2*>(row + kHeadDim / 2));
+        }
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float a[4], b[4];
+            unpack<T>(wa[i], a);
+            unpack<T>(wb[i], b);
+            const VCodes c = v_codes(a, b);
+            u[i] = c.codes;
+            const int64_t s = slots[4 * tg + i];
+            if (s >= 0)
+                put_v_scales(p.v_pool + mx4::chunk_offset(s, p.num_kv_heads, h),
+                             (int)(s % mx4::kTokens), lane, c);
+        }
+        uint32_t w[4];  // four tokens' bytes of elements 4 lane + k
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t two = k | (4 + k) << 4;
+            w[k] = __byte_perm(__byte_perm(u[0], u[1], two), __byte_perm(u[2], u[3], two), 0x5410);
+        }
+        *reinterpret_cast<uint4*>(words + tg * 128 + 4 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __syncthreads();
+    // runs of slots inside a chunk, half of the CTA each; a thread has one byte of the row
+    const int e = tid & 127;
+    uint64_t left = masks[0];
+    for (int run = 0; left; ++run) {
+        const int i = __ffsll((long long)left) - 1;
+        left &= left - 1;
+        const int len = (left ? __ffsll((long long)left) - 1 : kVGroup) - i;
+        const int64_t s = slots[i];
+        if ((run & 1) != tid >> 7 || s < 0) continue;
+        uint8_t* dst = p.v_pool + mx4::chunk_offset(s, p.num_kv_heads, h) + e * mx4::kTokens +
+                       s % mx4::kTokens;
+        const uint32_t* src = words + (i >> 2) * 128 + e;
+        const int shift = 8 * (i & 3);
+        if (len == mx4::kTokens) {  // (i <= 47 if it is shifted: the fifth word is there)
+            uint32_t w[5];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = src[k * 128];
+            w[4] = shift ? src[4 * 128] : 0;
+            *reinterpret_cast<uint4*>(dst) =
+                make_uint4(__funnelshift_r(w[0], w[1], shift), __funnelshift_r(w[1], w[2], shift),
+                           __funnelshift_r(w[2], w[3], shift), __funnelshift_r(w[3], w[4], shift));
+        } else {
+            for (int k = 0; k < len; ++k)
+                dst[k] = (uint8_t)(words[((i + k) >> 2) * 128 + e] >> (8 * ((i + k) & 3)));
+        }
     }
 }
 
@@ -242,13 +371,13 @@ __device__ __forceinline__ Pieces pieces_of(int lane, bool turned, int rotary_di
 }
 
 // Row r of token t: Q rows, then K's, then V's. Its two pieces (at, at + gap) normed and turned, then rounded
-// and stored, by the scale that scale_now(its head past Q's) gives. `row`: the warp's shared memory
-// (To::kMx4).
+// and stored, by the scale that scale_now(its head past Q's) gives. norm: its norm's factor (kNorm); row:
+// the warp's shared memory (To::kMx4).
 template <typename T, bool kHalf, To kTo, bool kNorm, typename Scale>
 __device__ __forceinline__ void put_row(const RopeParams& p, int64_t t, int64_t slot, int r, int at,
                                         int gap, bool turned, const uint2& wa, const uint2& wb,
                                         const float (&c)[4], const float (&s)[4], Scale scale_now,
-                                        float* row) {
+                                        float norm, float* row) {
     constexpr bool kWrite = kTo != To::kRows;
     const int h = r - p.num_q_heads;
     const bool is_q = h < 0, is_v = h >= p.num_kv_heads;
@@ -257,8 +386,8 @@ __device__ __forceinline__ void put_row(const RopeParams& p, int64_t t, int64_t 
     unpack<T>(wa, a);
     unpack<T>(wb, b);
     if constexpr (kNorm) {
-        const void* weight = is_q ? p.q_weight : p.k_weight;
-        if (!is_v && weight) norm_row<T>(p, weight, at, gap, a, b);
+        const void* weight = norm_weight(p, h);
+        if (weight) norm_row<T>(p, weight, norm, at, gap, a, b);
     }
     // (elements past the rotated part are not multiplied: an infinity times a zero sine
     // would be NaN)
@@ -288,16 +417,31 @@ __device__ __forceinline__ void put_row(const RopeParams& p, int64_t t, int64_t 
     }
 }
 
+// Rows of a token that its CTA has: Q's, K's and V's.
+template <To kTo>
+__host__ __device__ inline int rows_of(const RopeParams& p) {
+    return p.num_q_heads + p.num_kv_heads * (kTo != To::kRows ? (p.v_ctas ? 1 : 2) : (p.k ? 1 : 0));
+}
+
 // One token a CTA, up to kRows rows of it a warp at a time. K and V rows go to the pools;
 // To::kRows: K (if any) to k_out.
 template <typename T, bool kHalf, To kTo, bool kNorm>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, (ctas_per_sm<kTo, kNorm>())) rope_kernel(const RopeParams p) {
     constexpr bool kWrite = kTo != To::kRows;
     __shared__ __align__(16) float2 cs[kHeadDim / 2];
     __shared__ __align__(16) float staged[kTo == To::kMx4 ? kWarps : 1][kTo == To::kMx4 ? kHeadDim : 4];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rows = p.num_q_heads + p.num_kv_heads * (kWrite ? 2 : (p.k ? 1 : 0));
-    const int64_t t = blockIdx.x;
+    const int rows = rows_of<kTo>(p);
+    int64_t t = blockIdx.x;
+    if constexpr (kTo == To::kMx4) {
+        __shared__ int64_t v_slots[kVGroup];
+        __shared__ uint64_t v_masks;
+        if (t < p.v_ctas) {
+            put_v_group<T>(p, t, reinterpret_cast<uint32_t*>(staged), v_slots, &v_masks);
+            return;
+        }
+        t -= p.v_ctas;
+    }
     const int64_t slot = kWrite ? p.slots[t] : 0, live = live_tokens<kTo>(p);
     const int pos = p.positions[t];
     const T* q = static_cast<const T*>(p.q) + t * p.q_stride;
@@ -326,7 +470,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_kernel(const RopePa
             if (kWrite && slot >= p.num_slots && tid == 0)
                 atomicOr(p.status, DFLASH_FLAG_SLOT_RANGE);
         }
-        float c[4], s[4];
+        float c[4], s[4], norm[kRows];
+        if constexpr (kNorm) norm_factors<T>(p, wa, wb, norm);
         if (turned) lane_turns(cs, lane, c, s);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
@@ -335,21 +480,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_kernel(const RopePa
             const Pieces pc = piece(r - p.num_q_heads);
             put_row<T, kHalf, kTo, kNorm>(p, t, slot, r, pc.at, pc.gap, turned, wa[i], wb[i], c, s,
                                           [&](int hs) { return scale_of<kTo>(p, hs); },
-                                          staged[kTo == To::kMx4 ? warp : 0]);
+                                          kNorm ? norm[i] : 1.f, staged[kTo == To::kMx4 ? warp : 0]);
         }
     }
 }
 
 // kTokens tokens a CTA, for at most kWarps rows a token: warp w has row w of each of them.
 template <typename T, bool kHalf, To kTo, bool kNorm, int kTokens>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_tokens_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, (ctas_per_sm<kTo, kNorm>())) rope_tokens_kernel(const RopeParams p) {
     constexpr bool kWrite = kTo != To::kRows;
     __shared__ __align__(16) float2 cs[kTokens][kHeadDim / 2];
     __shared__ __align__(16) float staged[kTo == To::kMx4 ? kWarps : 1][kTo == To::kMx4 ? kHeadDim : 4];
     __shared__ int64_t slots[kTokens];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rows = p.num_q_heads + p.num_kv_heads * (kWrite ? 2 : (p.k ? 1 : 0));
-    const int64_t t0 = (int64_t)blockIdx.x * kTokens, last = p.num_tokens - 1;
+    const int rows = rows_of<kTo>(p);
+    int64_t block = blockIdx.x;
+    if constexpr (kTo == To::kMx4) {
+        __shared__ int64_t v_slots[kVGroup];
+        __shared__ uint64_t v_masks;
+        if (block < p.v_ctas) {
+            put_v_group<T>(p, block, reinterpret_cast<uint32_t*>(staged), v_slots, &v_masks);
+            return;
+        }
+        block -= p.v_ctas;
+    }
+    const int64_t t0 = block * kTokens, last = p.num_tokens - 1;
     const bool turned = lane < p.rotary_dim / 8;
     // (what is past the last row or token is read again and not stored)
     const int r = min(warp, rows - 1), h = r - p.num_q_heads;
@@ -374,6 +529,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_tokens_kernel(const
         wa[i] = __ldcs(reinterpret_cast<const uint2*>(row + at));
         wb[i] = __ldcs(reinterpret_cast<const uint2*>(row + at + gap));
     }
+    float norm[kTokens];
+    if constexpr (kNorm) norm_factors<T>(p, wa, wb, norm);
     const float scale = scale_of<kTo>(p, h);
     const int64_t live = live_tokens<kTo>(p);
     if (kWrite && tid < kTokens) {
@@ -397,15 +554,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_tokens_kernel(const
         float c[4], s[4];
         if (turned) lane_turns(cs[i], lane, c, s);
         put_row<T, kHalf, kTo, kNorm>(p, t, slot, r, at, gap, turned, wa[i], wb[i], c, s,
-                                      [&](int) { return scale; },
+                                      [&](int) { return scale; }, kNorm ? norm[i] : 1.f,
                                       staged[kTo == To::kMx4 ? warp : 0]);
     }
 }
 
 template <typename T, bool kHalf, To kTo, bool kNorm>
 cudaError_t launch_as(const RopeParams& p, cudaStream_t stream) {
-    const int rows = p.num_q_heads + p.num_kv_heads * (kTo != To::kRows ? 2 : (p.k ? 1 : 0));
-    auto ctas = [&](int tokens) { return (unsigned)((p.num_tokens + tokens - 1) / tokens); };
+    const int rows = rows_of<kTo>(p);
+    auto ctas = [&](int tokens) {
+        return (unsigned)((p.num_tokens + tokens - 1) / tokens + p.v_ctas);
+    };
     if (rows > kWarps)
         rope_kernel<T, kHalf, kTo, kNorm><<<ctas(1), kThreads, 0, stream>>>(p);
     else if (p.num_tokens <= kTokensOne)
@@ -568,6 +727,8 @@ int write(const dflash_rope_plan_t* plan, const dflash_head_norm* norm, int64_t 
     p.num_kv_heads = pr.num_kv_heads;
     p.rotary_dim = pr.rotary_dim;
     p.amplitude = plan->amplitude;
+    if (!kScaled && num_tokens >= kVGroupFrom && num_tokens <= kVGroupTo)
+        p.v_ctas = (num_tokens + kVGroup - 1) / kVGroup * pr.num_kv_heads;
     return launch<kTo>(plan, p, norm, cuda_stream);
 }
 

@@ -187,6 +187,40 @@ def test_mx4_write(T, Hq, Hkv, P, dtype, layout):
     assert r.read_flags() == (B.DFLASH_FLAG_SLOT_RANGE if T > 8 else 0)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("T,Hq,Hkv,P,off", [(1023, 2, 2, 16, 0), (1024, 6, 1, 64, 0), (1025, 24, 4, 64, 5),
+                                            (2111, 6, 1, 16, 3), (1500, 8, 8, 48, 13)])
+def test_mx4_write_of_prompts(T, Hq, Hkv, P, off, dtype):
+    """Runs of slots, as prompts have, that begin anywhere in a page, with padding in between: every byte
+    of both pools."""
+    from speculative_verify_paged_e4m3_gb300 import binding as B
+    q, k, v, pos, qw, kw = make(T + off, T, Hq, Hkv, dtype, fused=T % 2 == 1)
+    pages = -(-(T + off) // P) + 2
+    rng = np.random.default_rng(T)
+    order = rng.permutation(pages)
+    at = np.arange(T) + off
+    slots = order[at // P] * P + at % P
+    slots[rng.random(T) < 0.02] = -1
+    slots[T // 2:T // 2 + 20] = -1
+    slots[-1] = pages * P + 3
+    r = B.Rotary(Hq, Hkv, D, page_size=P, num_pages=pages, dtype=dtype)
+    kp, vp = B.Mx4Cache(Hkv, D, P, pages).empty()
+    kp.fill_(0x33)
+    vp.fill_(0x44)
+    zero = torch.zeros_like(pos)
+    q_out = torch.full((T, Hq, D), 3.0, dtype=dtype, device="cuda")
+    r.mx4_write(q, k, v, zero, torch.from_numpy(slots).cuda(), kp, vp, q_out=q_out)
+    on = (slots >= 0) & (slots < pages * P)
+    for got, x, of_v, fill in ((kp, k, False, 0x33), (vp, v, True, 0x44)):
+        want = np.full(got.shape, fill, dtype=np.uint8)
+        codes, s = M.quantise(x.double().cpu().numpy()[on])
+        M.put(want, slots[on], codes, s, of_v)
+        assert np.array_equal(got.cpu().numpy(), want)
+    keep = torch.from_numpy(slots >= 0).cuda()
+    assert torch.equal(q_out[keep], q[keep]) and (q_out[~keep] == 3).all()
+    assert r.read_flags() == B.DFLASH_FLAG_SLOT_RANGE
+
+
 def test_mx4_write_without_norm_or_rotation_is_the_formula():
     """Position 0 turns nothing: K's codes are then the formula's, bit for bit. Zeros, ties, numbers
     between 6 and 7 units, subnormal ones, infinities and NaN."""
