@@ -95,6 +95,7 @@ struct Small {
     uint64_t sfull[2], sfree[2], pfull, pfree, odone, qready;
     uint32_t tmem_base;
     int abort;
+    int never;  // stays 0: for a wait that goes on when the CTA gives up
     float rmax[kMaxRP / kGroupRows][4][kGroupRows];   // per-group, per-warp row maxima of a tile
     float rsum[kMaxRP / kGroupRows][4][kGroupRows];   // per-group, per-warp row sums of the split
     float mref[kMaxRP / kGroupRows][kGroupRows];      // the split state's max of each row
@@ -321,8 +322,8 @@ __device__ __forceinline__ void copy_tiles(const PartialParams& p, const Ctx& ct
     if (lane == 0)
 #pragma unroll 1
         for (int u = t - kStages < 0 ? 0 : t - kStages; u < t; ++u) {
-            mbar_wait(smem_u32(&sm.kfull[u % kStages]), (u / kStages) & 1, &sm.abort, kWaitLimitNs);
-            mbar_wait(smem_u32(&sm.vfull[u % kStages]), (u / kStages) & 1, &sm.abort, kWaitLimitNs);
+            mbar_wait(smem_u32(&sm.kfull[u % kStages]), (u / kStages) & 1, &sm.never, kWaitLimitNs);
+            mbar_wait(smem_u32(&sm.vfull[u % kStages]), (u / kStages) & 1, &sm.never, kWaitLimitNs);
         }
 }
 
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         mbar_init(smem_u32(&sm.pfree), 1);
         mbar_init(smem_u32(&sm.odone), 2);  // both threads that issue products
         mbar_init(smem_u32(&sm.qready), C::kSoftWarps);
-        sm.abort = 0;
+        sm.abort = sm.never = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
