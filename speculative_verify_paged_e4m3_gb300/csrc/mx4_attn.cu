@@ -7,7 +7,7 @@
 // memory: stored there as FP16, a tile of 128 keys would be written (128 KB) and read by the tensor core
 // (128 KB), 2048 clocks of 128 bytes, while its codes come from HBM in 1500. So neither K nor V goes there
 // decoded: both are the products' first operand, which may lie in tensor memory, and warps write it from
-// registers, a lane a key of K, or an element of the head (two: i and i + 128) of V. The cache's layout
+// registers, a lane a key of K, or two elements of the head, i and i + 128, of V. The cache's layout
 // is made for that (dflash_mx4_cache.h): a thread reads its codes in 16-byte pieces without bank
 // conflicts, and a chunk of 16 tokens comes by one bulk copy.
 //
@@ -19,7 +19,7 @@
 //    FP16 has a fixed step, 2^-24, 2^-32 of the largest at least.
 //  * NaN. A key with a NaN scale in K or V gets a NaN factor or exponent: its probability is NaN in
 //    every row that sees it and 0, selected, in the others. V's own factor is then 0.
-//  * Warps: 0 copies the codes (five tiles ahead), 1 and 2 issue the products of the scores and of the
+//  * Warps: 0 copies the codes (four tiles ahead), 1 and 2 issue the products of the scores and of the
 //    output, 3 works out the factors of a tile's keys, 4-7 decode K, 8-11 V, the others are the softmax, four
 //    for 16 rows.
 //  * Every wait on another warp or on a copy is bounded: on a timeout the CTA sets
@@ -52,7 +52,7 @@ constexpr int kTile = 128;       // keys per tile = MMA M
 constexpr int kChunks = kTile / kTokens;
 constexpr int kMaxRP = 48;       // padded rows a CTA carries
 constexpr int kGroupRows = 16;
-constexpr int kStages = 5;       // tiles of codes of K, and of V, on their way
+constexpr int kStages = 4;       // tiles of codes of K, and of V, on their way
 constexpr int kInfos = 4;        // tiles of factors
 constexpr uint32_t kStageBytes = kChunks * kChunkBytes;
 constexpr uint64_t kWaitLimitNs = 200ull * 1000 * 1000;
@@ -64,7 +64,7 @@ constexpr int kMaxEv = 40;
 constexpr int kKWarp = 4, kVWarp = 8, kSoftWarp = 12;
 
 // Shared memory: Q | P | codes of K | codes of V | factors | Small. Tensor memory: K [two head-dim
-// halves][64] | V [two halves of the keys][two of the head dim][32] | S [two tiles][RP] | O [two halves of
+// halves][64] | V [two halves of the keys][64] | S [two tiles][RP] | O [two halves of
 // the head dim][RP].
 template <int RP>
 struct Cfg {
@@ -72,7 +72,8 @@ struct Cfg {
     static constexpr int kSoftWarps = 4 * kGroups;
     static constexpr int kThreads = 32 * (kSoftWarp + kSoftWarps);
     static constexpr uint32_t kOffP = RP * kHeadDim * 2;
-    static constexpr uint32_t kOffK = kOffP + RP * kTile * 2;
+    static constexpr uint32_t kPBytes = 2 * RP * 2 * kTile * 2;
+    static constexpr uint32_t kOffK = kOffP + kPBytes;
     static constexpr uint32_t kOffV = kOffK + kStages * kStageBytes;
     static constexpr uint32_t kOffInfo = kOffV + kStages * kStageBytes;
     static constexpr uint32_t kColK = 0, kColV = 128, kColS = 256, kColO = kColS + 2 * RP;
@@ -85,7 +86,7 @@ struct Cfg {
 // Factors of a tile's keys: of their scores (in log2 units), V's exponent, and of V's blocks (FP16).
 struct Info {
     float2 c[kTile];  // (score factor, V's exponent)
-    uint16_t f[kBlocks][kTile];
+    uint32_t f[kBlocks / 2][kTile];  // blocks j and j + 4
 };
 
 struct Small {
@@ -114,10 +115,15 @@ static_assert(sizeof(Info) % 16 == 0, "factors are read in 16-byte pieces");
 __device__ __forceinline__ uint32_t q_off(int row, int u, int rows) {
     return (u >> 3) * rows * 128 + (row >> 3) * 1024 + (row & 7) * 128 + (((u & 7) ^ (row & 7)) << 4);
 }
-// P: MN-major without swizzle, core matrices of 8 rows x 8 keys (a key's 8 rows are 16 bytes): key groups 128
-// bytes apart (the descriptor's leading offset), blocks of 8 rows 2 KB (its stride offset).
-__device__ __forceinline__ uint32_t p_off(int row_block, int key) {
-    return row_block * 2048 + (key >> 3) * 128 + (key & 7) * 16;
+// P, the output's second operand. A byte of V's codes holds elements e and e + 128 of a key, and decoded as they
+// lie they are neighbours in the contraction, which so runs over 2 x 128 places: place 2 key has the key's
+// weights in columns row, place 2 key + 1 in columns RP + row, and zeros are in the others. That doubles the
+// products' work, of which there is room for, and spares V's decoder the sorting of half bytes into pairs of
+// keys, a third of its operations (24/4 heads over 261888 tokens 105 -> 99 us).
+// MN-major without swizzle, core matrices of 8 rows x 8 places (of 16 bytes each): groups of places 128
+// bytes apart (the descriptor's leading offset), blocks of 8 rows 4 KB (its stride offset).
+__device__ __forceinline__ uint32_t p_off(int row_block, int k) {
+    return row_block * 4096 + (k >> 3) * 128 + (k & 7) * 16;
 }
 
 __device__ __forceinline__ float f32(uint32_t x) { return __uint_as_float(x); }
@@ -435,7 +441,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                     tile(Even{}, t);
             }
         } else if (issuer) {
-            constexpr uint32_t idesc = idesc_f32acc(128, RP, 0, 0, 0, 1);
+            constexpr uint32_t idesc = idesc_f32acc(128, 2 * RP, 0, 0, 0, 1);
             const uint32_t pb = smem_u32(smem + C::kOffP);
 #pragma unroll 1
             for (int t = 0; ok && t < ntiles; ++t) {
@@ -446,13 +452,10 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-#pragma unroll
-                        for (int mh = 0; mh < 2; ++mh)
-                            mma_ts(C::kColO + mh * RP, C::kColV + hv * 64 + mh * 32 + kk * 8,
-                                   smem_desc(pb + (4 * hv + kk) * 256, 128, 2048, kSwizzleNone), idesc,
-                                   hv || kk || t != 0);
-                    }
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_ts(C::kColO, C::kColV + hv * 64 + kk * 8,
+                               smem_desc(pb + (8 * hv + kk) * 256, 128, 4096, kSwizzleNone), idesc,
+                               hv || kk || t != 0);
                     mma_commit(smem_u32(&sm.vafree[hv]));
                 }
                 if (ok) mma_commit(smem_u32(&sm.pfree));
@@ -486,9 +489,10 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                 // 2^26 below the key's largest
                 const int base = 127 + ev - kFactorTop - 15;
 #pragma unroll
-                for (int j = 0; j < kBlocks; ++j) {
-                    const int sj = (int)(((j < 4 ? vs.x : vs.y) >> (8 * (j & 3))) & 255u);
-                    info.f[j][key] = (uint16_t)(min(max(sj - base, 0), kFactorTop + 1 + 15) << 10);
+                for (int j = 0; j < kBlocks / 2; ++j) {
+                    const int s0 = (int)((vs.x >> (8 * j)) & 255u), s1 = (int)((vs.y >> (8 * j)) & 255u);
+                    info.f[j][key] = (uint32_t)min(max(s0 - base, 0), kFactorTop + 1 + 15) << 10 |
+                                     (uint32_t)min(max(s1 - base, 0), kFactorTop + 1 + 15) << 26;
                 }
             }
             __syncwarp();
@@ -553,8 +557,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                 !ctx.wait_warp(&sm.infofull[is], iring.parity))
                 break;
             const uint8_t* stage = smem + C::kOffV + s * kStageBytes + e * kTokens;
-            const uint16_t* f0 = infos[is].f[quad];
-            const uint16_t* f1 = infos[is].f[4 + quad];
+            const uint32_t* f = infos[is].f[quad];
             bool ok = true;
 #pragma unroll 1
             for (int hv = 0; hv < 2; ++hv) {
@@ -562,36 +565,19 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll 1
-                for (int it = 0; it < 2; ++it) {  // two chunks: 32 keys, 16 columns of each half
-                    uint32_t lo[16], hi[16];
+                for (int c = 4 * hv; c < 4 * hv + 4; ++c) {  // a chunk: 16 keys, a column each
+                    const uint4 w = *reinterpret_cast<const uint4*>(stage + c * kChunkBytes);
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t o[16];
 #pragma unroll
-                    for (int c2 = 0; c2 < 2; ++c2) {
-                        const int c = 4 * hv + 2 * it + c2;
-                        const uint4 w = *reinterpret_cast<const uint4*>(stage + c * kChunkBytes);
-                        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {  // 8 keys
-                            const uint4 a = *reinterpret_cast<const uint4*>(f0 + c * kTokens + 8 * q);
-                            const uint4 d = *reinterpret_cast<const uint4*>(f1 + c * kTokens + 8 * q);
-                            const uint32_t fa[4] = {a.x, a.y, a.z, a.w}, fb[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                // four keys' bytes: the two keys of a pair into bytes 1 and 3, low halves
-                                // (element e) and high halves (e + 128); bytes 0 and 2 are not used
-                                constexpr uint32_t m = 0x0F000F00u;
-                                const uint32_t x = u[2 * q + i], x4 = x << 4;
-                                const uint32_t l = ((x << 8) & m) | (x4 & ~m);
-                                const uint32_t g = (x4 & m) | (x & ~m);
-                                const int o = 8 * c2 + 4 * q + 2 * i;
-                                lo[o] = mul_f16x2(codes_to_f16x2<1>(l), fa[2 * i]);
-                                lo[o + 1] = mul_f16x2(codes_to_f16x2<3>(l), fa[2 * i + 1]);
-                                hi[o] = mul_f16x2(codes_to_f16x2<1>(g), fb[2 * i]);
-                                hi[o + 1] = mul_f16x2(codes_to_f16x2<3>(g), fb[2 * i + 1]);
-                            }
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(f + c * kTokens + 4 * i);
+                        o[4 * i] = mul_f16x2(codes_to_f16x2<0>(u[i]), x.x);
+                        o[4 * i + 1] = mul_f16x2(codes_to_f16x2<1>(u[i]), x.y);
+                        o[4 * i + 2] = mul_f16x2(codes_to_f16x2<2>(u[i]), x.z);
+                        o[4 * i + 3] = mul_f16x2(codes_to_f16x2<3>(u[i]), x.w);
                     }
-                    tmem_st16(lane_base + C::kColV + hv * 64 + it * 16, lo);
-                    tmem_st16(lane_base + C::kColV + hv * 64 + 32 + it * 16, hi);
+                    tmem_st16(lane_base + C::kColV + c * 16, o);
                 }
                 warp_arrive_tmem(&sm.vafull[hv]);
             }
@@ -633,6 +619,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                 if (__any_sync(0xffffffffu, bad)) qraw[k].x = 0x7E007E00u;
                 *reinterpret_cast<uint4*>(smem + q_off(sw + C::kSoftWarps * k, lane, RP)) = qraw[k];
             }
+            for (uint32_t i = (sw * 32 + lane) * 16; i < C::kPBytes; i += C::kSoftWarps * 32 * 16)
+                *reinterpret_cast<uint4*>(smem + C::kOffP + i) = make_uint4(0, 0, 0, 0);
             fence_async_smem();
             warp_arrive(&sm.qready);
         }
@@ -776,8 +764,12 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
             if (!ok) alive = false;
             if (!alive) continue;  // every warp still runs the remaining tiles' barriers
             uint8_t* pbuf = smem + C::kOffP;
-            *reinterpret_cast<uint4*>(pbuf + p_off(2 * g, st)) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-            *reinterpret_cast<uint4*>(pbuf + p_off(2 * g + 1, st)) = make_uint4(ph[4], ph[5], ph[6], ph[7]);
+#pragma unroll
+            for (int mh = 0; mh < 2; ++mh) {
+                uint8_t* at = pbuf + p_off(mh * (RP / 8) + 2 * g, 2 * st + mh);
+                *reinterpret_cast<uint4*>(at) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+                *reinterpret_cast<uint4*>(at + 4096) = make_uint4(ph[4], ph[5], ph[6], ph[7]);
+            }
             fence_async_smem();
             tc_fence_before();
             warp_arrive(&sm.pfull);
