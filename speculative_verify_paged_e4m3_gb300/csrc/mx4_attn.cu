@@ -179,23 +179,28 @@ __device__ __forceinline__ bool try_wait_hint(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
+// The rest of a wait whose first try failed. Not inlined: the warps' loops compete for the instruction caches, and
+// with this code at each of twenty waits 32 sequences of one token took 158 us for 155. (Reading the clock
+// between the tries keeps them apart: without, the waiting warps took the others' time, 131 us for 109.)
+__device__ __noinline__ bool wait_on(uint32_t addr, uint32_t parity, volatile int* abort,
+                                     int32_t* status) {
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+        if (try_wait_hint(addr, parity)) return true;
+        if (*abort) return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+    }
+    *abort = 1;
+    atomicOr(status, DFLASH_FLAG_KERNEL_TIMEOUT);
+    return false;
+}
+
 struct Ctx {
     Small* sm;
     int32_t* status;
     __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
         const uint32_t addr = smem_u32(bar);
-        if (try_wait_hint(addr, parity)) return true;
-        // (reading the clock between the tries keeps them apart: without, the waiting warps took the
-        // others' time, 131 us for 109)
-        const uint64_t t0 = globaltimer_ns();
-        while (true) {
-            if (try_wait_hint(addr, parity)) return true;
-            if (aborted()) return false;
-            if (globaltimer_ns() - t0 > kWaitLimitNs) break;
-        }
-        *reinterpret_cast<volatile int*>(&sm->abort) = 1;
-        atomicOr(status, DFLASH_FLAG_KERNEL_TIMEOUT);
-        return false;
+        return try_wait_hint(addr, parity) || wait_on(addr, parity, &sm->abort, status);
     }
     // by a whole warp, whose lanes agree on the result
     __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) const {
@@ -267,9 +272,9 @@ __device__ __forceinline__ float rows_reduce(float (&v)[kGroupRows], int lane, O
 }
 
 __device__ __forceinline__ int largest_byte(uint2 s) {
-    const uint32_t m4 = __vmaxu4(s.x, s.y);
-    const uint32_t m2 = __vmaxu4(m4, m4 >> 16);
-    return (int)(max(m2 & 255u, (m2 >> 8) & 255u));
+    // halves of 16 bits, whose upper bytes decide
+    const uint32_t m = __vmaxu2(__vimax3_u16x2(s.x, s.y, s.x << 8), s.y << 8);
+    return (int)(__vmaxu2(m, m << 16) >> 24);
 }
 
 // One warp's copies of both pools, tile after tile into their rings: lane c < 8 copies chunk c of K, lane 8 + c
@@ -410,15 +415,12 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         // one is decoded while the other is read.
         const bool issuer = elect_one();
         bool ok = issuer && ctx.wait(&sm.qready, 0);
-        using Even = std::integral_constant<int, 0>;
-        using Odd = std::integral_constant<int, 1>;
         if (warp == 1 && issuer) {
             constexpr uint32_t idesc = idesc_f32acc(128, RP, 0, 0, 0, 0);
             const uint32_t qb = smem_u32(smem);
-            auto tile = [&](auto parity, int t) {
-                constexpr int kS = decltype(parity)::value;
+            auto tile = [&](int kS, int t) {
                 ok = ctx.wait(&sm.sfree[kS], ((t >> 1) & 1) ^ 1);
-#pragma unroll
+#pragma unroll 1
                 for (int hd = 0; hd < 2; ++hd) {
                     ok = ok && ctx.wait(&sm.kafull[hd], kS);
                     if (!ok) return;
@@ -434,12 +436,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                 mma_commit(smem_u32(&sm.sfull[kS]));
             };
 #pragma unroll 1
-            for (int t = 0; ok && t < ntiles; ++t) {
-                if (t & 1)
-                    tile(Odd{}, t);
-                else
-                    tile(Even{}, t);
-            }
+            for (int t = 0; ok && t < ntiles; ++t) tile(t & 1, t);
         } else if (issuer) {
             constexpr uint32_t idesc = idesc_f32acc(128, 2 * RP, 0, 0, 0, 1);
             const uint32_t pb = smem_u32(smem + C::kOffP);
@@ -487,12 +484,12 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                 // block j's factor is 2^(s - 127 - ev + 12), at most 2^13 (finite for a NaN block and for
                 // whatever lies past the split's end: those weights are NaN and 0), and 0 for blocks
                 // 2^26 below the key's largest
-                const int base = 127 + ev - kFactorTop - 15;
+                const uint32_t shift = ((uint32_t)(kFactorTop + 15 - 127 - ev) & 0xFFFFu) * 0x00010001u;
 #pragma unroll
                 for (int j = 0; j < kBlocks / 2; ++j) {
-                    const int s0 = (int)((vs.x >> (8 * j)) & 255u), s1 = (int)((vs.y >> (8 * j)) & 255u);
-                    info.f[j][key] = (uint32_t)min(max(s0 - base, 0), kFactorTop + 1 + 15) << 10 |
-                                     (uint32_t)min(max(s1 - base, 0), kFactorTop + 1 + 15) << 26;
+                    const uint32_t two = __byte_perm(vs.x, vs.y, j | (4 + j) << 8) & 0x00FF00FFu;
+                    info.f[j][key] = __viaddmin_s16x2_relu(two, shift, (kFactorTop + 16) * 0x00010001u)
+                                     << 10;
                 }
             }
             __syncwarp();
@@ -519,7 +516,6 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
 #pragma unroll 1
             for (int hd = 0; hd < 2; ++hd) {
                 const uint8_t* codes = stage + at + 4 * hd * 256;
-                uint4 next = *reinterpret_cast<const uint4*>(codes);
                 uint32_t scale = hd ? sc.y : sc.x;
                 ok = ctx.wait_warp(&sm.kafree[hd], (t & 1) ^ 1);
                 if (!ok) break;
@@ -527,9 +523,9 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
 #pragma unroll 1
                 for (int j = 0; j < 4; ++j) {
                     const uint32_t f = f16x2_power((int)(scale & 255u) - top);
+                    const uint4 next = *reinterpret_cast<const uint4*>(codes + j * 256);
                     const uint32_t u[4] = {next.x, next.y, next.z, next.w};
                     scale >>= 8;
-                    next = *reinterpret_cast<const uint4*>(codes + ((j + 1) & 3) * 256);
                     uint32_t o[16];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -645,20 +641,15 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
             const float c = cev.x, ev = cev.y;
             if (alive && !ctx.wait_warp(&sm.sfull[t & 1], (t >> 1) & 1)) alive = false;
             tc_fence_after();
-            uint64_t y[kGroupRows / 2];
-            {
+            auto scores = [&](uint64_t (&y)[kGroupRows / 2]) {
                 uint32_t a[16];
                 tmem_ld16(lane_base + C::kColS + (t & 1) * RP + row0, a);
                 tmem_ld_wait(a);
 #pragma unroll
                 for (int q = 0; q < kGroupRows / 2; ++q) y[q] = pk2(f32(a[2 * q]), f32(a[2 * q + 1]));
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0 && alive) {
-                mbar_arrive(smem_u32(&sm.sfree[t & 1]));
-                mbar_arrive(smem_u32(&sm.infofree[is]));
-            }
+            };
+            uint64_t e[kGroupRows / 2];
+            scores(e);
             uint32_t validm = rowmask;  // bit i: key j visible to row row0 + i
             if (!((tile0 + kTile <= end) && (tile0 + kTile - 1 <= qoff))) {
                 // row r of the slot sees key j iff r >= (j - qoff) G: the group's rows from `first` on
@@ -670,10 +661,9 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
             }
             // exponents of the shifted weights: s c + ev + (shift - reference)
             const uint64_t c2 = pk2(c, c), ev2 = pk2(ev, ev);
-            uint64_t e[kGroupRows / 2];
             bool need = false;
 #pragma unroll
-            for (int q = 0; q < kGroupRows / 2; ++q) e[q] = fma2(y[q], c2, add2(nm[q], ev2));
+            for (int q = 0; q < kGroupRows / 2; ++q) e[q] = fma2(e[q], c2, add2(nm[q], ev2));
             const bool all_rows = validm == 0xFFFFu;
             if (all_rows) {
                 float m = lo2(e[0]);
@@ -695,6 +685,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                 // 2i + 1 derive row i's, the shuffles hand it to every lane. (The next tile's vote stands
                 // between these reads of the maxima and their next writing.)
                 float v[kGroupRows];
+                uint64_t y[kGroupRows / 2];
+                scores(y);
 #pragma unroll
                 for (int q = 0; q < kGroupRows / 2; ++q) {
                     y[q] = fma2(y[q], c2, ev2);
@@ -740,6 +732,12 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                         tmem_st_wait();
                     }
                 }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0 && alive) {
+                mbar_arrive(smem_u32(&sm.sfree[t & 1]));
+                mbar_arrive(smem_u32(&sm.infofree[is]));
             }
             // weights, their sum without V's exponent, and their FP16 rounding
             const float iev = ev == ev ? ex2(-ev) : 1.f;
