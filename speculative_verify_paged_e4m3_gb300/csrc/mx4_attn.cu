@@ -236,8 +236,9 @@ __device__ __forceinline__ void warp_arrive_tmem(uint64_t* bar) {
     warp_arrive(bar);
 }
 
-// Named barrier of one softmax group's 128 threads, optionally OR-reducing a vote. All four warps run every
-// tile (a failed wait skips work, never the loop), so each is always reached by all of them.
+// Named barrier of one softmax group's 128 threads, optionally OR-reducing a vote. After a failed wait a warp goes
+// on to the next vote, which takes all four out of the loop (what it computes until then is not stored:
+// the launch has failed), so each barrier is reached by all of them.
 __device__ __forceinline__ bool group_vote(int g, bool v) {
     uint32_t r;
     asm volatile(
@@ -636,10 +637,10 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
 #pragma unroll 1
         for (int t = 0; t < ntiles; ++t) {
             const int tile0 = start + t * kTile, j = tile0 + st, is = t % kInfos;
-            if (alive && !ctx.wait_warp(&sm.infofull[is], (t / kInfos) & 1)) alive = false;
+            alive = alive & ctx.wait_warp(&sm.infofull[is], (t / kInfos) & 1);
             const float2 cev = infos[is].c[st];
             const float c = cev.x, ev = cev.y;
-            if (alive && !ctx.wait_warp(&sm.sfull[t & 1], (t >> 1) & 1)) alive = false;
+            alive = alive & ctx.wait_warp(&sm.sfull[t & 1], (t >> 1) & 1);
             tc_fence_after();
             auto scores = [&](uint64_t (&y)[kGroupRows / 2]) {
                 uint32_t a[16];
@@ -678,9 +679,9 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                 }
             }
             bool need_any = true;  // tile 0 sets the reference
-            if (t > 0) need_any = group_vote(g, need);
-            bool ok = true;
+            if (t > 0) need_any = group_vote(g, need || !alive);
             if (need_any) {
+                if (group_vote(g, !alive)) break;  // all four warps together
                 // exact tile maximum per row -> new reference; row sums and O rescaled. Lanes 2i and
                 // 2i + 1 derive row i's, the shuffles hand it to every lane. (The next tile's vote stands
                 // between these reads of the maxima and their next writing.)
@@ -716,26 +717,24 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                     e[q] = add2(y[q], nm[q]);
                 }
                 if (t > 0) {
-                    ok = alive && ctx.wait_warp(&sm.pfree, (t - 1) & 1);  // O holds the tiles before
-                    if (ok) {
-                        tc_fence_after();
+                    alive = ctx.wait_warp(&sm.pfree, (t - 1) & 1);  // O holds the tiles before
+                    tc_fence_after();
 #pragma unroll 1
-                        for (int mh = 0; mh < 2; ++mh) {
-                            const uint32_t addr = lane_base + C::kColO + mh * RP + row0;
-                            uint32_t o[16];
-                            tmem_ld16(addr, o);
-                            tmem_ld_wait(o);
+                    for (int mh = 0; mh < 2; ++mh) {
+                        const uint32_t addr = lane_base + C::kColO + mh * RP + row0;
+                        uint32_t o[16];
+                        tmem_ld16(addr, o);
+                        tmem_ld_wait(o);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(f32(o[i]) * alpha[i]);
-                            tmem_st16(addr, o);
-                        }
-                        tmem_st_wait();
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(f32(o[i]) * alpha[i]);
+                        tmem_st16(addr, o);
                     }
+                    tmem_st_wait();
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0 && alive) {
+            if (lane == 0) {
                 mbar_arrive(smem_u32(&sm.sfree[t & 1]));
                 mbar_arrive(smem_u32(&sm.infofree[is]));
             }
@@ -758,9 +757,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                 make_p(std::true_type{});
             else
                 make_p(std::false_type{});
-            if (alive && ok && t > 0) ok = ctx.wait_warp(&sm.pfree, (t - 1) & 1);
-            if (!ok) alive = false;
-            if (!alive) continue;  // every warp still runs the remaining tiles' barriers
+            // (passes before the first product: the phase before the barrier's first)
+            alive = alive & ctx.wait_warp(&sm.pfree, (t - 1) & 1);
             uint8_t* pbuf = smem + C::kOffP;
 #pragma unroll
             for (int mh = 0; mh < 2; ++mh) {
