@@ -227,7 +227,6 @@ struct Ring {
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(bar));
-    __syncwarp();
 }
 // ... and its stores to tensor memory are complete.
 __device__ __forceinline__ void warp_arrive_tmem(uint64_t* bar) {
@@ -623,9 +622,6 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         }
         uint64_t lsum[kGroupRows / 2];
         uint64_t nm[kGroupRows / 2];  // the shift minus each row's reference (+inf: none yet), in pairs
-        uint32_t rowmask = 0;
-#pragma unroll
-        for (int i = 0; i < kGroupRows; ++i) rowmask |= (uint32_t)(row0 + i < R) << i;
 #pragma unroll
         for (int q = 0; q < kGroupRows / 2; ++q) {
             lsum[q] = 0;
@@ -651,33 +647,30 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
             };
             uint64_t e[kGroupRows / 2];
             scores(e);
-            uint32_t validm = rowmask;  // bit i: key j visible to row row0 + i
+            // bit i: key j visible to row row0 + i (rows past the slot's count: zeros of Q, not stored)
+            uint32_t validm = 0xFFFFu;
             if (!((tile0 + kTile <= end) && (tile0 + kTile - 1 <= qoff))) {
                 // row r of the slot sees key j iff r >= (j - qoff) G: the group's rows from `first` on
                 const int first = (j - qoff) * G - row_lo - row0;
                 if (j >= end)
                     validm = 0;
                 else if (first > 0)
-                    validm &= first >= kGroupRows ? 0u : (0xFFFFFFFFu << first);
+                    validm = first >= kGroupRows ? 0u : (0xFFFFu << first) & 0xFFFFu;
             }
             // exponents of the shifted weights: s c + ev + (shift - reference)
             const uint64_t c2 = pk2(c, c), ev2 = pk2(ev, ev);
-            bool need = false;
 #pragma unroll
             for (int q = 0; q < kGroupRows / 2; ++q) e[q] = fma2(e[q], c2, add2(nm[q], ev2));
-            const bool all_rows = validm == 0xFFFFu;
-            if (all_rows) {
-                float m = lo2(e[0]);
+            if (validm != 0xFFFFu) {
 #pragma unroll
-                for (int q = 0; q < kGroupRows / 2; ++q) m = fmaxf(m, fmaxf(lo2(e[q]), hi2(e[q])));
-                need = m > kLazyThreshold;
-            } else {
-#pragma unroll
-                for (int q = 0; q < kGroupRows / 2; ++q) {
-                    need |= ((validm >> (2 * q)) & 1u) && lo2(e[q]) > kLazyThreshold;
-                    need |= ((validm >> (2 * q + 1)) & 1u) && hi2(e[q]) > kLazyThreshold;
-                }
+                for (int q = 0; q < kGroupRows / 2; ++q)
+                    e[q] = pk2(((validm >> (2 * q)) & 1u) ? lo2(e[q]) : -INFINITY,
+                               ((validm >> (2 * q + 1)) & 1u) ? hi2(e[q]) : -INFINITY);
             }
+            float m = lo2(e[0]);
+#pragma unroll
+            for (int q = 0; q < kGroupRows / 2; ++q) m = fmaxf(m, fmaxf(lo2(e[q]), hi2(e[q])));
+            const bool need = m > kLazyThreshold;
             bool need_any = true;  // tile 0 sets the reference
             if (t > 0) need_any = group_vote(g, need || !alive);
             if (need_any) {
@@ -715,6 +708,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                                 __shfl_sync(0xffffffffu, nm_r, 4 * q + 2));
                     lsum[q] = mul2(lsum[q], pk2(alpha[2 * q], alpha[2 * q + 1]));
                     e[q] = add2(y[q], nm[q]);
+                    if (!((validm >> (2 * q)) & 1u)) e[q] = pk2(-INFINITY, hi2(e[q]));
+                    if (!((validm >> (2 * q + 1)) & 1u)) e[q] = pk2(lo2(e[q]), -INFINITY);
                 }
                 if (t > 0) {
                     alive = ctx.wait_warp(&sm.pfree, (t - 1) & 1);  // O holds the tiles before
@@ -742,21 +737,13 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
             const float iev = ev == ev ? ex2(-ev) : 1.f;
             const uint64_t iev2 = pk2(iev, iev);
             uint32_t ph[kGroupRows / 2];
-            auto make_p = [&](auto all) {
-                constexpr bool kAll = decltype(all)::value;
 #pragma unroll
-                for (int q = 0; q < kGroupRows / 2; ++q) {
-                    const float p0 = (kAll || ((validm >> (2 * q)) & 1u)) ? ex2(lo2(e[q])) : 0.f;
-                    const float p1 = (kAll || ((validm >> (2 * q + 1)) & 1u)) ? ex2(hi2(e[q])) : 0.f;
-                    lsum[q] = fma2(pk2(p0, p1), iev2, lsum[q]);
-                    const __half2 r = __floats2half2_rn(p0, p1);
-                    ph[q] = *reinterpret_cast<const uint32_t*>(&r);
-                }
-            };
-            if (all_rows)
-                make_p(std::true_type{});
-            else
-                make_p(std::false_type{});
+            for (int q = 0; q < kGroupRows / 2; ++q) {
+                const float p0 = ex2(lo2(e[q])), p1 = ex2(hi2(e[q]));
+                lsum[q] = fma2(pk2(p0, p1), iev2, lsum[q]);
+                const __half2 r = __floats2half2_rn(p0, p1);
+                ph[q] = *reinterpret_cast<const uint32_t*>(&r);
+            }
             // (passes before the first product: the phase before the barrier's first)
             alive = alive & ctx.wait_warp(&sm.pfree, (t - 1) & 1);
             uint8_t* pbuf = smem + C::kOffP;
