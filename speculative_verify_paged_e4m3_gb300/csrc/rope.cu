@@ -14,7 +14,8 @@
 // (two 8-byte pieces), interleaved 8 in a row; lanes past the rotated part pass 8 elements through.
 // Bound by HBM for many tokens, by latency for few: 24571 tokens of 24 + 4 heads in bf16, 112 us, 6.3 TB/s
 // (93 % of the copy rate); with the cache write 16381 tokens of 24 + 4 + 4 heads, 87 us, 5.8 TB/s; 8 tokens
-// of one rank 2.2 us.
+// of one rank 2.2 us. With norms 24571 tokens 149 us, 4.7 TB/s: the sum of a row's squares is five exchanges
+// between its loads and its stores, of up to four rows at a time; into the 4-bit cache 16381 tokens 129 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -36,7 +37,8 @@ enum class To { kRows, kE4m3, kMx4 };
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 5;  // registers cut to fit: 24571 tokens 121 us with 4, 112 with 5, 114 with 6
-constexpr int kCtasMore = 4;   // with norms, or into the 4-bit cache: they do not fit 48 registers
+// With norms, or into the 4-bit cache: 24571 normed tokens 161 us with 3, 149 with 4, 178 with 5 (spills).
+constexpr int kCtasMore = 4;
 template <To kTo, bool kNorm>
 constexpr int ctas_per_sm() {
     return kNorm || kTo == To::kMx4 ? kCtasMore : kCtasPerSm;
@@ -48,9 +50,11 @@ constexpr int kRows = 4;       // rows of a token that a warp has in flight
 // 3.8 / 4.6, 16000 tokens 21.9 / 20.7 / 17.5 and 30.9 / 27.1 / 26.1.
 constexpr int64_t kTokensOne = 760, kTokensTwo = 4560;
 constexpr int64_t kMaxTokens = 0x7FFFFFFF;  // CTAs of a launch
-// Tokens from which V goes to the 4-bit cache by groups of 64, and up to which its CTAs and the tokens' are
-// launched together (256 heads: 5 CTAs a token).
-constexpr int64_t kVGroupFrom = 1024, kVGroupTo = 1 << 28;
+// Rows of V (tokens x KV heads) from which they go to the 4-bit cache by groups of 64 tokens, and tokens up to
+// which its CTAs and the tokens' are launched together (256 heads: 5 CTAs a token). With norms, us by groups
+// and row by row: 24 + 4 heads 256 tokens 5.7 and 5.7, 512 tokens 6.7 and 8.2, 16381 tokens 129 and 141;
+// 6 + 1 heads 1024 tokens 5.7 and 5.2, 1536 tokens 6.4 and 7.2, 16381 tokens 38 and 42.
+constexpr int64_t kVGroupFrom = 1536, kVGroupTo = 1 << 28;
 
 struct RopeParams {
     const void *q, *k, *v;
@@ -727,7 +731,7 @@ int write(const dflash_rope_plan_t* plan, const dflash_head_norm* norm, int64_t 
     p.num_kv_heads = pr.num_kv_heads;
     p.rotary_dim = pr.rotary_dim;
     p.amplitude = plan->amplitude;
-    if (!kScaled && num_tokens >= kVGroupFrom && num_tokens <= kVGroupTo)
+    if (!kScaled && num_tokens * pr.num_kv_heads >= kVGroupFrom && num_tokens <= kVGroupTo)
         p.v_ctas = (num_tokens + kVGroup - 1) / kVGroup * pr.num_kv_heads;
     return launch<kTo>(plan, p, norm, cuda_stream);
 }
