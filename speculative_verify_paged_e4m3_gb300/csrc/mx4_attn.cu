@@ -98,7 +98,7 @@ struct Info {
 };
 
 struct Small {
-    uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
+    uint64_t full[kStages], empty[kStages];  // of codes
     uint64_t infofull[kInfos], infofree[kInfos];
     uint64_t kafull[2], kafree[2], vafull[2], vafree[2];  // halves of the operands in tensor memory
     uint64_t sfull[2], sfree[2], pfull, pfree, odone, qready;
@@ -307,7 +307,6 @@ __device__ __forceinline__ void copy_tiles(const PartialParams& p, const Ctx& ct
     const int c = lane & (kChunks - 1);
     const uint8_t* pool = is_v ? p.v_pool : p.k_pool;
     const uint32_t ring = smem_u32((is_v ? v_ring : k_ring) + c * kChunkBytes);
-    uint64_t* const full = is_v ? sm.vfull : sm.kfull;
     int64_t next = ahead(0), now = -1;
     bool dep_done = false;
     int t = 0;
@@ -320,7 +319,7 @@ __device__ __forceinline__ void copy_tiles(const PartialParams& p, const Ctx& ct
         }
         const int s = ring_at.i;
         const uint32_t parity = ring_at.parity ^ 1;
-        if (!ctx.wait_warp(&sm.kempty[s], parity) || !ctx.wait_warp(&sm.vempty[s], parity)) break;
+        if (!ctx.wait_warp(&sm.empty[s], parity)) break;
         // keys from `drafted` on may be written by the kernel just before this one
         if (!dep_done && start + (t + 1) * kTile > drafted) {
             griddep_wait();
@@ -328,22 +327,19 @@ __device__ __forceinline__ void copy_tiles(const PartialParams& p, const Ctx& ct
         }
         const int64_t chunk = __shfl_sync(0xffffffffu, now, (t & 3) * kChunks + c);
         const int n = min(kChunks, (end - start - t * kTile + kTokens - 1) / kTokens);
-        if (lane < 2)
-            mbar_arrive_expect_tx(smem_u32(lane ? &sm.vfull[s] : &sm.kfull[s]), n * kChunkBytes);
+        if (lane == 0) mbar_arrive_expect_tx(smem_u32(&sm.full[s]), 2 * n * kChunkBytes);
         __syncwarp();
         if (lane < 2 * kChunks && c < n)
             copy_chunk(ring + s * kStageBytes, pool + (chunk * p.num_kv_heads + h) * kChunkBytes,
-                       smem_u32(&full[s]), policy);
+                       smem_u32(&sm.full[s]), policy);
     }
     if (clamped) atomicOr(p.status, DFLASH_FLAG_PAGE_CLAMPED);
     // no copy may still be writing shared memory when the CTA retires
     __syncwarp();
     if (lane == 0)
 #pragma unroll 1
-        for (int u = t - kStages < 0 ? 0 : t - kStages; u < t; ++u) {
-            mbar_wait(smem_u32(&sm.kfull[u % kStages]), (u / kStages) & 1, &sm.never, kWaitLimitNs);
-            mbar_wait(smem_u32(&sm.vfull[u % kStages]), (u / kStages) & 1, &sm.never, kWaitLimitNs);
-        }
+        for (int u = t - kStages < 0 ? 0 : t - kStages; u < t; ++u)
+            mbar_wait(smem_u32(&sm.full[u % kStages]), (u / kStages) & 1, &sm.never, kWaitLimitNs);
 }
 
 template <int RP>
@@ -378,10 +374,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     const Ctx ctx{&sm, p.status};
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(smem_u32(&sm.kfull[i]), 1);
-            mbar_init(smem_u32(&sm.vfull[i]), 1);
-            mbar_init(smem_u32(&sm.kempty[i]), 5);  // four decoders and the factors' warp
-            mbar_init(smem_u32(&sm.vempty[i]), 5);
+            mbar_init(smem_u32(&sm.full[i]), 1);
+            mbar_init(smem_u32(&sm.empty[i]), 9);  // eight decoders and the factors' warp
         }
         for (int i = 0; i < kInfos; ++i) {
             mbar_init(smem_u32(&sm.infofull[i]), 1);
@@ -392,7 +386,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
             mbar_init(smem_u32(&sm.kafree[i]), 1);
             mbar_init(smem_u32(&sm.vafull[i]), 4);
             mbar_init(smem_u32(&sm.vafree[i]), 1);
-            mbar_init(smem_u32(&sm.sfull[i]), 1);
+            mbar_init(smem_u32(&sm.sfull[i]), 2);  // the products, and the tile's factors
             mbar_init(smem_u32(&sm.sfree[i]), C::kSoftWarps);
         }
         mbar_init(smem_u32(&sm.pfull), C::kSoftWarps);
@@ -442,6 +436,9 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                     mma_commit(smem_u32(&sm.kafree[hd]));
                 }
                 mma_commit(smem_u32(&sm.sfull[kS]));
+                // the softmax reads the factors of a tile's keys with its scores: one wait for both
+                ok = ctx.wait(&sm.infofull[t % kInfos], (t / kInfos) & 1);
+                if (ok) mbar_arrive(smem_u32(&sm.sfull[kS]));
             };
 #pragma unroll 1
             for (int t = 0; ok && t < ntiles; ++t) tile(t & 1, t);
@@ -476,7 +473,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         for (int t = 0; t < ntiles; ++t, ring.next(), iring.next()) {
             const int s = ring.i, is = iring.i;
             if (!ctx.wait_warp(&sm.infofree[is], iring.parity ^ 1) ||
-                !ctx.wait_warp(&sm.kfull[s], ring.parity) || !ctx.wait_warp(&sm.vfull[s], ring.parity))
+                !ctx.wait_warp(&sm.full[s], ring.parity))
                 break;
             Info& info = infos[is];
 #pragma unroll 1
@@ -502,8 +499,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
             }
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(smem_u32(&sm.kempty[s]));
-                mbar_arrive(smem_u32(&sm.vempty[s]));
+                mbar_arrive(smem_u32(&sm.empty[s]));
                 mbar_arrive(smem_u32(&sm.infofull[is]));
             }
         }
@@ -516,7 +512,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
 #pragma unroll 1
         for (int t = 0; t < ntiles; ++t, ring.next()) {
             const int s = ring.i;
-            if (!ctx.wait_warp(&sm.kfull[s], ring.parity)) break;
+            if (!ctx.wait_warp(&sm.full[s], ring.parity)) break;
             const uint8_t* stage = smem + C::kOffK + s * kStageBytes;
             const uint2 sc = *reinterpret_cast<const uint2*>(stage + scales);
             const int top = largest_byte(sc) - kFactorTop;
@@ -547,7 +543,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                 warp_arrive_tmem(&sm.kafull[hd]);
             }
             if (!ok) break;
-            warp_arrive(&sm.kempty[s]);
+            warp_arrive(&sm.empty[s]);
         }
     } else if (warp < kSoftWarp) {
         // ---------------------------------------------------------------- V: lane = element (and + 128)
@@ -557,9 +553,8 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
 #pragma unroll 1
         for (int t = 0; t < ntiles; ++t, ring.next(), iring.next()) {
             const int s = ring.i, is = iring.i;
-            if (!ctx.wait_warp(&sm.vfull[s], ring.parity) ||
-                !ctx.wait_warp(&sm.infofull[is], iring.parity))
-                break;
+            // the factors' warp has waited for the codes
+            if (!ctx.wait_warp(&sm.infofull[is], iring.parity)) break;
             const uint8_t* stage = smem + C::kOffV + s * kStageBytes + e * kTokens;
             const uint32_t* f = infos[is].f[quad];
             bool ok = true;
@@ -586,7 +581,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                 warp_arrive_tmem(&sm.vafull[hv]);
             }
             if (!ok) break;
-            warp_arrive(&sm.vempty[s]);
+            warp_arrive(&sm.empty[s]);
             warp_arrive(&sm.infofree[is]);
         }
     } else {
@@ -641,10 +636,9 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
 #pragma unroll 1
         for (int t = 0; t < ntiles; ++t) {
             const int tile0 = start + t * kTile, j = tile0 + st, is = t % kInfos;
-            alive = alive & ctx.wait_warp(&sm.infofull[is], (t / kInfos) & 1);
+            alive = alive & ctx.wait_warp(&sm.sfull[t & 1], (t >> 1) & 1);
             const float2 cev = infos[is].c[st];
             const float c = cev.x, ev = cev.y;
-            alive = alive & ctx.wait_warp(&sm.sfull[t & 1], (t >> 1) & 1);
             tc_fence_after();
             auto scores = [&](uint64_t (&y)[kGroupRows / 2]) {
                 uint32_t a[16];
