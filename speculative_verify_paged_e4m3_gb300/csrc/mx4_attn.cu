@@ -25,13 +25,13 @@
 //  * Every wait on another warp or on a copy is bounded: on a timeout the CTA sets
 //    DFLASH_FLAG_KERNEL_TIMEOUT, drains its copies and returns.
 //
-// Measured with the combine, in a graph: 24/4 heads, 8 drafted tokens over 261888 tokens 89 us, 47 % of the copy
-// rate; 32 sequences of one token up to 65536 long, 24/4 heads, 131 us, 45 %; one rank, 8 tokens over 262144
-// tokens 31.5 us. What bounds it is the warps: 8500 warp instructions a tile for 48 rows in 3400 clocks, 6100
-// for 16 in 2650, 67 and 60 % of the issue slots, with no role ahead of the others by more than a
+// Measured with the combine, in a graph: 24/4 heads, 8 drafted tokens over 261888 tokens 84 us, 50 % of the copy
+// rate; 32 sequences of one token up to 16384 long, 24/4 heads, 105 us, 56 %; one rank, 8 tokens over 261888
+// tokens 30.6 us. What bounds it is the warps: 7750 warp instructions a tile for 48 rows in 3150 clocks, 5380
+// for 16 in 2450, 68 and 60 % of the issue slots, with no role ahead of the others by more than a
 // few hundred clocks. They share the instruction caches, so that fewer instructions in a loop count
 // for more than their number, and unrolling costs: hence the rolled loops (two chunks of V at a time 104 us
-// for 99, two blocks of K 140 for 135 us of the single tokens).
+// for 99, two blocks of K 135 for 130 us of the single tokens).
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -411,10 +411,10 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     } else if (warp == 1 || warp == 2) {
         // ---------------------------------------------------------------- products
         // One thread issues the scores, another the output: a product takes its thread some 50 clocks, the
-        // tensor core half of that (N 48: 24 with two threads, 46 with one), a commit or a wait 50 to 80. Each
-        // product's addresses are a base and a constant: worked out from the indices they took 145
-        // clocks a product. Both operands come in halves (of the head dim, of the keys), so that
-        // one is decoded while the other is read.
+        // tensor core half of that for the scores (N 48: 24 with two threads, 46 with one) and as long for
+        // the output (N 96), a commit or a wait 50 to 80. Each product's addresses are a base and a constant:
+        // worked out from the indices they took 145 clocks a product. Both operands come in halves (of the
+        // head dim, of the keys), so that one is decoded while the other is read.
         const bool issuer = elect_one();
         bool ok = issuer && ctx.wait(&sm.qready, 0);
         if (warp == 1 && issuer) {
@@ -833,6 +833,8 @@ cudaError_t launch_rp(const PartialParams& p, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, mx4_partial_kernel<RP>, p);
 }
 
+constexpr int kTwoRoundsFrom = 8192;  // tokens
+
 int rows_pad(int rows) { return (rows + kGroupRows - 1) / kGroupRows * kGroupRows; }
 
 cudaError_t launch_partial(const PartialParams& p, cudaStream_t stream) {
@@ -872,6 +874,19 @@ int dflash_mx4_attn_plan(const dflash_verify_attn_problem* problem,
     const int rc = dflash_verify_attn_plan(&pr, plan);
     if (rc != DFLASH_OK) return rc;
     plan->kernel = DFLASH_KERNEL_MX4;
+    // A batch has an SM's worth of slots, shared out by length. With more than half as many units (of whole
+    // slots) that leaves SMs idle behind the longest ones; of long contexts two rounds of slots
+    // cost less. Ragged batches of 24/4 heads, one token each, us with 152 and 304 slots: up to 16384 tokens
+    // 64 units 61 and 65, 80 units 77 and 72, 128 units 124 and 106, 144 units 143 and 115; up to
+    // 4096 tokens 80 units 29 and 34, 128 units 42 and 43.
+    const int64_t units = (int64_t)pr.batch * pr.num_kv_heads * plan->row_blocks;
+    if (pr.batch > 1 && pr.num_splits == 0 && 2 * units > plan->sm_count && units <= plan->sm_count &&
+        pr.max_context >= mx4::kTwoRoundsFrom) {
+        plan->num_slots = 2 * plan->sm_count / plan->row_blocks;
+        const size_t rows = (size_t)plan->num_slots * plan->rows;
+        plan->ws_acc_offset = plan->ws_state_offset + (rows * sizeof(float2) + 255) / 256 * 256;
+        plan->workspace_bytes = plan->ws_acc_offset + rows * kHeadDim * sizeof(float);
+    }
     const int block_rows = (plan->rows + plan->row_blocks - 1) / plan->row_blocks;
     switch (mx4::rows_pad(block_rows)) {
         case 16:

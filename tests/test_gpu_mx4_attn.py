@@ -120,6 +120,21 @@ def test_forced_splits(splits):
     check(make(pr, num_splits=splits)(*dev(pr)), pr)
 
 
+@pytest.mark.parametrize("heads,q_len", [((12, 2), 1), ((4, 2), 30)])
+def test_a_long_batch_with_many_units(heads, q_len):
+    """More units than half the SMs and room for long contexts: two rounds of slots."""
+    rng = np.random.default_rng(q_len)
+    lens = rng.integers(0, 400, 41 if q_len == 1 else 20)
+    lens[[3, 11]] = 9000, 4099
+    lens[5] = 0
+    pr = problem(41, lens, q_len, *heads, 64)
+    att = make(pr)
+    units = len(lens) * heads[1] * att.plan.row_blocks
+    assert 2 * units > att.plan.sm_count >= units
+    assert att.plan.num_slots == 2 * att.plan.sm_count // att.plan.row_blocks
+    check(att(*dev(pr)), pr)
+
+
 @pytest.mark.parametrize("gain,strong", [(4.0, 0.0), (2.0, 4.0), (0.01, 0.0)])
 def test_peaked_and_flat_scores(gain, strong):
     pr = problem(11, [3000, 513], 8, 6, 1, 16, gain, strong)
