@@ -377,3 +377,48 @@ def test_pools_past_32_bit_offsets():
         want = M.numbers(*M.quantise(x.double().cpu().numpy()))
         assert np.array_equal(got.double().cpu().numpy(), want)
     assert not kp[:8].any() and r.read_flags() == 0 and cache.read_flags() == 0
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("T,Hq,Hkv", [(1535, 20, 4), (4099, 24, 4), (1024, 7, 2)])
+def test_many_tokens_of_many_heads(T, Hq, Hkv, dtype, layout):
+    """Held to the formula, and bit for bit to calls of few tokens: each destination, in place, with padding and
+    slots past the pool."""
+    from speculative_verify_paged_e4m3_gb300 import binding as B
+    test_norm_rope_apply(T, Hq, Hkv, dtype, layout)
+    P, pages = 16, -(-T // 16) + 3
+    q, k, v, pos, qw, kw = make(T + 2, T, Hq, Hkv, dtype, fused=True)
+    norm = B.HeadNorm(qw, kw, 1e-5, 0.5)
+    r = B.Rotary(Hq, Hkv, D, 64, layout=layout, dtype=dtype, page_size=P, num_pages=pages)
+    rng = np.random.default_rng(T)
+    slots = rng.permutation(pages * P)[:T]
+    slots[[0, 9, 600, T - 1]] = -1
+    slots[1000] = pages * P
+    slots = torch.from_numpy(slots).cuda()
+    starts = torch.tensor([0, 17], dtype=torch.int32, device="cuda")  # tokens 0 and 9 are not padding
+    scales = [torch.tensor([x], device="cuda") for x in (0.02, 0.03)]
+    cache = B.Mx4Cache(Hkv, D, P, pages)
+
+    def run(step, in_place):
+        e = [torch.full((pages, P, Hkv, D), 7, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        m = cache.empty()
+        outs = [x.clone() if in_place else torch.full_like(x, 9.0) for x in (q, k, q, q)]
+        for a in range(0, T, step):
+            b = min(a + step, T)
+            live = torch.clamp(starts - a, min=0)
+            src = outs if in_place else (q, k, q, q)
+            r.apply(src[0][a:b], src[1][a:b], pos[a:b], q_out=outs[0][a:b], k_out=outs[1][a:b], norm=norm)
+            r.kv_write(src[2][a:b], k[a:b], v[a:b], pos[a:b], slots[a:b], *scales, *e, q_out=outs[2][a:b],
+                       norm=norm, token_starts=live)
+            r.mx4_write(src[3][a:b], k[a:b], v[a:b], pos[a:b], slots[a:b], *m, q_out=outs[3][a:b],
+                        norm=norm, token_starts=live)
+        return outs + e + list(m)
+    few, many, there = run(300, False), run(T, False), run(T, True)
+    for i, (a, b) in enumerate(zip(few, many)):
+        assert torch.equal(a, b), i
+    padding = (slots < 0).cpu().numpy() & (np.arange(T) >= 17)
+    for i, (a, b) in enumerate(zip(many, there)):
+        keep = torch.from_numpy(~padding).cuda() if i in (2, 3) else slice(None)
+        assert torch.equal(a[keep], b[keep]), i
+    assert r.read_flags() == B.DFLASH_FLAG_SLOT_RANGE
