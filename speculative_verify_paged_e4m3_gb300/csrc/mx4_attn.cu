@@ -35,8 +35,6 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
-#include <type_traits>
-
 #include "common.cuh"
 #include "dflash_mx4_cache.h"
 #include "mx4.cuh"
