@@ -80,8 +80,10 @@ int dflash_mx4_read(int32_t num_kv_heads, int32_t head_dim, int32_t page_size, i
  * DFLASH_PROBLEM_PDL is taken, DFLASH_PROBLEM_FUSED_COMBINE is not (DFLASH_ERR_UNSUPPORTED).
  * Buffers, alignments and workspace as for dflash_verify_attn_forward.
  *
- * Q stays FP16, K and V are exact in FP16 up to the limits below, probabilities are FP16 with a step
- * of 2^-32 of a row's largest at most, all sums FP32. A key whose K or V has a NaN scale makes NaN of
+ * Q stays FP16, K and V are exact in FP16 up to the limits below, all sums are FP32. The output's weights
+ * are FP16: a probability times the largest power among its key's blocks of V, rounded by 2^-11 of
+ * itself or 2^-33 of the row's largest such product, whichever is more (so a key whose V is 2^20 times
+ * the others' in one block costs the others' weights precision in all blocks; lse is not affected). A key whose K or V has a NaN scale makes NaN of
  * every row that sees it, in out and lse, and of no other; so does a row of q with a NaN or an
  * infinity of itself, if it sees a key. Codes at or past a length are never used, whatever they hold.
  * Of a key's blocks, one whose scale is more than 2^26 below the key's largest counts as zeros; so do

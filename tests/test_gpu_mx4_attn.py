@@ -374,3 +374,13 @@ def test_refusals():
         make(pr, flags=B.DFLASH_PROBLEM_FUSED_COMBINE)
     with pytest.raises(B.DflashError):
         att(q, k, v, table, lens, out=q)
+
+
+@pytest.mark.parametrize("power", [6, 14])
+def test_a_key_whose_value_is_far_larger_in_one_block(power):
+    """Its power stands before its probability: the other keys' weights keep a step of 2^-33 of the largest product of
+    both, which the tolerance's last term has as vmax; lse does not know of it."""
+    pr = problem(20, [900, 257], 8, 6, 1, 16)
+    for b, j in ((0, 300), (1, 10)):
+        set_scale(pr, "v", b, j, 0, 3, 127 + power)
+    check(make(pr)(*dev(pr)), pr)
