@@ -23,7 +23,7 @@
 //    output, 3 works out the factors of a tile's keys, 4-7 decode K, 8-11 V, the others are the softmax, four
 //    for 16 rows.
 //  * Every wait on another warp or on a copy is bounded: on a timeout the CTA sets
-//    DFLASH_FLAG_KERNEL_TIMEOUT, drains its copies and returns.
+//    DFLASH_FLAG_KERNEL_TIMEOUT, sees its copies and products through (bounded too) and returns.
 //
 // Measured with the combine, in a graph: 24/4 heads, 8 drafted tokens over 261888 tokens 84 us, 50 % of the copy
 // rate; 32 sequences of one token up to 16384 long, 24/4 heads, 105 us, 56 %; one rank, 8 tokens over 261888
@@ -805,6 +805,9 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
+        // (of a CTA that gave up products may still be on their way: no wait above saw them through)
+        mbar_wait(smem_u32(&sm.odone), 0, &sm.never, kWaitLimitNs);
+        __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, C::kTmemCols);
     }
