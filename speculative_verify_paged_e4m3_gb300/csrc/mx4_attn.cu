@@ -208,10 +208,12 @@ struct Ctx {
         const uint32_t addr = smem_u32(bar);
         return try_wait_hint(addr, parity) || wait_on(addr, parity, &sm->abort, status);
     }
-    // by a whole warp, whose lanes agree on the result
+    // by a whole warp, whose lanes agree on the result. What follows (tcgen05.ld and st, group barriers) wants
+    // them together: a first try may succeed for some lanes only, and the vote alone does not promise it.
     __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) const {
-        const bool ok = wait(bar, parity);
-        return __all_sync(0xffffffffu, ok);
+        const bool ok = __all_sync(0xffffffffu, wait(bar, parity));
+        __syncwarp();
+        return ok;
     }
     __device__ bool aborted() const { return *reinterpret_cast<volatile int*>(&sm->abort) != 0; }
 };
@@ -246,6 +248,7 @@ __device__ __forceinline__ void warp_arrive_tmem(uint64_t* bar) {
 // the launch has failed), so each barrier is reached by all of them.
 __device__ __forceinline__ bool group_vote(int g, bool v) {
     uint32_t r;
+    __syncwarp();  // (lanes may come from a branch of their own)
     asm volatile(
         "{\n\t.reg .pred pv, pr;\n\t"
         "setp.ne.u32 pv, %1, 0;\n\t"
@@ -257,6 +260,7 @@ __device__ __forceinline__ bool group_vote(int g, bool v) {
     return r != 0;
 }
 __device__ __forceinline__ void group_bar(int g) {
+    __syncwarp();
     asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
 }
 
@@ -462,6 +466,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
             }
         }
         if (issuer) mma_commit(smem_u32(&sm.odone));  // tracks every product this thread issued
+        __syncwarp();
     } else if (warp == 3) {
         // ---------------------------------------------------------------- factors of a tile's keys
         constexpr float kScore = 0.0625f * kLog2e / (1 << kFactorTop);  // D^-1/2 = 1/16

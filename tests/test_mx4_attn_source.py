@@ -20,3 +20,25 @@ def test_products_are_through_before_tensor_memory_is_given_back():
     assert s.count("if (issuer) mma_commit(smem_u32(&sm.odone));") == 1
     assert "mbar_init(smem_u32(&sm.odone), 2)" in s
     assert not re.search(r"never\s*=\s*[^0;]", s.replace("sm.abort = sm.never = 0", ""))
+
+
+def body(s, head):
+    """The text of the braces that follow `head`."""
+    at = s.index("{", s.index(head))
+    depth = 0
+    for i in range(at, len(s)):
+        depth += {"{": 1, "}": -1}.get(s[i], 0)
+        if not depth:
+            return s[at:i]
+    raise AssertionError(head)
+
+
+def test_lanes_are_together_where_instructions_want_a_whole_warp():
+    """A wait's first try may succeed for some lanes of a warp only, and masks differ between lanes: tensor-memory
+    loads and stores and the groups' barriers come behind a __syncwarp()."""
+    s = source()
+    assert re.search(r"__all_sync\(.*?\);\s*__syncwarp\(\);", body(s, "bool wait_warp("), re.S)
+    for head in ("bool group_vote(", "void group_bar("):
+        b = body(s, head)
+        assert b.index("__syncwarp()") < b.index("asm volatile")
+    assert re.search(r"__syncwarp\(\);\s*tc_fence_after\(\);\s*tmem_dealloc\(", s)
