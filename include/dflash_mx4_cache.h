@@ -87,7 +87,8 @@ int dflash_mx4_read(int32_t num_kv_heads, int32_t head_dim, int32_t page_size, i
  * every row that sees it, in out and lse, and of no other; so does a row of q with a NaN or an
  * infinity of itself, if it sees a key. Codes at or past a length are never used, whatever they hold.
  * Of a key's blocks, one whose scale is more than 2^26 below the key's largest counts as zeros; so do
- * V's below 2^-66. V's scales above 2^41 count as 2^41.
+ * V's below 2^-66. V's scales above 2^41 count as 2^41. A key whose largest scale of K is above 2^100 counts
+ * with that one at 2^100 and its others as far below it as they are.
  */
 int dflash_mx4_attn_plan(const dflash_verify_attn_problem* problem,
                          dflash_verify_attn_plan_t* plan);

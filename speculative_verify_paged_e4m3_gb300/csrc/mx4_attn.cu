@@ -67,6 +67,9 @@ constexpr float kShift = 8.f;          // probabilities are 2^8 at the reference
 constexpr float kLazyThreshold = 15.f; // largest exponent of one
 constexpr int kFactorTop = 12;         // a key's largest block is brought to 2^12
 constexpr int kMaxEv = 40;
+// Largest scale byte of a key of K, 2^100: a score is below 2^38.6 (256 products of 65504 and 6 2^12) times the
+// factor 2^84.6, so that it stays a number. An infinite one could not be told from that of a key not seen.
+constexpr int kMaxKe = 127 + 100;
 constexpr int kKWarp = 4, kVWarp = 8, kSoftWarp = 12;
 
 // Shared memory: Q | P | codes of K | codes of V | factors | Small. Tensor memory: K [two head-dim
@@ -487,7 +490,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                 const uint2 vs = *reinterpret_cast<const uint2*>(smem + C::kOffV + s * kStageBytes + at);
                 const int ke = largest_byte(ks), ve = largest_byte(vs);
                 const int ev = max(-kMaxEv, min(kMaxEv, ve - 127));
-                info.c[key] = make_float2(ke == kNanScale ? NAN : __int_as_float(ke << 23) * kScore,
+                info.c[key] = make_float2(ke == kNanScale ? NAN : __int_as_float(min(ke, kMaxKe) << 23) * kScore,
                                           ve == kNanScale ? NAN : (float)ev);
                 // block j's factor is 2^(s - 127 - ev + 12), at most 2^13 (finite for a NaN block and for
                 // whatever lies past the split's end: those weights are NaN and 0), and 0 for blocks
