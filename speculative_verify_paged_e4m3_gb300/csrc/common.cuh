@@ -112,6 +112,12 @@ __device__ __forceinline__ void griddep_launch_dependents() {
 // without the programmatic attribute. The wait ends because that grid's CTAs are all resident
 // or done by the time this grid starts.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// For a CTA that needs nothing of the grid before it. Who waits for this grid must find that one complete
+// too (its outputs may be written again): the grid's last CTA stays until it is. (Every CTA doing so would
+// hold its SM for nothing.)
+__device__ __forceinline__ void griddep_end() {
+    if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1) griddep_wait();
+}
 
 // Context length of sequence b as the kernels see it: clamped into [0, max_context].
 __device__ __forceinline__ int clamped_context(const int32_t* context_lens, int b, int max_context,

@@ -366,10 +366,12 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                                     p.num_slots, p.max_context, p.q_len, slot, true);
     if (slot == 0 && tid == 0 && us.flags) atomicOr(p.status, us.flags);
     const int b = us.b, h = us.h, split = slot - us.first, n = us.n;
-    if (b < 0) return;
-    const int per = keys_per_split(n, us.count, kTile, p.min_split_keys);
+    const int per = b < 0 ? 1 : keys_per_split(n, us.count, kTile, p.min_split_keys);
     const int start = split * per;
-    if (start >= n) return;  // idle slot: the combine never reads it
+    if (b < 0 || start >= n) {  // idle slot: the combine never reads it
+        griddep_end();
+        return;
+    }
     const int end = min(n, start + per);
     const int ntiles = (end - start + kTile - 1) / kTile;
     if (smem_u32(smem) & 1023u) {  // the swizzled layouts need a 1 KB aligned base

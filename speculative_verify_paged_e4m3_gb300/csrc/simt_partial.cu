@@ -58,10 +58,12 @@ __global__ void __launch_bounds__(kSimtThreads, 1) simt_partial_kernel(PartialPa
                                       p.num_slots, p.max_context, p.q_len, slot, true);
     if (slot == 0 && tid == 0 && us.flags) atomicOr(p.status, us.flags);
     const int b = us.b, h = us.h, split = slot - us.first, n = us.n;
-    if (b < 0) return;
-    const int per = keys_per_split(n, us.count, p.tile_keys, p.min_split_keys);
+    const int per = b < 0 ? 1 : keys_per_split(n, us.count, p.tile_keys, p.min_split_keys);
     const int start = split * per;
-    if (start >= n) return;  // idle slot: the combine never reads it
+    if (b < 0 || start >= n) {  // idle slot: the combine never reads it
+        griddep_end();
+        return;
+    }
     const int end = min(n, start + per);
     // Q, the scales, the pages and the workspace only after the preceding kernel has completed
     // (a no-op unless this grid is its programmatic dependent)
