@@ -279,7 +279,7 @@ typedef struct {
     int32_t page_size;         /* a multiple of 16 */
     int32_t max_pages_per_seq; /* block-table row stride; >= ceil(max_context / page_size) */
     int32_t num_pages;
-    int32_t max_context;       /* largest N any call sees */
+    int32_t max_context;       /* largest N any call sees, 1 .. 2^30 */
     int32_t max_prefix;        /* largest *prefix_len, 0 .. max_context */
     int32_t device;            /* CUDA ordinal whose SM count sizes the plan; < 0: 152 SMs */
     int32_t kernel;            /* DFLASH_PREFIX_KERNEL_* of the prefix part */

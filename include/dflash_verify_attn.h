@@ -113,7 +113,7 @@ typedef struct {
     int32_t page_size;         /* tokens per page; a multiple of 16 */
     int32_t max_pages_per_seq; /* block-table row stride; >= ceil(max_context / page_size) */
     int32_t num_pages;         /* pages in each pool (bounds for block-table entries) */
-    int32_t max_context;       /* largest N any call of this plan sees, >= 1 */
+    int32_t max_context;       /* largest N any call of this plan sees, 1 .. 2^30 */
     int32_t device;            /* CUDA ordinal whose SM count sizes the plan */
     int32_t num_splits;        /* 0: planner's choice; > 0 forces the split count */
     int32_t kernel;            /* DFLASH_KERNEL_*; AUTO picks the fastest supported */

@@ -38,6 +38,10 @@ using namespace dflash;
 namespace {
 
 constexpr int kDefaultSmCount = 152;  // GB300
+// Largest max_context. The kernels count keys in 32 bits and go past a context's end by up to a split for each
+// of 65535 splits (2^24 keys) and a few tiles: with contexts next to 2^31 such an index would wrap and look up
+// a page in front of the block table. (2^30 keys of one KV head are more than the GPU's memory holds.)
+constexpr int kMaxContext = 1 << 30;
 constexpr size_t kHeaderBytes = 256;
 constexpr size_t kGridBarrierOffset = 8;  // 64-bit ticket counter of the fused merge's barrier
 
@@ -191,7 +195,7 @@ int dflash_verify_attn_plan(const dflash_verify_attn_problem* pr,
     if (pr->kernel < DFLASH_KERNEL_AUTO || pr->kernel > DFLASH_KERNEL_TCGEN05)
         return DFLASH_ERR_INVALID_ARGUMENT;
     if (pr->head_dim != kHeadDim) return DFLASH_ERR_UNSUPPORTED;
-    if (pr->page_size % 16 != 0) return DFLASH_ERR_UNSUPPORTED;
+    if (pr->page_size % 16 != 0 || pr->max_context > kMaxContext) return DFLASH_ERR_UNSUPPORTED;
     const int group = pr->num_q_heads / pr->num_kv_heads;
     const int64_t rows = (int64_t)pr->q_len * group;
     if (rows > kMaxRows) return DFLASH_ERR_UNSUPPORTED;
