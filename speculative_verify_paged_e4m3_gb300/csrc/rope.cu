@@ -52,9 +52,16 @@ constexpr int64_t kTokensOne = 760, kTokensTwo = 4560;
 constexpr int64_t kMaxTokens = 0x7FFFFFFF;  // CTAs of a launch
 // Rows of V (tokens x KV heads) from which they go to the 4-bit cache by groups of 64 tokens, and tokens up to
 // which its CTAs and the tokens' are launched together (256 heads: 5 CTAs a token). With norms, us by groups
-// and row by row: 24 + 4 heads 256 tokens 5.7 and 5.7, 512 tokens 6.7 and 8.2, 16381 tokens 129 and 141;
-// 6 + 1 heads 1024 tokens 5.7 and 5.2, 1536 tokens 6.4 and 7.2, 16381 tokens 38 and 42.
-constexpr int64_t kVGroupFrom = 1536, kVGroupTo = 1 << 28;
+// and row by row, slots in runs of 1 (single tokens of as many sequences), of 8 (drafted blocks), in one run
+// (a prompt); 24 + 4 heads, then 6 + 1 heads:
+//   rows    runs of 1    of 8         one run        runs of 1    of 8         one run
+//   1536    7.7   6.3    7.7   7.2    6.2   7.2      7.7   7.2    8.2   7.2    6.2   7.2
+//   2048    8.4   7.7    8.7   8.2    6.7   8.2      8.7   7.8    8.2   7.7    7.1   7.7
+//   4096   10.8  11.8   10.8  12.1   10.3  12.3     12.7  13.3   12.3  12.8   11.8  12.8
+//   8192   19.5  21.1   19.3  21.0   17.4  20.6     21.8  23.6   21.5  22.6   19.5  22.6
+//  32768   86.8  80.2   73.8  75.0   65.4  73.7
+// (Single tokens of 8192 and more sequences lose 8 %: each token's 128 bytes are sectors of their own either way.)
+constexpr int64_t kVGroupFrom = 2048, kVGroupTo = 1 << 28;
 
 struct RopeParams {
     const void *q, *k, *v;
@@ -280,27 +287,34 @@ __device__ __forceinline__ void put_mx4_v(uint8_t* chunk, int tok, int lane, con
 
 // V of many tokens: a CTA takes 64 tokens of one head, has their codes in shared memory by words of four
 // tokens ([group of four][byte of the row]), and writes what is a whole chunk (16 slots in a row, as tokens of
-// a prompt have) in 16-byte pieces, the rest byte by byte. Row by row, a token's bytes are 128 stores of
+// a prompt have) in 16-byte pieces, the other tokens byte by byte. Row by row, a token's bytes are 128 stores of
 // one, and the L2 takes a sector for each.
 constexpr int kVGroup = 64;
 template <typename T>
 __device__ __forceinline__ void put_v_group(const RopeParams& p, int64_t group, uint32_t* words,
-                                            int64_t* slots, uint64_t* masks) {
+                                            int64_t* places, uint64_t* masks) {
+    static_assert(mx4::kTokens == 16 && mx4::kChunkBytes % 16 == 0, "a token's place tells its chunk");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = (int)(group % p.num_kv_heads);
     const int64_t t0 = group / p.num_kv_heads * kVGroup;
     const int n = (int)min((int64_t)kVGroup, p.num_tokens - t0);
-    uint32_t* const bits = reinterpret_cast<uint32_t*>(masks);  // slots that end a run: starts, and none
+    // each token's first byte in the pool (-1: no slot), and as bits which have a slot, and which follow the
+    // token before them inside a chunk
+    uint32_t* const bits = reinterpret_cast<uint32_t*>(masks);
     if (tid < kVGroup) {
         auto slot_of = [&](int i) -> int64_t {
             const int64_t s = i >= 0 && i < n ? p.slots[t0 + i] : -1;
             return s < p.num_slots ? s : -1;
         };
         const int64_t s = slot_of(tid);
-        slots[tid] = s;
-        const bool start = s < 0 || s % mx4::kTokens == 0 || tid == 0 || slot_of(tid - 1) != s - 1;
-        const uint32_t m = __ballot_sync(0xffffffffu, start);
-        if (lane == 0) bits[warp] = m;
+        places[tid] = s < 0 ? -1 : mx4::chunk_offset(s, p.num_kv_heads, h) + s % mx4::kTokens;
+        const uint32_t has = __ballot_sync(0xffffffffu, s >= 0);
+        const uint32_t follows = __ballot_sync(
+            0xffffffffu, s >= 0 && s % mx4::kTokens != 0 && tid > 0 && slot_of(tid - 1) == s - 1);
+        if (lane == 0) {
+            bits[warp] = has;
+            bits[2 + warp] = follows;
+        }
     }
     __syncthreads();
     const T* v = static_cast<const T*>(p.v) + h * kHeadDim + 4 * lane;
@@ -322,10 +336,8 @@ __device__ __forceinline__ void put_v_group(const RopeParams& p, int64_t group, 
             unpack<T>(wb[i], b);
             const VCodes c = v_codes(a, b);
             u[i] = c.codes;
-            const int64_t s = slots[4 * tg + i];
-            if (s >= 0)
-                put_v_scales(p.v_pool + mx4::chunk_offset(s, p.num_kv_heads, h),
-                             (int)(s % mx4::kTokens), lane, c);
+            const int64_t at = places[4 * tg + i];
+            if (at >= 0) put_v_scales(p.v_pool + (at & ~15ll), (int)(at & 15), lane, c);
         }
         uint32_t w[4];  // four tokens' bytes of elements 4 lane + k
 #pragma unroll
@@ -336,31 +348,33 @@ __device__ __forceinline__ void put_v_group(const RopeParams& p, int64_t group, 
         *reinterpret_cast<uint4*>(words + tg * 128 + 4 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
     }
     __syncthreads();
-    // runs of slots inside a chunk, half of the CTA each; a thread has one byte of the row
-    const int e = tid & 127;
-    uint64_t left = masks[0];
-    for (int run = 0; left; ++run) {
-        const int i = __ffsll((long long)left) - 1;
-        left &= left - 1;
-        const int len = (left ? __ffsll((long long)left) - 1 : kVGroup) - i;
-        const int64_t s = slots[i];
-        if ((run & 1) != tid >> 7 || s < 0) continue;
-        uint8_t* dst = p.v_pool + mx4::chunk_offset(s, p.num_kv_heads, h) + e * mx4::kTokens +
-                       s % mx4::kTokens;
+    // a thread has one byte of the row; half of the CTA each second whole chunk, and half of the other tokens
+    const int e = tid & 127, half = tid >> 7;
+    uint64_t whole = masks[1] >> 1;  // first tokens of whole chunks: 15 that follow
+    whole &= whole >> 1;
+    whole &= whole >> 2;
+    whole &= whole >> 4;
+    whole &= whole >> 7;
+    uint64_t rest = masks[0];
+    for (int run = 0; whole; ++run, whole &= whole - 1) {
+        const int i = __ffsll((long long)whole) - 1;
+        rest &= ~(0xFFFFull << i);
+        if ((run & 1) != half) continue;
         const uint32_t* src = words + (i >> 2) * 128 + e;
         const int shift = 8 * (i & 3);
-        if (len == mx4::kTokens) {  // (i <= 47 if it is shifted: the fifth word is there)
-            uint32_t w[5];
+        uint32_t w[5];  // (i <= 47 if it is shifted: the fifth word is there)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = src[k * 128];
-            w[4] = shift ? src[4 * 128] : 0;
-            *reinterpret_cast<uint4*>(dst) =
-                make_uint4(__funnelshift_r(w[0], w[1], shift), __funnelshift_r(w[1], w[2], shift),
-                           __funnelshift_r(w[2], w[3], shift), __funnelshift_r(w[3], w[4], shift));
-        } else {
-            for (int k = 0; k < len; ++k)
-                dst[k] = (uint8_t)(words[((i + k) >> 2) * 128 + e] >> (8 * ((i + k) & 3)));
-        }
+        for (int k = 0; k < 4; ++k) w[k] = src[k * 128];
+        w[4] = shift ? src[4 * 128] : 0;
+        *reinterpret_cast<uint4*>(p.v_pool + places[i] + e * mx4::kTokens) =
+            make_uint4(__funnelshift_r(w[0], w[1], shift), __funnelshift_r(w[1], w[2], shift),
+                       __funnelshift_r(w[2], w[3], shift), __funnelshift_r(w[3], w[4], shift));
+    }
+    uint8_t* const pool = p.v_pool + e * mx4::kTokens;
+#pragma unroll 4
+    for (uint32_t left = (uint32_t)(rest >> (32 * half)); left; left &= left - 1) {
+        const int i = 32 * half + __ffs((int)left) - 1;
+        pool[places[i]] = (uint8_t)(words[(i >> 2) * 128 + e] >> (8 * (i & 3)));
     }
 }
 
@@ -438,10 +452,10 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<kTo, kNorm>())) rope_ke
     const int rows = rows_of<kTo>(p);
     int64_t t = blockIdx.x;
     if constexpr (kTo == To::kMx4) {
-        __shared__ int64_t v_slots[kVGroup];
-        __shared__ uint64_t v_masks;
+        __shared__ int64_t v_places[kVGroup];
+        __shared__ uint64_t v_masks[2];
         if (t < p.v_ctas) {
-            put_v_group<T>(p, t, reinterpret_cast<uint32_t*>(staged), v_slots, &v_masks);
+            put_v_group<T>(p, t, reinterpret_cast<uint32_t*>(staged), v_places, v_masks);
             return;
         }
         t -= p.v_ctas;
@@ -500,10 +514,10 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<kTo, kNorm>())) rope_to
     const int rows = rows_of<kTo>(p);
     int64_t block = blockIdx.x;
     if constexpr (kTo == To::kMx4) {
-        __shared__ int64_t v_slots[kVGroup];
-        __shared__ uint64_t v_masks;
+        __shared__ int64_t v_places[kVGroup];
+        __shared__ uint64_t v_masks[2];
         if (block < p.v_ctas) {
-            put_v_group<T>(p, block, reinterpret_cast<uint32_t*>(staged), v_slots, &v_masks);
+            put_v_group<T>(p, block, reinterpret_cast<uint32_t*>(staged), v_places, v_masks);
             return;
         }
         block -= p.v_ctas;
