@@ -57,7 +57,7 @@ int dflash_mx4_kv_write(const dflash_rope_plan_t* plan, const dflash_head_norm* 
                         void* v_pool, int32_t* status, void* cuda_stream);
 
 /* Types of the numbers that dflash_mx4_read writes. */
-#define DFLASH_E5M2 2 /* holds every number of the format within its range (2^-16 .. 57344) */
+#define DFLASH_E5M2 2 /* holds every number of the format from 2^-15 to 57344, and 2^-16 */
 
 /*
  * The numbers of cached tokens: row i of k_out and v_out gets the token at slots[i].
