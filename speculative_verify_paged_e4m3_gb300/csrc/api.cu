@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "dflash_mx4_cache.h"
 #include "e4m3.cuh"
 
 namespace dflash {
@@ -31,6 +32,7 @@ int tc_threads(int rows);
 bool tc_supports(int rows);
 int tc_max_rows();
 int simt_max_rows();
+int round_slots(const dflash_verify_attn_plan_t& plan);
 }  // namespace dflash
 
 using namespace dflash;
@@ -113,6 +115,7 @@ PartialParams partial_params(const dflash_verify_attn_plan_t* plan, const void* 
     p.max_context = pr.max_context;
     p.num_splits = plan->num_splits;
     p.num_slots = plan->num_slots;
+    p.round_slots = 0;
     p.tile_keys = plan->tile_keys;
     p.min_split_keys = plan->min_split_keys;
     p.grid_bar = reinterpret_cast<unsigned long long*>(ws + kGridBarrierOffset);
@@ -132,6 +135,16 @@ PartialParams partial_params(const dflash_verify_attn_plan_t* plan, const void* 
 namespace dflash {
 
 int check_attn_plan(const dflash_verify_attn_plan_t* plan) { return check_plan(plan); }
+
+// Slots of a plan that run at once, if it has more of them than that and than units (else 0).
+int round_slots(const dflash_verify_attn_plan_t& plan) {
+    const dflash_verify_attn_problem& pr = plan.problem;
+    const int round = plan.sm_count / plan.row_blocks;
+    return plan.kernel == DFLASH_KERNEL_MX4 && pr.batch > 1 && pr.num_splits == 0 &&
+                   plan.num_slots > round && plan.num_slots > (int64_t)pr.batch * pr.num_kv_heads
+               ? round
+               : 0;
+}
 
 PartialParams attn_params(const dflash_verify_attn_plan_t* plan, const void* q, const void* k_pool,
                           const void* v_pool, const int32_t* block_table,
@@ -160,6 +173,7 @@ CombineParams combine_params(const dflash_verify_attn_plan_t* plan, const void* 
     c.max_context = pr.max_context;
     c.num_splits = plan->num_splits;
     c.num_slots = plan->num_slots;
+    c.round_slots = 0;
     c.tile_keys = plan->tile_keys;
     c.min_split_keys = plan->min_split_keys;
     c.pdl = (pr.flags & DFLASH_PROBLEM_PDL) && !plan->combine_fused ? 1 : 0;
@@ -286,7 +300,10 @@ int dflash_verify_attn_plan(const dflash_verify_attn_problem* pr,
 int dflash_verify_attn_split_slots(const dflash_verify_attn_plan_t* plan,
                                    const int32_t* context_lens, int32_t* slot_start,
                                    int32_t* keys_per_split, int32_t* active) {
-    int rc = check_plan(plan);
+    if (!plan) return DFLASH_ERR_INVALID_ARGUMENT;
+    dflash_verify_attn_plan_t split = *plan;
+    if (split.kernel == DFLASH_KERNEL_MX4) split.kernel = DFLASH_KERNEL_TCGEN05;  // (the same tiles)
+    int rc = check_plan(&split);
     if (rc != DFLASH_OK) return rc;
     if (!context_lens || !slot_start || !keys_per_split || !active)
         return DFLASH_ERR_INVALID_ARGUMENT;
@@ -311,7 +328,12 @@ int dflash_verify_attn_split_slots(const dflash_verify_attn_plan_t* plan,
     if (W > 0 && B == 1) {
         c[0] = S;
     } else if (W > 0) {
-        const int64_t C = plan->num_slots;
+        int64_t C = plan->num_slots;
+        if (const int round = round_slots(*plan)) {
+            int E = 0;
+            for (int b = 0; b < B; ++b) E += w[b] > 0;
+            C = slots_of_lengths(W, (int)wmax, E, Hkv, (int)C, round);
+        }
         int64_t lo = 1, hi = wmax;  // T = wmax leaves one slot per non-empty unit: Hkv E <= C
         while (lo < hi) {
             const int64_t mid = (lo + hi) / 2;

@@ -28,6 +28,7 @@ struct PartialParams {
     int page_size, max_pages_per_seq, num_pages, max_context;
     int num_splits, tile_keys, min_split_keys;
     int num_slots;  // workspace split slots: Hkv * num_splits for one sequence, else the plan's
+    int round_slots;  // slots that run at once, where a batch may take more (0: it takes num_slots)
     // Row blocks: the grid's x extent is num_splits * row_blocks; CTA x = split * row_blocks + k
     // carries rows [k * block_rows, min(rows, (k + 1) * block_rows)) of that split's slot.
     int row_blocks, block_rows;
@@ -62,7 +63,7 @@ struct CombineParams {
     float* lse;
     int batch, q_len, num_q_heads, num_kv_heads, group, rows;
     int max_context, num_splits, tile_keys, min_split_keys;
-    int num_slots;
+    int num_slots, round_slots;
     int pdl;  // host side: launch as a programmatic dependent of the preceding kernel
 };
 
@@ -184,6 +185,45 @@ __device__ __forceinline__ int physical_page(const int32_t* block_table, int b,
 // contiguous pieces achieves), an empty unit owns no slot. A single sequence keeps num_splits
 // slots per KV head (the same splits: its units are equal). dflash_verify_attn_split_slots does
 // the same integer arithmetic on the host.
+//
+// With as many units as SMs, or more, one slot each would leave a long sequence to a single CTA. A plan of
+// several rounds (round_slots of its slots run at once) has slots to spare for every unit, and how many of them
+// a batch takes goes by its lengths: those of one round (or one a unit), or all, whichever
+// is expected to be done sooner. A slot costs kSlotStart tiles beside its own; the slots of one round take the
+// longest's time, those of several the mean work of an SM and, on average, half the longest's. The longest is
+// not searched for twice: c slots a KV head for E sequences of w tiles in all leave about w / (c - E / 2)
+// tiles a split, half a split a sequence being lost, and the longest sequence c - E + 1 of them at most. Measured
+// for the 4-bit attention, us with one round (or a slot a unit) and with all of the plan's slots, contexts of
+// L / 3 to L tokens, what is chosen in brackets. 24/4 heads, one token a sequence:
+//   units    L = 1024        L = 4096          L = 16384         one of 262144 among units of 1000 tokens
+//     96     [18.5] 23.3     [29.6] 35.2       102.9 [88.7]
+//    128     [18.6] 25.4     [40.7] 43.1       122.9 [105.3]
+//    152     [20.8] 29.3     [44.6] 49.9       [143.0] 136.4     2063 [139]
+//    156     [24.2] 29.2     48.4 [51.4]       [141.9] 144.6     2062 [102]
+//    192     [30.3] 32.8     65.1 [56.8]       206.4 [149.8]
+//    256     [33.8] 44.1     [75.6] 78.8       216.0 [202.7]
+//    384     [51.2] 64.9     [112.2] 116.9     321.8 [317.2]     2108 [190] (400 units, 3 rounds)
+// and of 48 rows: 24/4 heads 96 units L = 4096 [45] 52, 16384 141 [123], 156 units 4096 77 [83], 16384 202
+// [208]; 6/1 heads L = 4096, 80 units [48] 55, 152 [83] 98, 160 108 [102], 256 [161] 179.
+// The choice costs 1 us, slots left idle 2.
+constexpr int kSlotStart = 6;
+__host__ __device__ __forceinline__ int slots_of_lengths(long long w, int longest, int E, int Hkv, int slots,
+                                                         int round) {
+    const int units = E * Hkv, first = units > round ? units : round;
+    if (slots <= first) return slots;
+    auto split = [&](int C) {  // tiles of the longest split
+        const int c = C / Hkv, one = longest / (c - E + 1) + 1;
+        const long long even = 2 * w / (2ll * c - E) + 1, T = even > one ? even : one;
+        return T < longest ? T : longest;
+    };
+    // twice `round` times the tiles' time of n slots, T tiles the longest
+    auto slots_time = [&](int n, long long T) {
+        const long long last = (T + kSlotStart) * round;
+        return n <= round ? 2 * last : 2 * (w * Hkv + (long long)n * kSlotStart) + last;
+    };
+    return slots_time(slots, split(slots)) < slots_time(first, split(first)) ? slots : first;
+}
+
 struct UnitSlots {
     int b, h;    // the unit (b = -1: no unit owns the slot)
     int first;   // its first slot
@@ -228,11 +268,13 @@ __device__ __forceinline__ UnitSlots locate_slots_single(const int32_t* context_
 
 // Slots of a batch of several sequences. Warp-cooperative: every lane of the warp calls it with
 // the same arguments and gets the same result. by_slot: the unit owning slot key; else the slots
-// of unit key.
+// of unit key. kRounds: with round_slots.
+template <bool kRounds>
 __device__ __forceinline__ UnitSlots locate_slots_batch_body(const int32_t* context_lens,
                                                              int B, int Hkv, int num_slots,
-                                                             int max_context, int q_len,
-                                                             int key, bool by_slot, int base) {
+                                                             int round_slots, int max_context,
+                                                             int q_len, int key, bool by_slot,
+                                                             int base) {
     const int lane = threadIdx.x & 31;
     UnitSlots r = {-1, 0, 0, 0, 0, 0};
     int unused = 0;
@@ -260,24 +302,33 @@ __device__ __forceinline__ UnitSlots locate_slots_batch_body(const int32_t* cont
     }
     r.flags = flags;
     if (W == 0) return r;
+    const long long U = (long long)Hkv * E;
+    // slots that splits of T tiles need (counts of tiles stay below 2^24)
+    auto need = [&](int T) {
+        long long sum = 0;
+        for (int b0 = 0; b0 < B; b0 += 32)
+            sum += (unsigned)(tiles(b0 + lane) + T - 1) / (unsigned)T;
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        return sum * Hkv;
+    };
     // T: binary search between W Hkv / C (no split can do better) and the first count that is
     // surely enough, W Hkv / (C - U) (U = Hkv E: each unit's last split may be short), or wmax
-    const long long C = num_slots, U = (long long)Hkv * E;
-    long long lo = (W * Hkv + C - 1) / C;
-    long long hi = wmax;
-    if (C > U) hi = min(hi, (W * Hkv + (C - U) - 1) / (C - U));
-    lo = max(1ll, min(lo, hi));
+    long long C = num_slots;
+    if constexpr (kRounds) {
+        C = slots_of_lengths(W, wmax, E, Hkv, num_slots, round_slots);
+        if (by_slot && key >= C) return r;  // a slot of the rounds that this batch leaves out
+    }
+    int hi = wmax;
+    if (C > U) hi = (int)min((long long)hi, (W * Hkv + (C - U) - 1) / (C - U));
+    int lo = (int)max(1ll, min((W * Hkv + C - 1) / C, (long long)hi));
     while (lo < hi) {
-        const long long mid = (lo + hi) >> 1;
-        long long need = 0;
-        for (int b0 = 0; b0 < B; b0 += 32) need += (tiles(b0 + lane) + mid - 1) / mid;
-        for (int o = 16; o > 0; o >>= 1) need += __shfl_xor_sync(0xffffffffu, need, o);
-        if (need * Hkv <= C)
+        const int mid = (lo + hi) >> 1;
+        if (need(mid) <= C)
             hi = mid;
         else
             lo = mid + 1;
     }
-    const int T = (int)lo;
+    const int T = lo;
     // slots per KV head of each sequence, scanned over the batch
     int c_carry = 0;
     for (int b0 = 0; b0 < B; b0 += 32) {
@@ -312,12 +363,14 @@ __device__ __forceinline__ UnitSlots locate_slots_batch_body(const int32_t* cont
     return r;
 }
 
+template <bool kRounds>
 static __device__ __noinline__ UnitSlots locate_slots_batch(const int32_t* context_lens, int B,
                                                             int Hkv, int num_slots,
-                                                            int max_context, int q_len, int key,
-                                                            bool by_slot, int base) {
-    return locate_slots_batch_body(context_lens, B, Hkv, num_slots, max_context, q_len, key,
-                                   by_slot, base);
+                                                            int round_slots, int max_context,
+                                                            int q_len, int key, bool by_slot,
+                                                            int base) {
+    return locate_slots_batch_body<kRounds>(context_lens, B, Hkv, num_slots, round_slots, max_context,
+                                            q_len, key, by_slot, base);
 }
 
 // The slots of a unit or the unit of a slot (see above). Warp-cooperative. The several-sequence
@@ -325,11 +378,14 @@ static __device__ __noinline__ UnitSlots locate_slots_batch(const int32_t* conte
 __device__ __forceinline__ UnitSlots locate_slots(const int32_t* context_lens, int B, int Hkv,
                                                   int S, int num_slots, int max_context,
                                                   int q_len, int key, bool by_slot,
-                                                  int base = 0) {
+                                                  int base = 0, int round_slots = 0) {
     if (B == 1)
         return locate_slots_single(context_lens, Hkv, S, max_context, q_len, key, by_slot, base);
-    return locate_slots_batch(context_lens, B, Hkv, num_slots, max_context, q_len, key, by_slot,
-                              base);
+    if (round_slots)
+        return locate_slots_batch<true>(context_lens, B, Hkv, num_slots, round_slots, max_context,
+                                        q_len, key, by_slot, base);
+    return locate_slots_batch<false>(context_lens, B, Hkv, num_slots, 0, max_context, q_len, key,
+                                     by_slot, base);
 }
 
 // Grid of a partial launch: (splits x row blocks, Hkv, 1) for a single sequence, (slots x row

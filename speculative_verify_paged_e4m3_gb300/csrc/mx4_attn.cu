@@ -35,6 +35,8 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "dflash_mx4_cache.h"
 #include "mx4.cuh"
@@ -49,6 +51,7 @@ PartialParams attn_params(const dflash_verify_attn_plan_t* plan, const void* q, 
 CombineParams combine_params(const dflash_verify_attn_plan_t* plan, const void* workspace,
                              const int32_t* context_lens, void* out, float* lse);
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream);
+int round_slots(const dflash_verify_attn_plan_t& plan);
 
 namespace mx4 {
 
@@ -363,7 +366,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         p.batch == 1 ? locate_slots_single(p.context_lens, p.num_kv_heads, p.num_splits,
                                            p.max_context, p.q_len, blockIdx.y, false)
                      : locate_slots(p.context_lens, p.batch, p.num_kv_heads, p.num_splits,
-                                    p.num_slots, p.max_context, p.q_len, slot, true);
+                                    p.num_slots, p.max_context, p.q_len, slot, true, 0, p.round_slots);
     if (slot == 0 && tid == 0 && us.flags) atomicOr(p.status, us.flags);
     const int b = us.b, h = us.h, split = slot - us.first, n = us.n;
     const int per = b < 0 ? 1 : keys_per_split(n, us.count, kTile, p.min_split_keys);
@@ -844,7 +847,10 @@ cudaError_t launch_rp(const PartialParams& p, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, mx4_partial_kernel<RP>, p);
 }
 
-constexpr int kTwoRoundsFrom = 8192;  // tokens
+// Plans for contexts up to here have one round of slots: with more units than that has slots cutting them up costs
+// what it gains (16 tiles, common.cuh, slots_of_lengths); with fewer the longest split is 32 tiles, and slots
+// left idle cost 2.4 us (96 units up to 4096 tokens 29.6 and 32.0).
+constexpr int kRoundsFrom = 2048, kRoundsFromOne = 4096;
 
 int rows_pad(int rows) { return (rows + kGroupRows - 1) / kGroupRows * kGroupRows; }
 
@@ -885,15 +891,18 @@ int dflash_mx4_attn_plan(const dflash_verify_attn_problem* problem,
     const int rc = dflash_verify_attn_plan(&pr, plan);
     if (rc != DFLASH_OK) return rc;
     plan->kernel = DFLASH_KERNEL_MX4;
-    // A batch has an SM's worth of slots, shared out by length. With more than half as many units (of whole
-    // slots) that leaves SMs idle behind the longest ones; of long contexts two rounds of slots
-    // cost less. Ragged batches of 24/4 heads, one token each, us with 152 and 304 slots: up to 16384 tokens
-    // 64 units 61 and 65, 80 units 77 and 72, 128 units 124 and 106, 144 units 143 and 115; up to
-    // 4096 tokens 80 units 29 and 34, 128 units 42 and 43.
-    const int64_t units = (int64_t)pr.batch * pr.num_kv_heads * plan->row_blocks;
-    if (pr.batch > 1 && pr.num_splits == 0 && 2 * units > plan->sm_count && units <= plan->sm_count &&
-        pr.max_context >= mx4::kTwoRoundsFrom) {
-        plan->num_slots = 2 * plan->sm_count / plan->row_blocks;
+    // A batch has an SM's worth of slots, shared out by length, or one a unit. With more than half as many units
+    // as a round has slots that leaves little to share, or nothing: it gets rounds with about half a
+    // round to spare or more, of which a call takes what its lengths want (common.cuh, slots_of_lengths). Fewer units
+    // gain nothing: 64 of 24/4 heads, one token each, up to 4096 tokens 24 us with one round and 32 with two,
+    // up to 16384 tokens 67 and 66.
+    const int64_t units = (int64_t)pr.batch * pr.num_kv_heads, round = plan->sm_count / plan->row_blocks;
+    const int64_t cap = units * ((pr.max_context + plan->min_split_keys - 1) / plan->min_split_keys);
+    const int64_t slots = std::min(((units + (round - 1) / 2) / round + 1) * round, cap);
+    if (pr.batch > 1 && pr.num_splits == 0 && slots > plan->num_slots &&
+        pr.max_context > (units > round ? mx4::kRoundsFrom : mx4::kRoundsFromOne)) {
+        if (slots * plan->row_blocks > 0x7FFFFFFF) return DFLASH_ERR_UNSUPPORTED;
+        plan->num_slots = (int32_t)slots;
         const size_t rows = (size_t)plan->num_slots * plan->rows;
         plan->ws_acc_offset = plan->ws_state_offset + (rows * sizeof(float2) + 255) / 256 * 256;
         plan->workspace_bytes = plan->ws_acc_offset + rows * kHeadDim * sizeof(float);
@@ -939,9 +948,10 @@ int dflash_mx4_attn_forward(const dflash_verify_attn_plan_t* plan, const void* q
             if (outs[i] == outs[j]) return DFLASH_ERR_INVALID_ARGUMENT;
     }
     if (workspace_bytes < plan->workspace_bytes) return DFLASH_ERR_WORKSPACE_TOO_SMALL;
-    const PartialParams p = attn_params(&split, q, k_pool, v_pool, block_table, context_lens,
-                                        nullptr, nullptr, workspace);
+    PartialParams p = attn_params(&split, q, k_pool, v_pool, block_table, context_lens, nullptr, nullptr,
+                                  workspace);
     CombineParams c = combine_params(&split, workspace, context_lens, out, lse);
+    p.round_slots = c.round_slots = round_slots(*plan);
     c.pdl = 1;  // it waits for the partial kernel where it reads the split state
     cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
     if (mx4::launch_partial(p, stream) != cudaSuccess || launch_combine(c, stream) != cudaSuccess) {
