@@ -250,7 +250,7 @@ struct Ctx {
     }
 };
 
-// Wait (bounded, whatever became of the other warps) for a copy in flight.
+// Wait (bounded, whatever became of the other warps) for a copy, or products, in flight.
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
     const uint64_t t0 = globaltimer_ns();
     while (!mbar_try_wait(smem_u32(bar), parity) && globaltimer_ns() - t0 < kWaitLimitNs) {
@@ -784,6 +784,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (alive) ctx.wait_warp(&sm.done, 0);
     }
+    // products of a pair that gave up, and their arrivals here, may still be on their way
+    if (warp == kQkWarp) drain(&sm.done, 0);
     tc_fence_before();
     __syncthreads();
     cluster_arrive();

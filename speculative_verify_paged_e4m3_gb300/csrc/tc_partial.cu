@@ -137,6 +137,7 @@ struct Small {
     uint64_t odone, qready;
     uint32_t tmem_base;
     int abort;
+    int never;     // stays 0: for a wait that goes on when the CTA gives up
     float vscale;  // v_scale, loaded while Q is staged (read after the last PV)
     alignas(16) float c0[kMaxRP];  // score scale of each row (log2 units per MMA unit), as float4
     float rmax[kMaxRP / kGroupRows][4][kGroupRows];  // per-group, per-warp row maxima of a tile
@@ -454,7 +455,7 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
         mbar_init(smem_u32(&sm.vtail), 1);
         mbar_init(smem_u32(&sm.odone), 1);
         mbar_init(smem_u32(&sm.qready), C::kSoftWarps);
-        sm.abort = 0;
+        sm.abort = sm.never = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -618,13 +619,13 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
             if (clamped) atomicOr(p.status, DFLASH_FLAG_PAGE_CLAMPED);
             // no copy of this warp may still be writing shared memory when the CTA retires
             for (int t = tk - kKStages < 0 ? 0 : tk - kKStages; t < tk; ++t)
-                mbar_wait(smem_u32(&sm.kfull[t % kKStages]), (t / kKStages) & 1, &sm.abort,
+                mbar_wait(smem_u32(&sm.kfull[t % kKStages]), (t / kKStages) & 1, &sm.never,
                           kWaitLimitNs);
             for (int u = tv - kVStages < 0 ? 0 : tv - kVStages; u < tv; ++u) {
                 if (end - (start + u * kVKeys) < kVKeys) {
-                    if (tail_pending) mbar_wait(smem_u32(&sm.vtail), 0, &sm.abort, kWaitLimitNs);
+                    if (tail_pending) mbar_wait(smem_u32(&sm.vtail), 0, &sm.never, kWaitLimitNs);
                 } else {
-                    mbar_wait(smem_u32(&sm.vfull[u % kVStages]), (u / kVStages) & 1, &sm.abort,
+                    mbar_wait(smem_u32(&sm.vfull[u % kVStages]), (u / kVStages) & 1, &sm.never,
                               kWaitLimitNs);
                 }
             }
@@ -716,7 +717,12 @@ __global__ void __launch_bounds__(Cfg<RP>::kThreads, 1)
                 }
             }
         }
-        if (lane == 0) mma_commit(smem_u32(&sm.odone));  // tracks every MMA issued above
+        if (lane == 0) {
+            mma_commit(smem_u32(&sm.odone));  // tracks every MMA issued above
+            // (no other wait sees the products of a CTA that gave up through before it frees tensor memory)
+            mbar_wait(smem_u32(&sm.odone), 0, &sm.never, kWaitLimitNs);
+        }
+        __syncwarp();
     } else if (warp >= 4) {
         // ------------------------------------------------------------- softmax (RP/16 groups)
         const int sw = warp - 4;          // 0 .. kSoftWarps - 1

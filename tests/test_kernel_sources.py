@@ -1,12 +1,12 @@
-"""What the 4-bit attention's kernel must do and no call can show: read from its source."""
+"""What the tensor-core kernels must do and no call can show: read from their sources."""
 import os
 import re
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
-def source():
-    path = os.path.join(ROOT, "speculative_verify_paged_e4m3_gb300", "csrc", "mx4_attn.cu")
+def source(name="mx4_attn.cu"):
+    path = os.path.join(ROOT, "speculative_verify_paged_e4m3_gb300", "csrc", name)
     with open(path) as f:
         return re.sub(r"//[^\n]*", "", f.read())
 
@@ -42,3 +42,17 @@ def test_lanes_are_together_where_instructions_want_a_whole_warp():
         b = body(s, head)
         assert b.index("__syncwarp()") < b.index("asm volatile")
     assert re.search(r"__syncwarp\(\);\s*tc_fence_after\(\);\s*tmem_dealloc\(", s)
+
+
+def test_the_e4m3_kernels_see_copies_and_products_through():
+    s = source("tc_partial.cu")
+    assert re.search(r"mma_commit\(smem_u32\(&sm\.odone\)\);\s*"
+                     r"mbar_wait\(smem_u32\(&sm\.odone\), 0, &sm\.never, kWaitLimitNs\);", s)
+    assert s.count("mma_commit(smem_u32(&sm.odone))") == 1
+    drains = re.findall(r"mbar_wait\(smem_u32\(&sm\.(\w+)(?:\[[^]]*\])?\),[^;]*?&sm\.(\w+),", s)
+    assert sorted(drains) == [("kfull", "never"), ("odone", "never"), ("vfull", "never"), ("vtail", "never")]
+    assert not re.search(r"never\s*=\s*[^0;]", s.replace("sm.abort = sm.never = 0", ""))
+    s = source("prefix_pairs.cu")
+    end = s[s.index("ctx.wait_warp(&sm.done, 0)"):s.index("tcgen05.dealloc")]
+    assert end.index("drain(&sm.done, 0)") < end.index("__syncthreads()") < end.index("cluster_wait()")
+    assert s.count("commit_pair(smem_u32(&sm.done));") == 2 and "mbar_init(smem_u32(&sm.done), 2)" in s
