@@ -217,7 +217,8 @@ int dflash_rope_kv_write_live(const dflash_rope_plan_t* plan, int64_t num_tokens
  * Each head x of Q (and of K) is first normed over its head_dim elements,
  *   x_i * (weight_offset + w_i) / sqrt(mean of x^2 + eps),
  * then rotated as above; V is not normed. Sum and division are FP32, nothing is rounded between norm and
- * rotation. (The squares' sum must stay below 2^128: bf16 elements below 2^60.)
+ * rotation. (The squares' sum must stay below 2^128: bf16 elements below 2^60. With an eps below 2^-126 their
+ * mean must be above that: of bf16 elements that are all below 2^-63 the squares are lost.)
  */
 typedef struct {
     const void* q_weight; /* device, head_dim elements of the plan's dtype, 16-byte aligned; NULL: Q

@@ -16,7 +16,9 @@
 //    exponent (cut to +-40) the kernel takes p = 2^(s + ev - m), m the reference of s + ev, sums p 2^-ev
 //    for the denominator and multiplies p by v 2^-ev. A weight is so large only if its value is.
 //  * Probabilities are p 2^8 of a row's first maximum and move their reference past 2^15: below 2^-14
-//    FP16 has a fixed step, 2^-24, 2^-32 of the largest at least.
+//    FP16 has a fixed step, 2^-24, 2^-32 of the largest at least. Their rounding to FP16 (2^-11, as the output's)
+//    takes the error against 64 bits from 2.1e-4 to 2.9e-4 of the output; a second term of P would double
+//    the output's products. The denominator sums them unrounded.
 //  * NaN. A key with a NaN scale in K or V gets a NaN factor or exponent: its probability is NaN in
 //    every row that sees it and 0, selected, in the others. V's own factors are finite.
 //  * Warps: 0 copies the codes (four tiles ahead), 1 and 2 issue the products of the scores and of the
@@ -26,8 +28,8 @@
 //    DFLASH_FLAG_KERNEL_TIMEOUT, sees its copies and products through (bounded too) and returns.
 //
 // Measured with the combine, in a graph: 24/4 heads, 8 drafted tokens over 261888 tokens 84 us, 50 % of the copy
-// rate; 32 sequences of one token up to 16384 long, 24/4 heads, 105 us, 56 %; one rank, 8 tokens over 261888
-// tokens 30.6 us. What bounds it is the warps: 7750 warp instructions a tile for 48 rows in 3150 clocks, 5380
+// rate; 32 sequences of one token up to 16384 long, 24/4 heads, 106 us, 56 %; one rank, 8 tokens over 261888
+// tokens 30.4 us. What bounds it is the warps: 7750 warp instructions a tile for 48 rows in 3150 clocks, 5380
 // for 16 in 2450, 68 and 60 % of the issue slots, with no role ahead of the others by more than a
 // few hundred clocks. They share the instruction caches, so that fewer instructions in a loop count
 // for more than their number, and unrolling costs: hence the rolled loops (two chunks of V at a time 104 us
