@@ -77,7 +77,8 @@ int dflash_mx4_read(int32_t num_kv_heads, int32_t head_dim, int32_t page_size, i
 /*
  * Attention over the 4-bit pools: dflash_verify_attn_plan and _forward with these pools and without
  * scales (the numbers carry their own). problem.kernel is DFLASH_KERNEL_AUTO; of the flags
- * DFLASH_PROBLEM_PDL is taken, DFLASH_PROBLEM_FUSED_COMBINE is not (DFLASH_ERR_UNSUPPORTED).
+ * DFLASH_PROBLEM_PDL is taken, DFLASH_PROBLEM_FUSED_COMBINE is not (DFLASH_ERR_UNSUPPORTED). Sequences times
+ * KV heads are at most 65535.
  * Buffers, alignments and workspace as for dflash_verify_attn_forward. A batch of more units (sequences times
  * KV heads) than half the SMs gets several SMs' worths of slots, and a call shares out one of them (or a slot a
  * unit) or all, by its lengths; dflash_verify_attn_split_slots says what, for these plans too.

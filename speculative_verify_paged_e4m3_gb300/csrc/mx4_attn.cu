@@ -899,6 +899,7 @@ int dflash_mx4_attn_plan(const dflash_verify_attn_problem* problem,
     // gain nothing: 64 of 24/4 heads, one token each, up to 4096 tokens 24 us with one round and 32 with two,
     // up to 16384 tokens 67 and 66.
     const int64_t units = (int64_t)pr.batch * pr.num_kv_heads, round = plan->sm_count / plan->row_blocks;
+    if (units > 65535) return DFLASH_ERR_UNSUPPORTED;  // the combine's grid: found out here, not behind the products
     const int64_t cap = units * ((pr.max_context + plan->min_split_keys - 1) / plan->min_split_keys);
     const int64_t slots = std::min(((units + (round - 1) / 2) / round + 1) * round, cap);
     if (pr.batch > 1 && pr.num_splits == 0 && slots > plan->num_slots &&

@@ -72,6 +72,14 @@ def test_slots_of_plans(B):
     assert p.ws_acc_offset >= p.ws_state_offset + p.num_slots * p.rows * 8
 
 
+def test_more_units_than_a_grid_takes_are_refused_by_the_plan(B):
+    assert plan(B, 16383, (24, 4), 1, 4096).num_slots >= 65532
+    for batch, heads in ((16384, (24, 4)), (1, (65536, 65536))):
+        with pytest.raises(B.DflashError) as e:
+            plan(B, batch, heads, 1, 4096)
+        assert e.value.status == B.DFLASH_ERR_UNSUPPORTED
+
+
 def test_empty_and_single_sequences(B):
     p = plan(B, 64, (24, 4), 1, 32768)
     start, per, act = B.dflash_verify_attn_split_slots(p, [0] * 64)
