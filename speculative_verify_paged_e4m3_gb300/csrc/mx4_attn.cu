@@ -29,8 +29,8 @@
 //
 // Measured with the combine, in a graph: 24/4 heads, 8 drafted tokens over 261888 tokens 84 us, 50 % of the copy
 // rate; 32 sequences of one token up to 16384 long, 24/4 heads, 106 us, 56 %; one rank, 8 tokens over 261888
-// tokens 30.4 us. What bounds it is the warps: 7750 warp instructions a tile for 48 rows in 3150 clocks, 5380
-// for 16 in 2450, 68 and 60 % of the issue slots, with no role ahead of the others by more than a
+// tokens 30.4 us. What bounds it is the warps: 7810 warp instructions a tile for 48 rows in 3150 clocks, 5430
+// for 16 in 2450, 68 and 61 % of the issue slots, with no role ahead of the others by more than a
 // few hundred clocks. They share the instruction caches, so that fewer instructions in a loop count
 // for more than their number, and unrolling costs: hence the rolled loops (two chunks of V at a time 104 us
 // for 99, two blocks of K 135 for 130 us of the single tokens).
