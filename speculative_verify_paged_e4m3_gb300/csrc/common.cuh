@@ -190,7 +190,7 @@ __device__ __forceinline__ int physical_page(const int32_t* block_table, int b,
 // several rounds (round_slots of its slots run at once) has slots to spare for every unit, and how many of them
 // a batch takes goes by its lengths: those of one round (or one a unit), or all, whichever
 // is expected to be done sooner. A slot costs kSlotStart tiles beside its own; the slots of one round take the
-// longest's time, those of several the mean work of an SM and, on average, half the longest's. The longest is
+// longest's time, those of several the mean work of an SM and 0.4 (a slot a unit) or 0.3 (all slots) of the longest's. The longest is
 // not searched for twice: c slots a KV head for E sequences of w tiles in all leave about w / (c - E / 2)
 // tiles a split, half a split a sequence being lost, and the longest sequence c - E + 1 of them at most. Measured
 // for the 4-bit attention, us with one round (or a slot a unit) and with all of the plan's slots, contexts of
@@ -198,15 +198,15 @@ __device__ __forceinline__ int physical_page(const int32_t* block_table, int b,
 //   units    L = 1024        L = 4096          L = 16384         one of 262144 among units of 1000 tokens
 //     96     [18.5] 23.3     [29.6] 35.2       102.9 [88.7]
 //    128     [18.6] 25.4     [40.7] 43.1       122.9 [105.3]
-//    152     [20.8] 29.3     [44.6] 49.9       [143.0] 136.4     2063 [139]
-//    156     [24.2] 29.2     48.4 [51.4]       [141.9] 144.6     2062 [102]
+//    152     [20.8] 29.3     [44.6] 49.9       143.0 [136.4]     2063 [139]
+//    156     [24.2] 29.2     48.4 [51.4]       141.9 [144.6]     2062 [102]
 //    192     [30.3] 32.8     65.1 [56.8]       206.4 [149.8]
 //    256     [33.8] 44.1     [75.6] 78.8       216.0 [202.7]
-//    384     [51.2] 64.9     [112.2] 116.9     321.8 [317.2]     2108 [190] (400 units, 3 rounds)
+//    384     [51.2] 64.9     [112.2] 116.9     321.8 [317.2]     2108 [150] (400 units)
 // and of 48 rows: 24/4 heads 96 units L = 4096 [45] 52, 16384 141 [123], 156 units 4096 77 [83], 16384 202
 // [208]; 6/1 heads L = 4096, 80 units [48] 55, 152 [83] 98, 160 108 [102], 256 [161] 179.
 // The choice costs 1 us, slots left idle 2.
-constexpr int kSlotStart = 6;
+constexpr int kSlotStart = 8;
 __host__ __device__ __forceinline__ int slots_of_lengths(long long w, int longest, int E, int Hkv, int slots,
                                                          int round) {
     const int units = E * Hkv, first = units > round ? units : round;
@@ -216,12 +216,12 @@ __host__ __device__ __forceinline__ int slots_of_lengths(long long w, int longes
         const long long even = 2 * w / (2ll * c - E) + 1, T = even > one ? even : one;
         return T < longest ? T : longest;
     };
-    // twice `round` times the tiles' time of n slots, T tiles the longest
-    auto slots_time = [&](int n, long long T) {
+    // ten times `round` times the tiles' time of n slots, T tiles the longest
+    auto slots_time = [&](int n, long long T, int tenths) {
         const long long last = (T + kSlotStart) * round;
-        return n <= round ? 2 * last : 2 * (w * Hkv + (long long)n * kSlotStart) + last;
+        return n <= round ? 10 * last : 10 * (w * Hkv + (long long)n * kSlotStart) + tenths * last;
     };
-    return slots_time(slots, split(slots)) < slots_time(first, split(first)) ? slots : first;
+    return slots_time(slots, split(slots), 3) < slots_time(first, split(first), 4) ? slots : first;
 }
 
 struct UnitSlots {
